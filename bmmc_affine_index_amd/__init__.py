@@ -624,3 +624,9 @@ def flip(t, dims: Sequence[int], stream=None, tune: bool = False):
 def transpose2d(t, stream=None, tune: bool = False):
     """The transpose of a 2^a x 2^b matrix (a rotation of the index bits)."""
     return permute_dims(t, [1, 0], stream=stream, tune=tune)
+
+
+# Rows of tokens moved to where the data says (include/bmmc_tokens.h).
+from .tokens import (ExpertOrder, cache_append, expert_combine, expert_combine_backward,  # noqa: E402
+                     expert_gather, expert_gather_backward, expert_order, rotary, rotary_axes,
+                     rotary_backward)

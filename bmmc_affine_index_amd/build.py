@@ -30,7 +30,9 @@ HIP_FLAGS = ["--offload-arch=" + ARCH, "-Xclang", "-target-feature", "-Xclang",
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.hip")) +
-                  glob.glob(os.path.join(CSRC, "kernels", "*.hip")))
+                  glob.glob(os.path.join(CSRC, "kernels", "*.hip")) +
+                  glob.glob(os.path.join(CSRC, "tokens", "*.cpp")) +
+                  glob.glob(os.path.join(CSRC, "tokens", "*.hip")))
 
 
 def _compile(src: str) -> str:

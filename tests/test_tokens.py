@@ -1,0 +1,448 @@
+"""CPU tests of the calls on token rows: exports, argument checks of the C
+entry points and of the Python calls, and the host side of the kernels'
+indexing.  No GPU call is made: accepted arguments are only tried on a build
+whose launchers are stand-ins."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import bmmc_affine_index_amd as bm  # noqa: E402
+from bmmc_affine_index_amd import tokens as tk  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+TESTS = os.path.join(ROOT, "tests")
+CSRC = os.path.join(ROOT, "bmmc_affine_index_amd", "csrc")
+HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+INCLUDE = ["-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I" + os.path.join(ROOT, "include")]
+SANITIZE = ["-fsanitize=address,undefined", "-fno-sanitize-recover=undefined"]
+ACCEPTED = bm.ERR_HIP  # what the stand-in launchers return
+
+
+def test_library_exports_every_header_function():
+    header = open(os.path.join(ROOT, "include", "bmmc_tokens.h")).read()
+    names = set(re.findall(r"^\S[^;()]*?\b(bmmc_\w+)\s*\(", header, flags=re.M))
+    assert names == set(tk.TOKENS_EXPORTED)
+    L = tk.tokens_lib()
+    for name in names:
+        assert hasattr(L, name), name
+
+
+def test_struct_layouts_match_header(tmp_path):
+    structs = {c.__name__: c for c in (tk.bmmc_heads, tk.bmmc_rotation, tk.bmmc_paged_cache)}
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "bmmc_tokens.h"',
+             "int main(void) {"]
+    for name, cls in structs.items():
+        lines.append('printf("%s %%zu\\n", sizeof(%s));' % (name, name))
+        for field, _ in cls._fields_:
+            lines.append('printf("%s.%s %%zu\\n", offsetof(%s, %s));' % (name, field, name, field))
+    src = tmp_path / "layout.c"
+    src.write_text("\n".join(lines + ["return 0; }"]))
+    exe = tmp_path / "layout"
+    subprocess.check_call(["gcc", "-I" + os.path.join(ROOT, "include"), str(src), "-o", str(exe)])
+    out = dict(l.split() for l in subprocess.check_output([str(exe)]).decode().splitlines())
+    for name, cls in structs.items():
+        assert int(out[name]) == ctypes.sizeof(cls), name
+        for field, _ in cls._fields_:
+            assert int(out[name + "." + field]) == getattr(cls, field).offset, (name, field)
+
+
+@pytest.mark.skipif(shutil.which("g++") is None or bool(os.environ.get("LD_PRELOAD")),
+                    reason="needs g++, and no library preloaded before the sanitizer's")
+def test_host_side_of_the_indexing(tmp_path):
+    exe = str(tmp_path / "host")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-g", *SANITIZE, *INCLUDE,
+                    os.path.join(TESTS, "tokens_host.cpp"), "-L/opt/rocm/lib", "-lamdhip64",
+                    "-Wl,-rpath,/opt/rocm/lib", "-o", exe], check=True, timeout=300)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0"))
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout + r.stderr
+
+
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="needs hipcc")
+@pytest.mark.parametrize("src", ["order.hip", "experts.hip", "rotary.hip"])
+def test_every_kernel_has_a_body(src, tmp_path):
+    """Undefined behaviour can leave a kernel without instructions, which a
+    wave would run past; every kernel ends in s_endpgm and none spills vector
+    registers."""
+    out = tmp_path / (src + ".s")
+    subprocess.run([HIPCC, "-O3", "-std=c++17", "-I" + os.path.join(ROOT, "include"),
+                    "--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang",
+                    "-packed-fp32-ops", "--cuda-device-only", "-S", "-o", str(out),
+                    os.path.join(CSRC, "tokens", src)],
+                   check=True, capture_output=True, timeout=600)
+    s = out.read_text()
+    kernels = re.findall(r"^\s*\.amdhsa_kernel\s+(\S+)", s, flags=re.M)
+    assert kernels
+    for name in kernels:
+        start = s.index("\n%s:" % name)
+        ins = [l.strip() for l in s[start:s.index(".Lfunc_end", start)].splitlines()[1:]]
+        assert any(l.startswith("s_endpgm") for l in ins), name
+    assert set(re.findall(r"\.vgpr_spill_count:\s*(\d+)", s)) == {"0"}
+
+
+# --------------------------------------------------------------------------
+# The C entry points' checks, on a build whose launchers are stand-ins
+# --------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    if shutil.which("g++") is None or not os.path.exists("/opt/rocm/lib"):
+        pytest.skip("needs g++ and the ROCm runtime library")
+    so = str(tmp_path_factory.mktemp("host") / "libtokens_host.so")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-fsanitize=undefined",
+                    "-fno-sanitize-recover=undefined", *INCLUDE,
+                    os.path.join(CSRC, "tokens", "api.cpp"), os.path.join(TESTS, "token_stubs.cpp"),
+                    "-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib", "-o", so],
+                   check=True, timeout=300)
+    L = ctypes.CDLL(so)
+    real = tk.tokens_lib()
+    for name in tk.TOKENS_EXPORTED:
+        getattr(L, name).argtypes = getattr(real, name).argtypes
+        getattr(L, name).restype = getattr(real, name).restype
+    return L
+
+
+A, B, C, D, E, G = (0x10000000 * k for k in range(1, 7))  # addresses nothing is read from
+
+
+def _with(base, changes):
+    args = dict(base)
+    args.update(changes)
+    return list(args.values())
+
+
+@pytest.mark.parametrize("n,e,align,rows", [(0, 1, 1, 0), (10, 4, 1, 10), (10, 4, 16, 70),
+                                            (3, 64, 16, 48), (1 << 20, 2048, 128, (1 << 20) + 2048 * 127),
+                                            (-1, 4, 1, -1), (1 << 31, 4, 1, -1), (4, 0, 1, -1),
+                                            (4, 2049, 1, -1), (4, 4, 0, -1), (4, 4, 1 << 31, -1),
+                                            (4, 4, (1 << 31) - 1, -1)])
+def test_rows_of_an_order(n, e, align, rows):
+    assert tk.tokens_lib().bmmc_expert_rows(n, e, align) == rows
+
+
+ORDER = dict(experts=A, kind=tk.I64, n=100000, e=8, align=1, offsets=B, counts=C, rows=D, slots=E,
+             work=G, bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("changes,status", [
+    ({}, ACCEPTED), ({"n": 0, "experts": None, "rows": None, "slots": None}, ACCEPTED),
+    ({"n": 4096, "work": None, "bytes": 0}, ACCEPTED),
+    ({"n": -1}, bm.ERR_INVALID_ARG), ({"n": 1 << 31}, bm.ERR_INVALID_ARG),
+    ({"e": 0}, bm.ERR_INVALID_ARG), ({"e": 2049}, bm.ERR_INVALID_ARG),
+    ({"align": 0}, bm.ERR_INVALID_ARG), ({"align": 1 << 30}, bm.ERR_INVALID_ARG),
+    ({"kind": 2}, bm.ERR_INVALID_ARG), ({"experts": None}, bm.ERR_INVALID_ARG),
+    ({"experts": A + 4}, bm.ERR_INVALID_ARG), ({"kind": tk.I32, "experts": A + 4}, ACCEPTED),
+    ({"offsets": None}, bm.ERR_INVALID_ARG), ({"counts": C + 1}, bm.ERR_INVALID_ARG),
+    ({"rows": None}, bm.ERR_INVALID_ARG), ({"slots": None}, bm.ERR_INVALID_ARG),
+    ({"work": None}, bm.ERR_INVALID_ARG), ({"bytes": 8}, bm.ERR_INVALID_ARG)])
+def test_order_refusals(host, changes, status):
+    assert host.bmmc_expert_order(*_with(ORDER, changes)) == status
+
+
+GATHER = dict(x=A, x_stride=100, rows=B, slots=C, tokens=10, choices=4, capacity=40, dim=100,
+              kind=tk.BF16, out=D, out_stride=100, stream=None)
+
+
+@pytest.mark.parametrize("changes,status", [
+    ({}, ACCEPTED), ({"x": A + 2}, ACCEPTED), ({"x_stride": 0}, ACCEPTED),
+    ({"tokens": 0, "capacity": 0}, bm.OK), ({"tokens": 0, "x": None, "rows": None}, ACCEPTED),
+    ({"capacity": 0}, bm.ERR_INVALID_ARG), ({"tokens": -1}, bm.ERR_INVALID_ARG),
+    ({"tokens": 1 << 30}, bm.ERR_INVALID_ARG), ({"choices": 0}, bm.ERR_INVALID_ARG),
+    ({"choices": 1025}, bm.ERR_INVALID_ARG), ({"dim": 0}, bm.ERR_INVALID_ARG),
+    ({"dim": 1 << 31}, bm.ERR_INVALID_ARG), ({"kind": tk.E4M3}, bm.ERR_INVALID_ARG),
+    ({"kind": -1}, bm.ERR_INVALID_ARG), ({"x": None}, bm.ERR_INVALID_ARG),
+    ({"x": A + 1}, bm.ERR_INVALID_ARG), ({"kind": tk.F32, "out": D + 2}, bm.ERR_INVALID_ARG),
+    ({"rows": None}, bm.ERR_INVALID_ARG), ({"slots": None}, bm.ERR_INVALID_ARG),
+    ({"x_stride": -100}, bm.ERR_INVALID_ARG), ({"out_stride": 99}, bm.ERR_INVALID_ARG),
+    ({"x_stride": 1 << 50}, bm.ERR_INVALID_ARG), ({"out": A}, bm.ERR_ALIAS),
+    ({"out": A + 10 * 200 - 2}, bm.ERR_ALIAS), ({"out": A + 10 * 200}, ACCEPTED),
+    ({"x": D + 40 * 200 - 2}, bm.ERR_ALIAS), ({"x": D + 40 * 200}, ACCEPTED)])
+def test_gather_refusals(host, changes, status):
+    assert host.bmmc_expert_gather(*_with(GATHER, changes)) == status
+
+
+COMBINE = dict(x=A, x_stride=100, rows=B, weights=C, wkind=tk.F32, tokens=10, choices=4,
+               capacity=40, dim=100, kind=tk.F16, out=D, out_stride=100, stream=None)
+
+
+@pytest.mark.parametrize("changes,status", [
+    ({}, ACCEPTED), ({"weights": None}, ACCEPTED), ({"wkind": tk.F16}, ACCEPTED),
+    ({"tokens": 0}, bm.OK), ({"capacity": 0}, bm.ERR_INVALID_ARG),
+    ({"wkind": tk.BF16}, bm.ERR_INVALID_ARG), ({"weights": C + 2}, bm.ERR_INVALID_ARG),
+    ({"x": None}, bm.ERR_INVALID_ARG), ({"out": None}, bm.ERR_INVALID_ARG),
+    ({"rows": B + 2}, bm.ERR_INVALID_ARG), ({"out_stride": 0}, bm.ERR_INVALID_ARG),
+    ({"tokens": 1, "out_stride": 0}, ACCEPTED), ({"out": A}, bm.ERR_ALIAS)])
+def test_combine_refusals(host, changes, status):
+    assert host.bmmc_expert_combine(*_with(COMBINE, changes)) == status
+
+
+BACKWARD = dict(grad=A, grad_stride=100, x=B, x_stride=100, rows=C, slots=D, weights=E,
+                wkind=tk.F32, tokens=10, choices=4, capacity=40, dim=100, kind=tk.BF16,
+                grad_in=G, grad_in_stride=100, grad_weights=G + (1 << 20), stream=None)
+
+
+@pytest.mark.parametrize("changes,status", [
+    ({}, ACCEPTED), ({"tokens": 0, "capacity": 0}, bm.OK), ({"capacity": 0}, bm.ERR_INVALID_ARG),
+    ({"weights": None}, bm.ERR_INVALID_ARG), ({"grad_weights": None}, bm.ERR_INVALID_ARG),
+    ({"grad": None}, bm.ERR_INVALID_ARG), ({"x": None}, bm.ERR_INVALID_ARG),
+    ({"slots": None}, bm.ERR_INVALID_ARG), ({"grad_in": A}, bm.ERR_ALIAS),
+    ({"grad_in": B}, bm.ERR_ALIAS), ({"grad_in_stride": 50}, bm.ERR_INVALID_ARG),
+    ({"wkind": tk.F16}, bm.ERR_INVALID_ARG), ({"dim": 0}, bm.ERR_INVALID_ARG)])
+def test_combine_backward_refusals(host, changes, status):
+    assert host.bmmc_expert_combine_backward(*_with(BACKWARD, changes)) == status
+
+
+def _heads(**changes):
+    h = dict(x=A, out=B, heads=8, in_batch=0, in_token=1024, in_head=128, out_batch=0,
+             out_token=1024, out_head=128)
+    h.update(changes)
+    return tk.bmmc_heads(*h.values())
+
+
+def _turn(**changes):
+    r = dict(positions=C, freqs=D, axis_of_pair=None, axis_stride=0, position_type=tk.I64,
+             freqs_are_64=1, axes=1, pairs=64, interleaved=0, inverse=0, scale=1.0)
+    r.update(changes)
+    return tk.bmmc_rotation(*r.values())
+
+
+@pytest.mark.parametrize("heads,turn,args,status", [
+    ({}, {}, {}, ACCEPTED),
+    ({"out": A}, {}, {}, ACCEPTED),                                   # in place
+    ({"out": A, "out_token": 2048}, {}, {}, bm.ERR_ALIAS),            # in place, other strides
+    ({"out": A + 256}, {}, {}, bm.ERR_ALIAS),
+    ({"out_head": 64}, {}, {}, bm.ERR_ALIAS),                         # heads of the result overlap
+    ({"out_token": 0}, {}, {}, bm.ERR_ALIAS),
+    ({"in_head": 0}, {}, {}, ACCEPTED),                               # one head read for all
+    ({"out_head": 1280, "out_token": 128}, {}, {}, ACCEPTED),         # heads before tokens
+    ({"heads": 0}, {}, {}, bm.ERR_INVALID_ARG), ({"x": None}, {}, {}, bm.ERR_INVALID_ARG),
+    ({"out": None}, {}, {}, bm.ERR_INVALID_ARG), ({"x": A + 1}, {}, {}, bm.ERR_INVALID_ARG),
+    ({"in_token": -1}, {}, {}, bm.ERR_INVALID_ARG),
+    ({}, {"pairs": 0}, {}, bm.ERR_INVALID_ARG), ({}, {"pairs": 65}, {}, bm.ERR_INVALID_ARG),
+    ({}, {"axes": 0}, {}, bm.ERR_INVALID_ARG), ({}, {"axes": 9}, {}, bm.ERR_INVALID_ARG),
+    ({}, {"positions": None}, {}, bm.ERR_INVALID_ARG), ({}, {"freqs": None}, {}, bm.ERR_INVALID_ARG),
+    ({}, {"freqs": D + 4}, {}, bm.ERR_INVALID_ARG),
+    ({}, {"freqs": D + 4, "freqs_are_64": 0}, {}, ACCEPTED),
+    ({}, {"positions": C + 4}, {}, bm.ERR_INVALID_ARG),
+    ({}, {"position_type": 3}, {}, bm.ERR_INVALID_ARG),
+    ({}, {"axis_of_pair": E + 2}, {}, bm.ERR_INVALID_ARG),
+    ({}, {}, {"tokens": 0}, bm.OK), ({}, {}, {"batch": 0}, bm.OK),
+    ({}, {}, {"tokens": -1}, bm.ERR_INVALID_ARG),
+    ({}, {}, {"batch": 1 << 16, "tokens": 1 << 16}, bm.ERR_INVALID_ARG),
+    ({}, {}, {"dim": 513}, bm.ERR_INVALID_ARG), ({}, {}, {"dim": 0}, bm.ERR_INVALID_ARG),
+    ({}, {}, {"kind": tk.E4M3}, bm.ERR_INVALID_ARG), ({}, {}, {"count": 3}, bm.ERR_INVALID_ARG),
+    ({}, {}, {"count": 0}, bm.ERR_INVALID_ARG)])
+def test_rotary_refusals(host, heads, turn, args, status):
+    a = dict(count=1, batch=1, tokens=10, dim=128, kind=tk.BF16)
+    a.update(args)
+    h = (tk.bmmc_heads * 2)(_heads(**heads), _heads(x=E, out=G))
+    r = _turn(**turn)
+    assert host.bmmc_rotary(h, a["count"], a["batch"], a["tokens"], a["dim"], a["kind"],
+                            ctypes.byref(r), None) == status
+
+
+def test_rotary_of_two(host):
+    """Views of one projection, in place, lie between one another; a result of
+    its own must not lie in the other tensor."""
+    wide = dict(in_token=2048, out_token=2048)
+
+    def status(q, k):
+        h = (tk.bmmc_heads * 2)(q, k)
+        return host.bmmc_rotary(h, 2, 1, 10, 128, tk.BF16, ctypes.byref(_turn()), None)
+    assert status(_heads(out=A, **wide), _heads(x=A + 2048, out=A + 2048, **wide)) == ACCEPTED
+    assert status(_heads(out=A, **wide), _heads(x=A + 2048, out=A, **wide)) == bm.ERR_ALIAS
+    assert status(_heads(out=B, **wide), _heads(x=B + 2048, out=C, **wide)) == bm.ERR_ALIAS
+    assert status(_heads(out=B), _heads(x=E, out=G)) == ACCEPTED
+
+
+def _cache(**changes):
+    c = dict(data=E, scale=None, page_stride=16 * 1024, place_stride=1024, head_stride=128,
+             scale_stride=0, kind=tk.BF16)
+    c.update(changes)
+    return tk.bmmc_paged_cache(*c.values())
+
+
+APPEND = dict(pages=64, page_size=16, table=B, batch=4, width=16, stride=16, sequences=C,
+              positions=D, pkind=tk.I64)
+E4 = dict(kind=tk.E4M3, scale=A + (1 << 24))
+
+
+@pytest.mark.parametrize("case,status", [
+    ({}, ACCEPTED), ({"q": {}}, ACCEPTED), ({"turn": None}, ACCEPTED),
+    ({"q": {"out": A + (1 << 26)}}, ACCEPTED),
+    ({"tokens": 0}, bm.OK), ({"args": {"sequences": None}}, ACCEPTED),
+    ({"args": {"batch": 0, "table": None}}, ACCEPTED), ({"args": {"pages": 0}}, ACCEPTED),
+    ({"turn": {"positions": None}}, ACCEPTED),
+    ({"turn": {"positions": None, "axes": 2}}, bm.ERR_INVALID_ARG),
+    ({"turn": None, "q": {}}, bm.ERR_INVALID_ARG),
+    ({"kc": E4, "vc": dict(E4, data=E + (1 << 24))}, ACCEPTED),
+    ({"kc": E4}, bm.ERR_INVALID_ARG),                              # one 8-bit cache of two
+    ({"kc": {"kind": tk.E4M3}, "vc": {"kind": tk.E4M3}}, bm.ERR_INVALID_ARG),  # no scale
+    ({"kc": {"scale": A}}, bm.ERR_INVALID_ARG),                    # a scale without 8 bits
+    ({"kc": dict(E4, scale_stride=2), "vc": E4}, bm.ERR_INVALID_ARG),
+    ({"kc": {"kind": tk.F32}, "vc": {"kind": tk.F32}}, bm.ERR_INVALID_ARG),
+    ({"kc": {"data": None}}, bm.ERR_INVALID_ARG), ({"kc": {"data": E + 1}}, bm.ERR_INVALID_ARG),
+    ({"kc": {"head_stride": 64}}, bm.ERR_ALIAS),                   # heads overlap
+    ({"kc": {"page_stride": 1024}}, bm.ERR_ALIAS),                 # pages overlap
+    ({"kc": {"place_stride": 128, "head_stride": 2048}}, ACCEPTED),  # heads before places
+    ({"kc": {"data": A}}, bm.ERR_ALIAS),                           # the keys lie in the cache
+    ({"v": {"heads": 4}}, bm.ERR_INVALID_ARG), ({"k": {"x": None}}, bm.ERR_INVALID_ARG),
+    ({"args": {"page_size": 0}}, bm.ERR_INVALID_ARG), ({"args": {"pages": -1}}, bm.ERR_INVALID_ARG),
+    ({"args": {"table": None}}, bm.ERR_INVALID_ARG), ({"args": {"positions": None}}, bm.ERR_INVALID_ARG),
+    ({"args": {"pkind": 2}}, bm.ERR_INVALID_ARG), ({"args": {"batch": -1}}, bm.ERR_INVALID_ARG),
+    ({"args": {"sequences": C + 1}}, bm.ERR_INVALID_ARG),
+    ({"args": {"stride": -16}}, bm.ERR_INVALID_ARG),
+    ({"k_dim": 0}, bm.ERR_INVALID_ARG), ({"k_dim": 513}, bm.ERR_INVALID_ARG),
+    ({"k_dim": 100}, bm.ERR_INVALID_ARG),                          # 64 pairs do not fit
+    ({"tokens": -1}, bm.ERR_INVALID_ARG), ({"kind": tk.E4M3}, bm.ERR_INVALID_ARG)])
+def test_append_refusals(host, case, status):
+    args = dict(APPEND)
+    args.update(case.get("args", {}))
+    k, v = _heads(**case.get("k", {})), _heads(x=A + (1 << 22), **case.get("v", {}))
+    q = _heads(x=A + (1 << 23), **case["q"]) if "q" in case else None
+    if q is not None and "out" not in case["q"]:
+        q.out = G
+    turn = case.get("turn", {})
+    turn = None if turn is None else _turn(**turn)
+    kc, vc = _cache(**case.get("kc", {})), _cache(**{"data": E + (1 << 26), **case.get("vc", {})})
+    assert host.bmmc_cache_append(q, k, v, kc, vc, *args.values(), turn, case.get("tokens", 10),
+                                  case.get("k_dim", 128), 128, case.get("kind", tk.BF16),
+                                  None) == status
+
+
+def test_two_caches_in_one_array(host):
+    """Keys and values of a page next to each other: [pages, 2, places, heads, size]."""
+    k, v = _heads(), _heads(x=A + (1 << 22))
+    kc = _cache(page_stride=2 * 16 * 1024)
+    vc = _cache(page_stride=2 * 16 * 1024, data=E + 16 * 1024 * 2)
+    assert host.bmmc_cache_append(None, k, v, kc, vc, *APPEND.values(), None, 10, 128, 128,
+                                  tk.BF16, None) == ACCEPTED
+
+
+# --------------------------------------------------------------------------
+# The Python calls' checks
+# --------------------------------------------------------------------------
+
+def _order(tokens=4, choices=2, rows=None):
+    rows = tokens * choices if rows is None else rows
+    i = torch.int32
+    return bm.ExpertOrder(torch.zeros(4, dtype=i), torch.zeros(3, dtype=i),
+                          torch.zeros(tokens, choices, dtype=i), torch.zeros(rows, dtype=i))
+
+
+BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("call", [
+    lambda: bm.expert_order(torch.zeros(4, 2), 3),
+    lambda: bm.expert_order(torch.zeros(4, 4, dtype=torch.int32)[:, :2], 3),
+    lambda: bm.expert_order(torch.zeros(4, 2, dtype=torch.int64), 0),
+    lambda: bm.expert_order(torch.zeros(4, 2, dtype=torch.int64), 2049),
+    lambda: bm.expert_order(torch.zeros(4, 2, dtype=torch.int64), 3, align=0),
+    lambda: bm.expert_gather(torch.zeros(4, 8), None),
+    lambda: bm.expert_gather(torch.zeros(5, 8), _order()),
+    lambda: bm.expert_gather(torch.zeros(4, 8, dtype=torch.float64), _order()),
+    lambda: bm.expert_gather(torch.zeros(8, 4).t(), _order()),
+    lambda: bm.expert_gather(torch.zeros(4, 0), _order()),
+    lambda: bm.expert_gather(torch.zeros(4, 8), _order(rows=7)),
+    lambda: bm.expert_gather(torch.zeros(4, 8), _order(), out=torch.zeros(8, 7)),
+    lambda: bm.expert_gather(torch.zeros(4, 8), _order(), out=torch.zeros(8, 8, dtype=BF)),
+    lambda: bm.expert_gather(torch.zeros(4, 8, requires_grad=True), _order(), out=torch.zeros(8, 8)),
+    lambda: bm.expert_combine(torch.zeros(7, 8), _order()),
+    lambda: bm.expert_combine(torch.zeros(8, 8), _order(), torch.zeros(4, 3)),
+    lambda: bm.expert_combine(torch.zeros(8, 8), _order(), torch.zeros(4, 2, dtype=BF)),
+    lambda: bm.expert_combine(torch.zeros(8, 8), _order(), torch.zeros(2, 4).t()),
+    lambda: bm.expert_combine_backward(torch.zeros(4, 7), torch.zeros(8, 8), _order(), torch.zeros(4, 2)),
+    lambda: bm.expert_combine_backward(torch.zeros(4, 8, dtype=BF), torch.zeros(8, 8), _order(),
+                                       torch.zeros(4, 2)),
+    lambda: bm.expert_gather_backward(torch.zeros(7, 8), _order()),
+    lambda: bm.rotary_axes([]), lambda: bm.rotary_axes([-1, 2]), lambda: bm.rotary_axes([0]),
+])
+def test_expert_calls_refuse(call):
+    with pytest.raises(ValueError):
+        call()
+
+
+POS = torch.zeros(4, dtype=torch.int64)
+F = torch.ones(4, dtype=torch.float64)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: bm.rotary(torch.zeros(4, 8), POS, F),
+    lambda: bm.rotary(torch.zeros(4, 2, 8, dtype=torch.float64), POS, F),
+    lambda: bm.rotary(torch.zeros(4, 2, 6), POS, F),
+    lambda: bm.rotary(torch.zeros(4, 2, 514), POS, F),
+    lambda: bm.rotary(torch.zeros(4, 0, 8), POS, F),
+    lambda: bm.rotary(torch.zeros(4, 8, 2).transpose(1, 2), POS, F),
+    lambda: bm.rotary(torch.zeros(4, 2, 8), POS.int()[:3], F),
+    lambda: bm.rotary(torch.zeros(4, 2, 8), POS.float(), F),
+    lambda: bm.rotary(torch.zeros(4, 2, 8), None, F),
+    lambda: bm.rotary(torch.zeros(4, 2, 8), torch.zeros(9, 4, dtype=torch.int64), F),
+    lambda: bm.rotary(torch.zeros(4, 2, 8), torch.zeros(4, 3, dtype=torch.int64).t(), F),
+    lambda: bm.rotary(torch.zeros(4, 2, 8), POS, F.half()),
+    lambda: bm.rotary(torch.zeros(4, 2, 8), POS, F[None]),
+    lambda: bm.rotary(torch.zeros(4, 2, 8), POS, F, axes=torch.zeros(3, dtype=torch.int32)),
+    lambda: bm.rotary(torch.zeros(4, 2, 8), POS, F, axes=torch.zeros(4, dtype=torch.int64)),
+    lambda: bm.rotary((torch.zeros(4, 2, 8), torch.zeros(3, 2, 8)), POS, F),
+    lambda: bm.rotary((torch.zeros(4, 2, 8), torch.zeros(4, 2, 8, dtype=BF)), POS, F),
+    lambda: bm.rotary([torch.zeros(4, 2, 8)] * 3, POS, F),
+    lambda: bm.rotary(torch.zeros(4, 2, 8), POS, F, out=torch.zeros(4, 2, 9)),
+    lambda: bm.rotary(torch.zeros(4, 2, 8, requires_grad=True), POS, F, out=torch.zeros(4, 2, 8)),
+])
+def test_rotary_calls_refuse(call):
+    with pytest.raises(ValueError):
+        call()
+
+
+def _append(**changes):
+    a = dict(k=torch.zeros(4, 2, 8), v=torch.zeros(4, 2, 8), k_cache=torch.zeros(3, 4, 2, 8),
+             v_cache=torch.zeros(3, 4, 2, 8), page_table=torch.zeros(4, 2, dtype=torch.int32),
+             positions=POS)
+    a.update(changes)
+    return bm.cache_append(**a)
+
+
+F8 = torch.float8_e4m3fn
+
+
+@pytest.mark.parametrize("changes", [
+    {"k": torch.zeros(4, 2, 8, dtype=BF)}, {"k": torch.zeros(5, 2, 8)}, {"k": torch.zeros(4, 8)},
+    {"k_cache": torch.zeros(3, 4, 2, 9)}, {"k_cache": torch.zeros(3, 4, 2, 8, dtype=BF)},
+    {"k_cache": torch.zeros(2, 4, 2, 8)}, {"k_cache": torch.zeros(3, 4, 8, 2).transpose(2, 3)},
+    {"k_cache": torch.zeros(3, 4, 2, 8).to(F8)},
+    {"k_scale": torch.ones(2)},
+    {"k_cache": torch.zeros(3, 4, 2, 8).to(F8), "k_scale": torch.ones(3)},
+    {"k_cache": torch.zeros(3, 0, 2, 8), "v_cache": torch.zeros(3, 0, 2, 8)},
+    {"page_table": torch.zeros(4, 2, dtype=torch.int64)},
+    {"page_table": torch.zeros(2, 4, dtype=torch.int32).t()},
+    {"positions": POS[:3]}, {"positions": POS.float()},
+    {"sequences": torch.zeros(4, dtype=torch.int64)}, {"sequences": torch.zeros(3, dtype=torch.int32)},
+    {"q": torch.zeros(4, 2, 8)}, {"turns": POS}, {"q_out": torch.zeros(4, 2, 8)},
+    {"freqs": F, "q": torch.zeros(4, 2, 6)}, {"freqs": F, "turns": POS[:2]},
+    {"freqs": torch.ones(5)}, {"freqs": F, "q_out": torch.zeros(4, 2, 8)},
+    {"k": torch.zeros(4, 2, 8, requires_grad=True)},
+    {"k": torch.zeros(4, 2, 520), "v": torch.zeros(4, 2, 520)}])
+def test_append_calls_refuse(changes):
+    with pytest.raises(ValueError):
+        _append(**changes)
+
+
+def test_host_tensors_are_refused():
+    """Everything else in order: there is no path for host memory."""
+    for call in (lambda: bm.expert_order(torch.zeros(4, 2, dtype=torch.int64), 3),
+                 lambda: bm.expert_gather(torch.zeros(4, 8), _order()),
+                 lambda: bm.expert_combine(torch.zeros(8, 8), _order(), torch.zeros(4, 2)),
+                 lambda: bm.rotary(torch.zeros(4, 2, 8), POS, F), lambda: _append()):
+        with pytest.raises(ValueError, match="device"):
+            call()
+
+
+def test_rotary_axes():
+    assert bm.rotary_axes([2, 1, 1]).tolist() == [0, 0, 1, 2]
+    assert bm.rotary_axes([1, 3, 2], interleaved=True).tolist() == [0, 1, 2, 1, 2, 1]
