@@ -147,6 +147,15 @@ at::TensorOptions int32_on(const Tensor &t) { return t.options().dtype(at::kInt)
 
 // ---- tokens by expert ------------------------------------------------------
 
+// The elements of `all` from `first` on as a contiguous tensor of its own shape.
+Tensor part_of(const Tensor &all, int64_t first, at::IntArrayRef shape) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()),
+                                                        all.key_set(), all.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(first);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    return t;
+}
+
 // order(experts, num_experts, align, stream) -> offsets, counts, rows, slots
 // and the workspace or None, which other streams than the current one use.
 PyObject *py_order(PyObject *, PyObject *const *a, Py_ssize_t) {
@@ -163,9 +172,12 @@ PyObject *py_order(PyObject *, PyObject *const *a, Py_ssize_t) {
     const int64_t need = lib.expert_order_workspace(n, e);
     const at::TensorOptions like = int32_on(experts);
     const bool flat = experts.dim() != 2;
-    Tensor offsets = at::empty({e + 1}, like), counts = at::empty({e}, like);
-    Tensor rows = at::empty({flat ? n : experts.size(0), flat ? 1 : experts.size(1)}, like);
-    Tensor slots = at::empty({capacity}, like), work;
+    // one allocation for the four results
+    const Tensor all = at::empty({2 * e + 1 + n + capacity}, like);
+    Tensor offsets = part_of(all, 0, {e + 1}), counts = part_of(all, e + 1, {e});
+    Tensor rows = part_of(all, 2 * e + 1,
+                          {flat ? n : experts.size(0), flat ? 1 : experts.size(1)});
+    Tensor slots = part_of(all, 2 * e + 1 + n, {capacity}), work;
     if (need) work = at::empty({need / 4}, like);
     check_status(lib.expert_order(experts.data_ptr(), index_type(experts), n, e, align,
                                   offsets.data_ptr<int32_t>(), counts.data_ptr<int32_t>(),
@@ -175,9 +187,7 @@ PyObject *py_order(PyObject *, PyObject *const *a, Py_ssize_t) {
     PyObject *got[5] = {THPVariable_Wrap(offsets), THPVariable_Wrap(counts),
                         THPVariable_Wrap(rows), THPVariable_Wrap(slots),
                         need ? THPVariable_Wrap(work) : Py_NewRef(Py_None)};
-    PyObject *all = PyTuple_New(5);
-    for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(all, i, got[i]);
-    return all;
+    return Py_BuildValue("NNNNN", got[0], got[1], got[2], got[3], got[4]);
     END_HANDLE_TH_ERRORS
 }
 

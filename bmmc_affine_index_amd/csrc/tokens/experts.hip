@@ -1,13 +1,13 @@
 // experts.hip -- token rows to their experts and back (gfx950).
 //
-// All three passes are bound by memory.  They go token by token, so that each
-// token's own row is read or written once however many choices it has, and
-// the rows by expert, which are choices times as many, are touched once each:
+// All three passes are bound by memory:
 //   gather    reads T D, writes R D elements
 //   combine   reads up to T K D, writes T D
 //   backward  reads T D + T K D, writes R D
-// A lane holds one 16-byte vector of the token's row and moves the same
-// columns of all its choices' rows, whose loads are in flight together.
+// They go token by token, so that each token's own row is read or written once
+// however many choices it has: a lane holds one 16-byte vector of the token's
+// row and moves the same columns of all its choices' rows, whose loads are in
+// flight together.
 #include "device.h"
 #include "tokens.h"
 
@@ -15,8 +15,12 @@ namespace bmmc {
 
 namespace {
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveWaves = kMoveThreads / 64;
+// Threads of a workgroup, measured on 16384 tokens of 8 choices, 8 KiB a row:
+// gather 224 us with 256 and 230 with 128, combine 212 and 200; at other sizes
+// (2 to 14 KiB a row) the two differ by up to 3% the same way.
+constexpr int kGatherThreads = 256;
+constexpr int kCombineThreads = 128;
+constexpr int kBackwardThreads = 256;
 // Rows of the order that one wave looks through for padding.
 constexpr int kPadRows = 16;
 
@@ -37,16 +41,17 @@ struct Cut {
 // WAVE: each wave is one token's, so that its row numbers and weights are
 // scalars; else lanes take the vectors of successive tokens in turn, which
 // leaves no lane without work when a row is not a multiple of 64 vectors.
-template <bool WAVE, int N>
+template <int THREADS, bool WAVE, int N>
 __device__ __forceinline__ Place locate(const Cut &c, int64_t tokens, int64_t dim,
                                         uint32_t block) {
     uint32_t token, vec;
     if constexpr (WAVE) {
-        const uint32_t task = block * kMoveWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const uint32_t task =
+            block * (THREADS / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         token = quotient(c.by, task);
         vec = (task - token * c.by.d) * 64 + (threadIdx.x & 63);
     } else {
-        const uint32_t task = block * kMoveThreads + threadIdx.x;
+        const uint32_t task = block * THREADS + threadIdx.x;
         token = quotient(c.by, task);
         vec = task - token * c.by.d;
     }
@@ -93,14 +98,15 @@ __device__ __forceinline__ void zero_padding(const MoveArgs &a, int64_t wave) {
 }
 
 template <typename T, int N, bool WAVE>
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kGatherThreads)
     bmmc_expert_gather_kernel(const MoveArgs a, const Cut c, uint32_t block0) {
     const uint32_t block = block0 + blockIdx.x;
     if (block >= c.parts) {
-        zero_padding<T, N>(a, (int64_t)(block - c.parts) * kMoveWaves + (threadIdx.x >> 6));
+        zero_padding<T, N>(
+            a, (int64_t)(block - c.parts) * (kGatherThreads / 64) + (threadIdx.x >> 6));
         return;
     }
-    const Place p = locate<WAVE, N>(c, a.tokens, a.dim, block);
+    const Place p = locate<kGatherThreads, WAVE, N>(c, a.tokens, a.dim, block);
     if (p.at < 0) return;
     const dev::Vec<T, N> v =
         dev::load<T, N>(static_cast<const T *>(a.x) + p.token * a.x_stride + p.at);
@@ -133,9 +139,9 @@ __device__ __forceinline__ void add_rows(const MoveArgs &a, const Place &p, int 
 }
 
 template <typename T, int N, bool WAVE>
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kCombineThreads)
     bmmc_expert_combine_kernel(const MoveArgs a, const Cut c, uint32_t block0) {
-    const Place p = locate<WAVE, N>(c, a.tokens, a.dim, block0 + blockIdx.x);
+    const Place p = locate<kCombineThreads, WAVE, N>(c, a.tokens, a.dim, block0 + blockIdx.x);
     if (p.at < 0) return;
     dev::Floats<N> sum = 0.0f;
     int k = 0;
@@ -147,150 +153,195 @@ __global__ void __launch_bounds__(kMoveThreads)
                      dev::narrow<T, N>(sum));
 }
 
+// Sums of G values over the 64 lanes of a wave (every lane active), that of
+// value g in the lanes with lane % G == g: while there are several values,
+// each step sends half of them to the lane that keeps that half, 10 exchanges
+// for 8 values against 48 one by one.
+template <int G> __device__ __forceinline__ float wave_sums(float (&v)[G]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int h = G / 2; h; h /= 2) {
+        const bool upper = lane & h;
+#pragma unroll
+        for (int g = 0; g < h; ++g) {
+            const float keep = upper ? v[g + h] : v[g], send = upper ? v[g] : v[g + h];
+            v[g] = keep + __shfl_xor(send, h, 64);
+        }
+    }
+#pragma unroll
+    for (int d = G; d < 64; d *= 2) v[0] += __shfl_xor(v[0], d, 64);
+    return v[0];
+}
+
 // Gradients of G choices from k on of one token, by WAVES waves: each lane
 // sums its columns, then the lanes, then the waves, in a fixed order.
+// sums[WAVES][8] is the token's.
 template <typename T, int N, int WAVES, int G>
 __device__ __forceinline__ void choices_backward(const MoveArgs &a, int64_t token, int k,
-                                                 int part, float *lds) {
+                                                 int part, float *sums) {
     const int lane = threadIdx.x & 63;
+    const int dim = (int)a.dim, last = dim - N;
+    const bool on = token < a.tokens;
     float dot[G], w[G];
     int32_t row[G];
-    const int64_t i = token * a.choices + k;
+    const int64_t i = (on ? token : 0) * a.choices + k;
     choices_at<T, G>(a, i, row, w);
 #pragma unroll
     for (int g = 0; g < G; ++g) dot[g] = 0.0f;
-    const T *grad = static_cast<const T *>(a.x) + token * a.x_stride;
-    for (int64_t from = (int64_t)(part * 64 + lane) * N; from < a.dim; from += WAVES * 64 * N) {
-        const int64_t at = min(from, a.dim - N);
-        const dev::Floats<N> d = dev::widen<T, N>(dev::load<T, N, false>(grad + at));
+    const T *grad = static_cast<const T *>(a.x) + (on ? token : 0) * a.x_stride;
+    for (int from = (part * 64 + lane) * N; on && from < dim; from += WAVES * 64 * N) {
+        const int at = min(from, last);
+        const dev::Vec<T, N> own = dev::load<T, N, false>(grad + at);
         dev::Vec<T, N> v[G];
+        // a dropped choice reads row 0, which is there
 #pragma unroll
         for (int g = 0; g < G; ++g)
             v[g] = dev::load<T, N>(static_cast<const T *>(a.in) +
                                    max(row[g], 0) * a.in_stride + at);
+        // every load is under way before the first is waited for
+        __builtin_amdgcn_sched_barrier(0);
+        const dev::Floats<N> d = dev::widen<T, N>(own);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const dev::Floats<N> f = dev::widen<T, N>(v[g]);
-            // elements that the vector before holds too are summed there alone
-#pragma unroll
-            for (int j = 0; j < N; ++j) dot[g] = j >= from - at ? fmaf(d[j], f[j], dot[g]) : dot[g];
+        for (int g = 0; g < G; ++g)
             if (row[g] >= 0)
                 dev::store<T, N>(static_cast<T *>(a.out) + row[g] * a.out_stride + at,
                                  dev::narrow<T, N>(d * w[g]));
+        // elements that the vector before holds too are summed there alone
+        const int first = from - at;
+        if (first > 0) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const dev::Floats<N> f = dev::widen<T, N>(v[g]);
+#pragma unroll
+                for (int j = 0; j < N; ++j) dot[g] = j >= first ? fmaf(d[j], f[j], dot[g]) : dot[g];
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const dev::Floats<N> f = dev::widen<T, N>(v[g]);
+#pragma unroll
+                for (int j = 0; j < N; ++j) dot[g] = fmaf(d[j], f[j], dot[g]);
+            }
         }
     }
-#pragma unroll
-    for (int g = 0; g < G; ++g) dot[g] = dev::wave_sum(dot[g]);
+    float sum = wave_sums<G>(dot);
     if constexpr (WAVES > 1) {
         __syncthreads();  // the last group's sums have been read
-        if (lane == 0)
-#pragma unroll
-            for (int g = 0; g < G; ++g) lds[part * 8 + g] = dot[g];
+        if (lane < G) sums[part * 8 + lane] = sum;
         __syncthreads();
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            dot[g] = 0.0f;
-            for (int p = 0; p < WAVES; ++p) dot[g] += lds[p * 8 + g];
+        if (lane < G) {
+            sum = 0.0f;
+            for (int p = 0; p < WAVES; ++p) sum += sums[p * 8 + lane];
         }
     }
-    if (part == 0 && lane == 0) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const float r = row[g] < 0 ? 0.0f : dot[g];
-            if (a.weights_are_f32)
-                static_cast<float *>(a.grad_weights)[i + g] = r;
-            else
-                static_cast<T *>(a.grad_weights)[i + g] = (T)r;
-        }
+    if (on && part == 0 && lane < G) {
+        const int32_t mine = a.rows[i + lane];
+        const float r = mine >= 0 && mine < a.capacity ? sum : 0.0f;
+        if (a.weights_are_f32)
+            static_cast<float *>(a.grad_weights)[i + lane] = r;
+        else
+            static_cast<T *>(a.grad_weights)[i + lane] = (T)r;
     }
 }
 
 template <typename T, int N, int WAVES>
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kBackwardThreads)
     bmmc_expert_combine_backward_kernel(const MoveArgs a, uint32_t parts, uint32_t block0) {
-    __shared__ float lds[kMoveWaves * 8];
+    constexpr int kWaves = kBackwardThreads / 64;
+    __shared__ float sums[kWaves * 8];
     const uint32_t block = block0 + blockIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (block >= parts) {
-        zero_padding<T, N>(a, (int64_t)(block - parts) * kMoveWaves + wave);
+        zero_padding<T, N>(a, (int64_t)(block - parts) * kWaves + wave);
         return;
     }
-    const int64_t token = (int64_t)block * (kMoveWaves / WAVES) + (WAVES == 1 ? wave : 0);
-    const int part = WAVES == 1 ? 0 : wave;
-    if (token >= a.tokens) return;  // a whole wave, or with 4 waves a token the workgroup
+    // a wave past the last token stays for the workgroup's barriers
+    const int64_t token = (int64_t)block * (kWaves / WAVES) + wave / WAVES;
+    const int part = wave % WAVES;
+    float *mine = sums + wave / WAVES * WAVES * 8;
     int k = 0;
-    for (; k + 8 <= a.choices; k += 8) choices_backward<T, N, WAVES, 8>(a, token, k, part, lds);
-    if (a.choices & 4) choices_backward<T, N, WAVES, 4>(a, token, k, part, lds), k += 4;
-    if (a.choices & 2) choices_backward<T, N, WAVES, 2>(a, token, k, part, lds), k += 2;
-    if (a.choices & 1) choices_backward<T, N, WAVES, 1>(a, token, k, part, lds);
+    for (; k + 8 <= a.choices; k += 8) choices_backward<T, N, WAVES, 8>(a, token, k, part, mine);
+    if (a.choices & 4) choices_backward<T, N, WAVES, 4>(a, token, k, part, mine), k += 4;
+    if (a.choices & 2) choices_backward<T, N, WAVES, 2>(a, token, k, part, mine), k += 2;
+    if (a.choices & 1) choices_backward<T, N, WAVES, 1>(a, token, k, part, mine);
 }
 
 // Whether each wave is one token's: where that leaves at most a fifth of the
 // lanes idle, or where the vectors of all tokens pass the 31 bits of a
 // quotient.  *fits is false where the waves pass them too.
-template <int N> bool by_waves(const MoveArgs &a, Cut *c, bool *fits) {
+template <int N, int THREADS> bool by_waves(const MoveArgs &a, Cut *c, bool *fits) {
     constexpr int64_t kMost = int64_t(1) << 31;
+    constexpr int kWaves = THREADS / 64;
     const int64_t vectors = (a.dim + N - 1) / N, waves = (vectors + 63) / 64;
     c->vectors = (uint32_t)vectors;
-    *fits = a.tokens * waves < kMost - kMoveThreads;
-    if (vectors * 5 >= waves * 64 * 4 || a.tokens * vectors >= kMost - kMoveThreads) {
+    *fits = a.tokens * waves < kMost - THREADS;
+    if (vectors * 5 >= waves * 64 * 4 || a.tokens * vectors >= kMost - THREADS) {
         c->by = fast_div((uint32_t)waves);
-        c->parts = (uint32_t)((a.tokens * waves + kMoveWaves - 1) / kMoveWaves);
+        c->parts = (uint32_t)((a.tokens * waves + kWaves - 1) / kWaves);
         return true;
     }
     c->by = fast_div((uint32_t)vectors);
-    c->parts = (uint32_t)((a.tokens * vectors + kMoveThreads - 1) / kMoveThreads);
+    c->parts = (uint32_t)((a.tokens * vectors + THREADS - 1) / THREADS);
     return false;
 }
 
 int64_t pad_blocks(int64_t capacity) {
-    return (capacity + kMoveWaves * kPadRows - 1) / (kMoveWaves * kPadRows);
+    static_assert(kGatherThreads == kBackwardThreads, "both look for padding");
+    constexpr int kRows = kGatherThreads / 64 * kPadRows;
+    return (capacity + kRows - 1) / kRows;
 }
 
 template <typename T, int N> int gather_n(const MoveArgs &a, hipStream_t s) {
     Cut c;
     bool fits;
-    const bool wave = by_waves<N>(a, &c, &fits);
+    const bool wave = by_waves<N, kGatherThreads>(a, &c, &fits);
     if (!fits) return BMMC_ERR_UNSUPPORTED;
-    return in_launches(c.parts + pad_blocks(a.capacity), kMoveThreads, [&](uint32_t nb, int64_t b0) {
+    return in_launches(c.parts + pad_blocks(a.capacity), kGatherThreads, [&](uint32_t nb, int64_t b0) {
         if (wave)
             hipLaunchKernelGGL((bmmc_expert_gather_kernel<T, N, true>), dim3(nb),
-                               dim3(kMoveThreads), 0, s, a, c, (uint32_t)b0);
+                               dim3(kGatherThreads), 0, s, a, c, (uint32_t)b0);
         else
             hipLaunchKernelGGL((bmmc_expert_gather_kernel<T, N, false>), dim3(nb),
-                               dim3(kMoveThreads), 0, s, a, c, (uint32_t)b0);
+                               dim3(kGatherThreads), 0, s, a, c, (uint32_t)b0);
     });
 }
 
 template <typename T, int N> int combine_n(const MoveArgs &a, hipStream_t s) {
     Cut c;
     bool fits;
-    const bool wave = by_waves<N>(a, &c, &fits);
+    const bool wave = by_waves<N, kCombineThreads>(a, &c, &fits);
     if (!fits) return BMMC_ERR_UNSUPPORTED;
-    return in_launches(c.parts, kMoveThreads, [&](uint32_t nb, int64_t b0) {
+    return in_launches(c.parts, kCombineThreads, [&](uint32_t nb, int64_t b0) {
         if (wave)
             hipLaunchKernelGGL((bmmc_expert_combine_kernel<T, N, true>), dim3(nb),
-                               dim3(kMoveThreads), 0, s, a, c, (uint32_t)b0);
+                               dim3(kCombineThreads), 0, s, a, c, (uint32_t)b0);
         else
             hipLaunchKernelGGL((bmmc_expert_combine_kernel<T, N, false>), dim3(nb),
-                               dim3(kMoveThreads), 0, s, a, c, (uint32_t)b0);
+                               dim3(kCombineThreads), 0, s, a, c, (uint32_t)b0);
     });
 }
 
-// One wave a token fills the card from about four waves a SIMD on (1024
-// SIMDs); below that four waves share a token.
-constexpr int64_t kBackwardWaveTokens = 4096;
-
+// Waves of a token: as many as its row has vectors for, at most 4.  8192
+// tokens of 8 choices, 4 KiB a row: 104 us with 4 waves, 114 with one that
+// takes 4 vectors in turn (and 112 row by row in the order, where rows are read
+// and written one after the other but each token's gradient is read 8 times).
 template <typename T, int N> int combine_backward_n(const MoveArgs &a, hipStream_t s) {
-    const bool wide = a.tokens < kBackwardWaveTokens;
-    const int64_t parts = wide ? a.tokens : (a.tokens + kMoveWaves - 1) / kMoveWaves;
-    return in_launches(parts + pad_blocks(a.capacity), kMoveThreads, [&](uint32_t nb, int64_t b0) {
-        if (wide)
-            hipLaunchKernelGGL((bmmc_expert_combine_backward_kernel<T, N, kMoveWaves>), dim3(nb),
-                               dim3(kMoveThreads), 0, s, a, (uint32_t)parts, (uint32_t)b0);
+    const int64_t vectors = (a.dim + N - 1) / N;
+    const int waves = vectors <= 64 ? 1 : vectors <= 128 ? 2 : 4;
+    const int64_t tokens = kBackwardThreads / 64 / waves;  // a workgroup
+    const int64_t parts = (a.tokens + tokens - 1) / tokens;
+    return in_launches(parts + pad_blocks(a.capacity), kBackwardThreads,
+                       [&](uint32_t nb, int64_t b0) {
+        const auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3(nb), dim3(kBackwardThreads), 0, s, a,
+                               (uint32_t)parts, (uint32_t)b0);
+        };
+        if (waves == 1)
+            launch(bmmc_expert_combine_backward_kernel<T, N, 1>);
+        else if (waves == 2)
+            launch(bmmc_expert_combine_backward_kernel<T, N, 2>);
         else
-            hipLaunchKernelGGL((bmmc_expert_combine_backward_kernel<T, N, 1>), dim3(nb),
-                               dim3(kMoveThreads), 0, s, a, (uint32_t)parts, (uint32_t)b0);
+            launch(bmmc_expert_combine_backward_kernel<T, N, 4>);
     });
 }
 

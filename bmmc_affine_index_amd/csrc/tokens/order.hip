@@ -10,17 +10,19 @@
 // per wave and expert in LDS holds how many came before.  Nothing depends on
 // the order in which waves run.
 //
-// Bound by latency: it reads 4 or 8 bytes and writes 8 for each choice.
+// Bound by latency: it reads 4 or 8 bytes and writes 8 for each choice, in two
+// launches for many choices.  256 choices of 64 experts take 3.0 us, 131072 of
+// 128 experts 10.9 us.
 #include "tokens.h"
 
 namespace bmmc {
 
 namespace {
 
-constexpr int kOrderThreads = 1024;
-// Counters per wave and expert: 16 waves up to 1024 experts, 8 beyond, so
-// that the counters fill at most 64 KiB of LDS.
+// Counters per wave and expert fill at most 64 KiB of LDS: 16 waves up to
+// 1024 experts, 8 beyond.
 constexpr int kOrderWideExperts = 1024;
+constexpr int kOrderMaxWaves = 16;
 
 __device__ __forceinline__ int32_t expert_at(const OrderArgs &a, int64_t i) {
     if (a.is64) {
@@ -32,7 +34,7 @@ __device__ __forceinline__ int32_t expert_at(const OrderArgs &a, int64_t i) {
 }
 
 // Choices of each expert in each chunk.
-__global__ void __launch_bounds__(kOrderThreads)
+__global__ void __launch_bounds__(kOrderMaxWaves * 64)
     bmmc_expert_count_kernel(const OrderArgs a) {
     extern __shared__ int32_t cnt[];
     const int tid = threadIdx.x;
@@ -50,8 +52,9 @@ __global__ void __launch_bounds__(kOrderThreads)
 }
 
 // Exclusive scan over the workgroup of one value a thread; *total is the sum.
+template <int WAVES>
 __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *wsum, int32_t *total) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int32_t inc = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -62,7 +65,8 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *wsum, int32_t 
     if (lane == 63) wsum[wave] = inc;
     __syncthreads();
     int32_t before = 0, all = 0;
-    for (int w = 0; w < waves; ++w) {
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
         const int32_t s = wsum[w];
         before += w < wave ? s : 0;
         all += s;
@@ -71,111 +75,200 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t *wsum, int32_t 
     return before + inc - v;
 }
 
-// Rows of every choice of this workgroup's chunk.  MANY: the other chunks'
-// counts come from a.hist.
-template <bool MANY>
-__global__ void __launch_bounds__(kOrderThreads) bmmc_expert_place_kernel(const OrderArgs a) {
-    extern __shared__ int32_t cnt[];  // [waves][num_experts]
-    __shared__ int32_t wsum[16];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
-    const int E = a.num_experts;
-    for (int i = tid; i < waves * E; i += blockDim.x) cnt[i] = 0;
+// This lane's place among its wave's choices of expert e (-1: none) so far;
+// my[e] counts them.
+__device__ __forceinline__ int32_t place_in_wave(int32_t *my, int32_t e, int E, int bits) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t key = e >= 0 ? (uint32_t)e : (uint32_t)E;
+    uint64_t same = ~uint64_t(0);
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((key >> b) & 1u);
+        same &= ((key >> b) & 1u) ? set : ~set;
+    }
+    int32_t at = -1;
+    if (e >= 0)
+        at = __hip_atomic_load(&my[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) +
+             __popcll(same & ((uint64_t(1) << lane) - 1));
+    // every lane has read before the last lane of each expert writes
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (e >= 0 && (same >> lane) == 1)
+        __hip_atomic_store(&my[e], at + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    return at;
+}
+
+// Sums over the chunks of a.hist for this workgroup's expert e0 + column: of
+// those before this chunk and of all.  The threads take the chunks of a column
+// in turn, as many threads a column as there are, so that the loads of 64
+// chunks and 128 experts are 8 a thread and not 64 in a row (the kernel took
+// 20.6 us of 131072 choices with one thread a column).
+struct Before {
+    int32_t before, all;
+};
+template <int THREADS>
+__device__ __forceinline__ Before sum_chunks(const OrderArgs &a, int e0, int32_t (*part)[THREADS]) {
+    const int tid = threadIdx.x, E = a.num_experts;
+    const int columns = min(E - e0, THREADS);
+    const int threads = THREADS / columns;  // a column
+    const int share = tid / columns, e = tid - share * columns;
+    int32_t before = 0, all = 0;
+    if (share < threads) {
+        const int32_t *h = a.hist + e0 + e;
+#pragma unroll 4
+        for (int b = share; b < (int)gridDim.x; b += threads) {
+            const int32_t c = h[(int64_t)b * E];
+            before += b < (int)blockIdx.x ? c : 0;
+            all += c;
+        }
+    }
+    __syncthreads();  // part may still be read from the last columns
+    part[0][tid] = before;
+    part[1][tid] = all;
     __syncthreads();
+    Before sum{0, 0};
+    if (tid < columns)
+        for (int s = 0; s < threads; ++s) {
+            sum.before += part[0][s * columns + tid];
+            sum.all += part[1][s * columns + tid];
+        }
+    return sum;
+}
+
+// Rows of every choice of this workgroup's chunk.  MANY: the other chunks'
+// counts come from a.hist.  ROUNDS: choices a lane, kept in registers; 0: as
+// many as there are, read a second time.
+template <int WAVES, int ROUNDS, bool MANY>
+__global__ void __launch_bounds__(WAVES * 64) bmmc_expert_place_kernel(const OrderArgs a) {
+    constexpr int kThreads = WAVES * 64;
+    extern __shared__ int32_t cnt[];  // [WAVES][num_experts]
+    __shared__ int32_t wsum[WAVES];
+    __shared__ int32_t part[2][MANY ? kThreads : 1];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int E = a.num_experts;
+    const int bits = 32 - __clz(E);  // of the numbers 0 .. E
 
     // each wave's piece of the chunk, in order
     const int64_t from = blockIdx.x * a.chunk;
     const int64_t to = min(from + a.chunk, a.n);
-    const int64_t rounds = (a.chunk + 64 * waves - 1) / (64 * waves);
-    const int64_t mine = from + wave * rounds * 64;
+    const int rounds = (int)((a.chunk + kThreads - 1) / kThreads);
+    const int64_t mine = from + (int64_t)wave * rounds * 64 + lane;
     int32_t *my = cnt + wave * E;
-    for (int64_t r = 0; r < rounds; ++r) {
-        const int64_t i = mine + r * 64 + lane;
-        const int32_t e = i < to ? expert_at(a, i) : -1;
-        if (e >= 0) atomicAdd(&my[e], 1);
+    int32_t held[ROUNDS ? ROUNDS : 1], at[ROUNDS ? ROUNDS : 1];
+    if constexpr (ROUNDS > 0) {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int64_t i = mine + r * 64;
+            held[r] = r < rounds && i < to ? expert_at(a, i) : -1;
+        }
+    }
+    for (int i = tid; i < WAVES * E; i += kThreads) cnt[i] = 0;
+    __syncthreads();
+    if constexpr (ROUNDS > 0) {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+            if (r < rounds) at[r] = place_in_wave(my, held[r], E, bits);
+    } else {
+        for (int r = 0; r < rounds; ++r) {
+            const int64_t i = mine + (int64_t)r * 64;
+            const int32_t e = i < to ? expert_at(a, i) : -1;
+            if (e >= 0) atomicAdd(&my[e], 1);
+        }
     }
     __syncthreads();
 
     // first row of each wave's choices of each expert
-    int64_t start = 0;
-    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+    int32_t start = 0;
+    for (int e0 = 0; e0 < E; e0 += kThreads) {
         const int e = e0 + tid;
-        int32_t here = 0, before = 0, all = 0;
-        if (e < E) {
-            for (int w = 0; w < waves; ++w) {
-                const int32_t c = cnt[w * E + e];
-                cnt[w * E + e] = here;
-                here += c;
-            }
-            all = here;
-            if constexpr (MANY) {
-                all = 0;
-                for (int b = 0; b < (int)gridDim.x; ++b) {
-                    const int32_t c = a.hist[(int64_t)b * E + e];
-                    before += b < (int)blockIdx.x ? c : 0;
-                    all += c;
-                }
-            }
+        int32_t here[WAVES], sum = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) here[w] = e < E ? cnt[w * E + e] : 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const int32_t c = here[w];
+            here[w] = sum;
+            sum += c;
         }
-        const int32_t padded = (int32_t)((all + a.align - 1) / a.align * a.align);
-        int32_t sum;
-        const int32_t off = (int32_t)start + block_scan(padded, wsum, &sum);
-        start += sum;
+        Before b{0, sum};
+        if constexpr (MANY) b = sum_chunks<kThreads>(a, e0, part);
+        const int32_t padded =
+            e < E ? (int32_t)((b.all + a.align - 1) / a.align * a.align) : 0;
+        int32_t total;
+        const int32_t off = start + block_scan<WAVES>(padded, wsum, &total);
+        start += total;
         if (e < E) {
-            for (int w = 0; w < waves; ++w) cnt[w * E + e] += off + before;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) cnt[w * E + e] = here[w] + off + b.before;
             if (blockIdx.x == 0) {
                 a.offsets[e] = off;
-                a.counts[e] = all;
-                for (int32_t r = off + all; r < off + padded; ++r) a.slots[r] = -1;
+                a.counts[e] = b.all;
             }
+            if (e % gridDim.x == blockIdx.x)
+                for (int32_t r = off + b.all; r < off + padded; ++r) a.slots[r] = -1;
         }
     }
-    if (blockIdx.x == 0 && tid == 0) a.offsets[E] = (int32_t)start;
+    if (blockIdx.x == 0 && tid == 0) a.offsets[E] = start;
     // rows past the last expert's
-    for (int64_t r = start + (int64_t)blockIdx.x * blockDim.x + tid; r < a.capacity;
-         r += (int64_t)gridDim.x * blockDim.x)
+    for (int64_t r = start + (int64_t)blockIdx.x * kThreads + tid; r < a.capacity;
+         r += (int64_t)gridDim.x * kThreads)
         a.slots[r] = -1;
     __syncthreads();
 
-    const int bits = 32 - __clz(E);  // of the numbers 0 .. E
-    for (int64_t r = 0; r < rounds; ++r) {
-        const int64_t i = mine + r * 64 + lane;
-        if (mine + r * 64 >= to) break;
-        const int32_t e = i < to ? expert_at(a, i) : -1;
-        const uint32_t key = e >= 0 ? (uint32_t)e : (uint32_t)E;
-        uint64_t same = ~uint64_t(0);
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t set = __ballot((key >> b) & 1u);
-            same &= ((key >> b) & 1u) ? set : ~set;
+    if constexpr (ROUNDS > 0) {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int64_t i = mine + r * 64;
+            if (r >= rounds || i >= to) continue;
+            const int32_t row = held[r] >= 0 ? my[held[r]] + at[r] : -1;
+            a.rows[i] = row;
+            if (row >= 0) a.slots[row] = (int32_t)i;
         }
-        const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-        int32_t row = -1;
-        if (e >= 0) {
-            row = __hip_atomic_load(&my[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) + rank;
+    } else {
+        for (int r = 0; r < rounds; ++r) {
+            const int64_t i = mine + (int64_t)r * 64;
+            if (i - lane >= to) break;
+            const int32_t row = place_in_wave(my, i < to ? expert_at(a, i) : -1, E, bits);
+            if (i < to) a.rows[i] = row;
+            if (row >= 0) a.slots[row] = (int32_t)i;
         }
-        // every lane has read before the last lane of each expert writes
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (e >= 0) {
-            if ((same >> lane) == 1)
-                __hip_atomic_store(&my[e], row + 1, __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_WORKGROUP);
-            a.slots[row] = (int32_t)i;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (i < to) a.rows[i] = row;
     }
+}
+
+template <int WAVES, int ROUNDS, bool MANY>
+void place(const OrderArgs &a, int blocks, hipStream_t s) {
+    hipLaunchKernelGGL((bmmc_expert_place_kernel<WAVES, ROUNDS, MANY>), dim3(blocks),
+                       dim3(WAVES * 64), sizeof(int32_t) * (size_t)a.num_experts * WAVES, s, a);
+}
+
+// Most choices of a lane that stay in registers.
+constexpr int kOrderHeld = 8;
+
+template <int WAVES, bool MANY> void place_by_rounds(const OrderArgs &a, int blocks, hipStream_t s) {
+    const int64_t rounds = (a.chunk + WAVES * 64 - 1) / (WAVES * 64);
+    if (rounds <= 1) return place<WAVES, 1, MANY>(a, blocks, s);
+    if (rounds <= kOrderHeld / 2) return place<WAVES, kOrderHeld / 2, MANY>(a, blocks, s);
+    if (rounds <= kOrderHeld) return place<WAVES, kOrderHeld, MANY>(a, blocks, s);
+    place<WAVES, 0, MANY>(a, blocks, s);
 }
 
 }  // namespace
 
 int launch_expert_order(const OrderArgs &a, int blocks, hipStream_t s) {
-    const int threads = a.num_experts > kOrderWideExperts ? kOrderThreads / 2 : kOrderThreads;
-    const size_t lds = sizeof(int32_t) * (size_t)a.num_experts * (threads / 64);
+    const bool wide = a.num_experts > kOrderWideExperts;
     if (blocks == 1) {
-        hipLaunchKernelGGL(bmmc_expert_place_kernel<false>, dim3(1), dim3(threads), lds, s, a);
+        if (a.n <= 4 * 64)
+            place<4, 1, false>(a, 1, s);
+        else if (wide)
+            place_by_rounds<8, false>(a, 1, s);
+        else
+            place_by_rounds<16, false>(a, 1, s);
     } else {
-        hipLaunchKernelGGL(bmmc_expert_count_kernel, dim3(blocks), dim3(kOrderThreads),
+        hipLaunchKernelGGL(bmmc_expert_count_kernel, dim3(blocks), dim3(kOrderMaxWaves * 64),
                            sizeof(int32_t) * (size_t)a.num_experts, s, a);
-        hipLaunchKernelGGL(bmmc_expert_place_kernel<true>, dim3(blocks), dim3(threads), lds, s, a);
+        if (wide)
+            place_by_rounds<8, true>(a, blocks, s);
+        else
+            place_by_rounds<16, true>(a, blocks, s);
     }
     return hipGetLastError() == hipSuccess ? BMMC_OK : BMMC_ERR_HIP;
 }

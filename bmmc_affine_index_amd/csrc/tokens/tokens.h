@@ -76,9 +76,11 @@ __host__ __device__ inline PagePlace page_place(const PageTable &t, int64_t toke
 // ---- experts ---------------------------------------------------------------
 
 // How bmmc_expert_order cuts its choices: one workgroup up to
-// kOrderOneBlockMax choices, else at most kOrderMaxBlocks workgroups of
-// `chunk` choices each, which first count into the workspace.
-constexpr int64_t kOrderOneBlockMax = 4096;
+// kOrderOneBlockMax choices, which it holds in registers (12297 choices took it
+// 17.6 us, reading them twice, and take two launches 9.6 us); else at most
+// kOrderMaxBlocks workgroups of `chunk` choices each, which first count into
+// the workspace.
+constexpr int64_t kOrderOneBlockMax = 8192;
 constexpr int64_t kOrderMaxBlocks = 256;
 constexpr int64_t kOrderMinChunk = 2048;
 

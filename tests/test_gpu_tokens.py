@@ -90,6 +90,20 @@ def test_order_of_skewed_choices(n):
     _check_order(torch.where(some < 8, some, 3).to(DEV), 8)
 
 
+@pytest.mark.parametrize("n,count", [
+    (256, 5), (257, 2048), (4096, 1024), (8192, 64), (8193, 64), (9000, 2048), (16384, 9),
+    (16384, 2048), (16385, 9), (30000, 1), (530000, 700), (4300000, 5), (4300000, 1500)])
+def test_order_of_many_lengths(n, count):
+    """One workgroup and several, choices held in registers and read twice."""
+    experts = torch.randint(-1, count + 1, (n, 1), generator=_gen(n + count))
+    _check_order(experts.to(torch.int32).to(DEV), count, align=3)
+
+
+def test_order_with_wide_padding():
+    experts = torch.randint(0, 7, (20000, 1), generator=_gen(9))
+    _check_order(experts.to(DEV), 7, align=5000)
+
+
 def test_order_drops_far_values():
     """Values that would be experts if their upper half were lost."""
     v = torch.tensor([1 << 32, (1 << 32) + 1, -(1 << 32), 2, (1 << 62) + 2, 0, -1, 3],
@@ -119,7 +133,8 @@ MOVES = [  # tokens, choices, experts, width, drop, align
     (9, 2, 4, 8, 0.5, 1), (33, 4, 16, 9, 0.2, 8), (64, 7, 9, 64, 0.0, 1), (65, 9, 17, 65, 0.1, 16),
     (130, 5, 8, 513, 0.5, 1), (257, 6, 60, 1001, 0.2, 32), (300, 8, 64, 2048, 0.0, 1),
     (128, 10, 40, 2880, 0.1, 1), (4099, 3, 8, 136, 0.3, 1), (5000, 8, 16, 40, 0.0, 64),
-    (70, 17, 32, 1100, 0.9, 16), (20, 4, 8, 512, 1.0, 1), (40, 25, 64, 4100, 0.0, 1)]
+    (70, 17, 32, 1100, 0.9, 16), (20, 4, 8, 512, 1.0, 1), (40, 25, 64, 4100, 0.0, 1),
+    (7, 8, 8, 256, 0.0, 1), (3, 3, 4, 700, 0.0, 1), (5, 8, 16, 1024, 0.2, 1), (11, 15, 16, 515, 0.1, 1)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
