@@ -6,9 +6,16 @@
 // turn, p f / 2 pi, is made and reduced to an eighth of a turn in 64 bits;
 // what is left goes through the Taylor series in 32.  One pair of cosine and
 // sine serves every head of the token: a workgroup makes those of its tokens
-// once, in LDS, and then streams the heads past them.
+// once, in LDS, and then streams the heads past them.  Its first heads are on
+// their way from memory while it does.
 //
-// Bound by memory: each element of the heads is read and written once.
+// Bound by memory: each element of the heads is read and written once.  A
+// workgroup takes as few tokens as keep its waves busy, usually one: what runs
+// at the same time then lies close together in memory (plain copies of 40 heads
+// of 256 bytes a token: 6.2 TB/s by workgroups of one token, 5.9 of two, 5.8 of
+// four, 5.4 of eight).
+#include <algorithm>
+
 #include "device.h"
 #include "tokens.h"
 
@@ -16,27 +23,30 @@ namespace bmmc {
 
 namespace {
 
-constexpr int kTurnThreads = 256;
-constexpr int kTurnWaves = kTurnThreads / 64;
+constexpr int kTurnWaves = 4;  // most waves a workgroup
+constexpr int kTurnThreads = 64 * kTurnWaves;
+constexpr int kTurnTokens = 4;   // most tokens a workgroup
 constexpr int kTurnPairs = 256;  // pairs of LDS a workgroup: BMMC_MAX_HEAD_DIM / 2
-constexpr int kTurnTokens = 8;   // most tokens a workgroup takes
 
 struct Turn {
     const void *positions, *freqs;
     const int32_t *axis_of_pair;
     int64_t axis_stride;
-    FastDiv by_pairs, by_units, by_heads;
+    FastDiv by_pairs, by_units;
     int32_t positions_are_64, freqs_are_64, axes, pairs;
-    int32_t units;  // vectors of pairs a head, at most 64
-    int32_t heads_a_wave;
+    int32_t units;         // vectors of pairs a head, at most 64
+    int32_t heads_a_wave;  // 64 / units
     float scale, sign;
 };
 
+// Heads to turn, and what of them is only copied.  A wave's task is
+// heads_a_wave heads of one token, or 64 vectors of what is copied of them.
 struct Heads {
     const void *in;
     void *out;
     int64_t in_batch, in_token, in_head, out_batch, out_token, out_head;
-    int32_t heads, in_place;
+    int32_t heads;
+    int32_t turns, copies;  // tasks a token
 };
 
 // Cosine and sine, times scale, of a whole number of turns' fraction.
@@ -62,19 +72,29 @@ __device__ __forceinline__ float2 cos_sin(double turns) {
 }
 
 // The workgroup's cosines and sines: cs[t * pairs + i] for its tokens t.
-__device__ __forceinline__ void make_turns(const Turn &r, int64_t token0, int tokens,
-                                           float2 *cs) {
+// `meanwhile` runs once, in every thread, after the first loads for them have
+// been issued.
+template <class F>
+__device__ __forceinline__ void make_turns(const Turn &r, int64_t token0, int tokens, float2 *cs,
+                                           F meanwhile) {
     constexpr double kInvTwoPi = 0.15915494309189535;
-    for (int n = threadIdx.x; n < tokens * r.pairs; n += kTurnThreads) {
+    bool first = true;
+    for (int n = threadIdx.x; first || n < tokens * r.pairs; n += blockDim.x) {
+        const bool on = n < tokens * r.pairs;
         const int t = (int)quotient(r.by_pairs, (uint32_t)n);
         const int i = n - t * r.pairs;
-        const int axis = r.axis_of_pair ? r.axis_of_pair[i] : 0;
-        const double f = r.freqs_are_64 ? static_cast<const double *>(r.freqs)[i]
-                                        : (double)static_cast<const float *>(r.freqs)[i];
-        double p = 0.0;
-        if (axis >= 0 && axis < r.axes)
-            p = (double)position_at(r.positions, r.positions_are_64,
-                                    axis * r.axis_stride + token0 + t);
+        double p = 0.0, f = 0.0;
+        if (on) {
+            const int axis = r.axis_of_pair ? r.axis_of_pair[i] : 0;
+            f = r.freqs_are_64 ? static_cast<const double *>(r.freqs)[i]
+                               : (double)static_cast<const float *>(r.freqs)[i];
+            if (axis >= 0 && axis < r.axes)
+                p = (double)position_at(r.positions, r.positions_are_64,
+                                        axis * r.axis_stride + token0 + t);
+        }
+        if (first) meanwhile();
+        first = false;
+        if (!on) break;
         const float2 u = cos_sin(p * (f * kInvTwoPi));
         cs[n] = make_float2(u.x * r.scale, u.y * r.scale * r.sign);
     }
@@ -110,116 +130,152 @@ __device__ __forceinline__ void turn_vector(const dev::Vec<T, N> &a, const dev::
     }
 }
 
-// Where the two vectors of pairs [i, i + N) of a head start.
-template <int N, bool PAIRED> __device__ __forceinline__ int second_at(int i, int pairs) {
-    return PAIRED ? 2 * i + N : pairs + i;
-}
-template <bool PAIRED> __device__ __forceinline__ int first_at(int i) {
-    return PAIRED ? 2 * i : i;
-}
-
 // A lane's head and first pair among a wave's heads_a_wave heads.  All
 // vectors of a head are one wave's, so that the last, which overlaps the one
 // before where the pairs are not whole vectors, is read before that one is
 // written even when the head is turned in place.
 struct Lane {
-    int head, pair;
+    int head, at;  // at: its first vector; the second is `gap` elements on
     bool on;
 };
-template <int N> __device__ __forceinline__ Lane lane_of(const Turn &r) {
+template <int N, bool PAIRED> __device__ __forceinline__ Lane lane_of(const Turn &r) {
     const int lane = threadIdx.x & 63;
     const int g = (int)quotient(r.by_units, (uint32_t)lane);
-    const int j = lane - g * r.units;
-    return Lane{g, min(j * N, r.pairs - N), g < r.heads_a_wave};
+    const int pair = min((lane - g * r.units) * N, r.pairs - N);
+    return Lane{g, PAIRED ? 2 * pair : pair, g < r.heads_a_wave};
+}
+template <int N, bool PAIRED> __device__ __forceinline__ int gap_of(const Turn &r) {
+    return PAIRED ? N : r.pairs;
+}
+template <bool PAIRED> __device__ __forceinline__ int pair_of(const Lane &l) {
+    return PAIRED ? l.at / 2 : l.at;
+}
+
+// `len` elements of each head that are moved as they are, in whole vectors
+// (the last may overlap the one before; both write the same) or, of less than
+// a vector, single elements by one lane.
+struct Part {
+    FastDiv by_units;
+    int32_t from, len, units;  // of a head; units: vectors
+};
+template <typename T> Part part_of(int from, int len) {
+    constexpr int N = dev::Lanes<T>::N;
+    const int units = (len + N - 1) / N;
+    return Part{fast_div((uint32_t)(units ? units : 1)), from, len, units};
+}
+int copies_of(const Part &p, int64_t heads) { return (int)((heads * p.units + 63) / 64); }
+
+// Task `task` of a part of one token's heads: put(h, element, vector) moves
+// one vector or element of head h.
+template <int N> struct Count {
+    constexpr operator int() const { return N; }
+};
+template <typename T, class F>
+__device__ __forceinline__ void copy_task(const Part &p, int heads, int task, const T *in,
+                                          int64_t in_head, F put) {
+    constexpr int N = dev::Lanes<T>::N;
+    const int u = task * 64 + (threadIdx.x & 63);
+    if (u >= heads * p.units) return;
+    const int h = (int)quotient(p.by_units, (uint32_t)u);
+    in += h * in_head;
+    if (p.len >= N) {
+        const int at = p.from + min((u - h * p.units) * N, p.len - N);
+        put(h, at, dev::load<T, N>(in + at));
+    } else {
+        for (int at = p.from; at < p.from + p.len; ++at) put(h, at, dev::load<T, 1>(in + at));
+    }
 }
 
 struct TurnHeads {
     Heads x[2];
+    Part rest;
     int64_t tokens;  // of all batch entries
-    FastDiv by_tokens;
-    FastDiv by_rest;
+    FastDiv by_tokens, by_tasks;
     int32_t batch, tokens_a_block;
-    int32_t rest, rest_units;  // elements past the pairs, their vectors a head; 0 if all is in place
 };
 
-__device__ __forceinline__ void split_token(const FastDiv &by, int batch, int64_t token,
-                                            int64_t *b, int64_t *t) {
-    *b = batch > 1 ? quotient(by, (uint32_t)token) : 0;
-    *t = token - *b * by.d;
-}
-
-// Part j of `len` elements that are moved as they are: move(n, at) moves the n
-// elements at `at`, a whole vector (the last may overlap the one before; both
-// write the same) or, of less than a vector, single elements by one lane.
-template <int N> struct Count {
-    constexpr operator int() const { return N; }
+// This wave's first task and the waves of the workgroups that share its tokens.
+struct Waves {
+    int first, count;
 };
-template <typename T, class F> __device__ __forceinline__ void copy_part(int len, int j, F move) {
-    constexpr int N = dev::Lanes<T>::N;
-    if (len >= N)
-        move(Count<N>(), min(j * N, len - N));
-    else
-        for (int at = 0; at < len; ++at) move(Count<1>(), at);
-}
-template <typename T> int copy_parts(int len) {
-    constexpr int N = dev::Lanes<T>::N;
-    return (len + N - 1) / N;
+__device__ __forceinline__ Waves waves_of() {
+    const int n = blockDim.x >> 6;
+    return Waves{(int)(blockIdx.y * n + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)),
+                 (int)(gridDim.y * n)};
 }
 
+// A task's numbers are the same in all lanes, and so are its token's place in
+// memory and in the cache: they are made in scalar registers, and a lane adds
+// its own offset.
 template <typename T, int N, bool PAIRED>
 __global__ void __launch_bounds__(kTurnThreads)
     bmmc_rotary_kernel(const TurnHeads a, const Turn r, int64_t block0) {
     __shared__ float2 cs[kTurnPairs];
     const int64_t token0 = (block0 + blockIdx.x) * a.tokens_a_block;
     const int tokens = (int)min((int64_t)a.tokens_a_block, a.tokens - token0);
-    make_turns(r, token0, tokens, cs);
+    const int per = (int)a.by_tasks.d, tasks = tokens * per;
+    const int turns0 = a.x[0].turns, turns = turns0 + a.x[1].turns;
+    const Waves waves = waves_of();
+    const Lane l = lane_of<N, PAIRED>(r);
+    const int gap = gap_of<N, PAIRED>(r);
+    const int64_t lane_in[2] = {l.head * a.x[0].in_head + l.at, l.head * a.x[1].in_head + l.at};
+    const int64_t lane_out[2] = {l.head * a.x[0].out_head + l.at, l.head * a.x[1].out_head + l.at};
+
+    struct Task {
+        int token, number;  // of the workgroup's tokens, of its token's tasks
+        int64_t in_batch, in_token;
+    };
+    const auto locate = [&](int task) {
+        const int t = (int)quotient(a.by_tasks, (uint32_t)task);
+        const int64_t tok = token0 + t;
+        const int64_t b = a.batch > 1 ? quotient(a.by_tokens, (uint32_t)tok) : 0;
+        return Task{t, task - t * per, b, tok - b * a.by_tokens.d};
+    };
+    dev::Vec<T, N> va, vb;
+    const auto fetch = [&](int task) {
+        const Task k = locate(task);
+        if (k.number >= turns) return;
+        const bool second = k.number >= turns0;
+        const Heads &x = a.x[second];
+        const int head = (k.number - (second ? turns0 : 0)) * r.heads_a_wave;
+        if (!l.on || head + l.head >= x.heads) return;
+        const T *in = static_cast<const T *>(x.in) + k.in_batch * x.in_batch +
+                      k.in_token * x.in_token + head * x.in_head + lane_in[second];
+        va = dev::load<T, N>(in);
+        vb = dev::load<T, N>(in + gap);
+    };
+    make_turns(r, token0, tokens, cs, [&] {
+        if (waves.first < tasks) fetch(waves.first);
+    });
     __syncthreads();
-
-    const int wave = blockIdx.y * kTurnWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = gridDim.y * kTurnWaves;
-    const int heads = (int)r.by_heads.d;
-    const Lane l = lane_of<N>(r);
-    for (int i0 = wave * r.heads_a_wave; i0 < tokens * heads; i0 += waves * r.heads_a_wave) {
-        const int i = i0 + l.head;
-        if (!l.on || i >= tokens * heads) continue;
-        const int t = (int)quotient(r.by_heads, (uint32_t)i);
-        int h = i - t * heads;
-        const bool second = h >= a.x[0].heads;
-        const Heads &x = a.x[second ? 1 : 0];
-        h -= second ? a.x[0].heads : 0;
-        int64_t b, tok;
-        split_token(a.by_tokens, a.batch, token0 + t, &b, &tok);
-        const T *in = static_cast<const T *>(x.in) + b * x.in_batch + tok * x.in_token +
-                      h * x.in_head;
-        T *out = static_cast<T *>(x.out) + b * x.out_batch + tok * x.out_token + h * x.out_head;
-        const int at = first_at<PAIRED>(l.pair), to = second_at<N, PAIRED>(l.pair, r.pairs);
-        const dev::Vec<T, N> va = dev::load<T, N>(in + at), vb = dev::load<T, N>(in + to);
-        dev::Floats<N> fx, fy;
-        turn_vector<T, N, PAIRED>(va, vb, cs + t * r.pairs + l.pair, fx, fy);
-        dev::store<T, N>(out + at, dev::narrow<T, N>(fx));
-        dev::store<T, N>(out + to, dev::narrow<T, N>(fy));
-    }
-
-    // elements past the pairs
-    if (!a.rest) return;
-    const int n = tokens * heads * a.rest_units;
-    for (int i = blockIdx.y * kTurnThreads + threadIdx.x; i < n;
-         i += gridDim.y * kTurnThreads) {
-        const int th = (int)quotient(a.by_rest, (uint32_t)i);
-        const int t = (int)quotient(r.by_heads, (uint32_t)th);
-        int h = th - t * heads;
-        const bool second = h >= a.x[0].heads;
-        const Heads &x = a.x[second ? 1 : 0];
-        if (x.in_place) continue;
-        h -= second ? a.x[0].heads : 0;
-        int64_t b, tok;
-        split_token(a.by_tokens, a.batch, token0 + t, &b, &tok);
-        const T *in = static_cast<const T *>(x.in) + b * x.in_batch + tok * x.in_token +
-                      h * x.in_head + 2 * r.pairs;
-        T *out = static_cast<T *>(x.out) + b * x.out_batch + tok * x.out_token + h * x.out_head +
-                 2 * r.pairs;
-        copy_part<T>(a.rest, i - th * a.rest_units,
-                     [&](auto n, int at) { dev::store<T, n>(out + at, dev::load<T, n>(in + at)); });
+    for (int task = waves.first; task < tasks; task += waves.count) {
+        const Task k = locate(task);
+        const dev::Vec<T, N> a0 = va, b0 = vb;
+        // the next heads are others: what is read here is not written below
+        if (task + waves.count < tasks) fetch(task + waves.count);
+        if (k.number < turns) {
+            const bool second = k.number >= turns0;
+            const Heads &x = a.x[second];
+            const int head = (k.number - (second ? turns0 : 0)) * r.heads_a_wave;
+            if (!l.on || head + l.head >= x.heads) continue;
+            T *out = static_cast<T *>(x.out) + k.in_batch * x.out_batch +
+                     k.in_token * x.out_token + head * x.out_head + lane_out[second];
+            dev::Floats<N> fx, fy;
+            turn_vector<T, N, PAIRED>(a0, b0, cs + k.token * r.pairs + pair_of<PAIRED>(l), fx, fy);
+            dev::store<T, N>(out, dev::narrow<T, N>(fx));
+            dev::store<T, N>(out + gap, dev::narrow<T, N>(fy));
+        } else {
+            const int c = k.number - turns;
+            const bool second = c >= a.x[0].copies;
+            const Heads &x = a.x[second];
+            T *out = static_cast<T *>(x.out) + k.in_batch * x.out_batch + k.in_token * x.out_token;
+            copy_task<T>(a.rest, x.heads, c - (second ? a.x[0].copies : 0),
+                         static_cast<const T *>(x.in) + k.in_batch * x.in_batch +
+                             k.in_token * x.in_token,
+                         x.in_head, [&](int h, int at, auto v) {
+                             dev::store(out + h * x.out_head + at, v);
+                         });
+        }
     }
 }
 
@@ -231,10 +287,10 @@ struct Append {
     const float *k_scale, *v_scale;
     int64_t k_page, k_place, k_head, v_page, v_place, v_head;
     PageTable where;
+    Part rest, values;
     int64_t tokens;
-    FastDiv by_rest, by_v, by_v_heads;
-    int32_t rest, rest_units, v_dim, v_units, k_scale_stride, v_scale_stride;
-    int32_t tokens_a_block;
+    FastDiv by_tasks;
+    int32_t k_scale_stride, v_scale_stride, tokens_a_block;
 };
 
 // Stored 8-bit values: clamped, NaN kept, rounded to nearest, ties to even.
@@ -271,7 +327,7 @@ __device__ __forceinline__ void put(uint8_t *cache, int64_t at, const dev::Float
     else
         dev::store<T, N>(reinterpret_cast<T *>(cache) + at, dev::narrow<T, N>(x));
 }
-template <typename T, int N, bool E4M3>
+template <bool E4M3, typename T, int N>
 __device__ __forceinline__ void put_as_is(uint8_t *cache, int64_t at, const dev::Vec<T, N> &x,
                                           const float *scale, int64_t which) {
     if constexpr (E4M3)
@@ -280,116 +336,130 @@ __device__ __forceinline__ void put_as_is(uint8_t *cache, int64_t at, const dev:
         dev::store<T, N>(reinterpret_cast<T *>(cache) + at, x);
 }
 
+// A token's tasks: q's and k's heads to turn, what of q, of k and of v is copied.
 template <typename T, int N, bool PAIRED, bool E4M3>
 __global__ void __launch_bounds__(kTurnThreads)
     bmmc_cache_append_kernel(const Append a, const Turn r, int64_t block0) {
     __shared__ float2 cs[kTurnPairs];
     __shared__ PagePlace places[kTurnTokens];
+    constexpr int VN = dev::Lanes<T>::N;
     const int64_t token0 = (block0 + blockIdx.x) * a.tokens_a_block;
     const int tokens = (int)min((int64_t)a.tokens_a_block, a.tokens - token0);
-    if ((int)threadIdx.x < tokens) places[threadIdx.x] = page_place(a.where, token0 + threadIdx.x);
-    if (r.pairs) make_turns(r, token0, tokens, cs);
-    __syncthreads();
+    const int per = (int)a.by_tasks.d, tasks = tokens * per;
+    const int turns = a.q.turns + a.k.turns, values = turns + a.q.copies + a.k.copies;
+    const Waves waves = waves_of();
+    const Lane l = r.pairs ? lane_of<N, PAIRED>(r) : Lane{0, 0, false};
+    const int gap = gap_of<N, PAIRED>(r);
+    const int64_t q_in = l.head * a.q.in_head + l.at, q_out = l.head * a.q.out_head + l.at;
+    const int64_t k_in = l.head * a.k.in_head + l.at, k_out = l.head * a.k_head + l.at;
 
-    // A wave's tasks: heads_a_wave heads of q and k to turn, or 64 vectors of v.
-    const int wave = blockIdx.y * kTurnWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = gridDim.y * kTurnWaves;
-    const int heads = (int)r.by_heads.d;
-    const int turns = r.pairs ? (tokens * heads + r.heads_a_wave - 1) / r.heads_a_wave : 0;
-    const int vectors = tokens * a.v.heads * a.v_units;
-    const int copies = (vectors + 63) / 64;
-    const Lane l = r.pairs ? lane_of<N>(r) : Lane{0, 0, false};
-    for (int task = wave; task < turns + copies; task += waves) {
-        if (task < turns) {
-            const int i = task * r.heads_a_wave + l.head;
-            if (!l.on || i >= tokens * heads) continue;
-            const int t = (int)quotient(r.by_heads, (uint32_t)i);
-            const int h = i - t * heads;
-            const int at = first_at<PAIRED>(l.pair), to = second_at<N, PAIRED>(l.pair, r.pairs);
-            const float2 *u = cs + t * r.pairs + l.pair;
-            const int64_t tok = token0 + t;
-            dev::Floats<N> x, y;
-            if (h < a.q.heads) {
-                const T *in = static_cast<const T *>(a.q.in) + tok * a.q.in_token + h * a.q.in_head;
-                T *out = static_cast<T *>(a.q.out) + tok * a.q.out_token + h * a.q.out_head;
-                turn_vector<T, N, PAIRED>(dev::load<T, N>(in + at), dev::load<T, N>(in + to), u,
-                                          x, y);
-                dev::store<T, N>(out + at, dev::narrow<T, N>(x));
-                dev::store<T, N>(out + to, dev::narrow<T, N>(y));
-            } else {
-                const int kh = h - a.q.heads;
-                const PagePlace p = places[t];
-                if (p.page < 0) continue;
-                const T *in =
-                    static_cast<const T *>(a.k.in) + tok * a.k.in_token + kh * a.k.in_head;
-                const int64_t base = p.page * a.k_page + p.place * a.k_place + kh * a.k_head;
-                turn_vector<T, N, PAIRED>(dev::load<T, N>(in + at), dev::load<T, N>(in + to), u,
-                                          x, y);
-                put<T, N, E4M3>(a.k_cache, base + at, x, a.k_scale, kh * a.k_scale_stride);
-                put<T, N, E4M3>(a.k_cache, base + to, y, a.k_scale, kh * a.k_scale_stride);
-            }
-        } else {
-            const int i = (task - turns) * 64 + (threadIdx.x & 63);
-            if (i >= vectors) continue;
-            const int th = (int)quotient(a.by_v, (uint32_t)i);
-            const int t = (int)quotient(a.by_v_heads, (uint32_t)th);
-            const int h = th - t * a.v.heads;
-            const PagePlace p = places[t];
-            if (p.page < 0) continue;
-            const T *in = static_cast<const T *>(a.v.in) + (token0 + t) * a.v.in_token +
-                          h * a.v.in_head;
-            const int64_t base = p.page * a.v_page + p.place * a.v_place + h * a.v_head;
-            copy_part<T>(a.v_dim, i - th * a.v_units, [&](auto n, int at) {
-                put_as_is<T, n, E4M3>(a.v_cache, base + at, dev::load<T, n>(in + at), a.v_scale,
-                                      h * a.v_scale_stride);
-            });
+    const auto source = [](const Heads &x, int64_t token) {
+        return static_cast<const T *>(x.in) + token * x.in_token;
+    };
+    // This lane's vector of v in task `number`.
+    struct Value {
+        int head, at;
+        bool on;
+    };
+    const auto value = [&](int number) {
+        const int u = (number - values) * 64 + (threadIdx.x & 63);
+        const int h = (int)quotient(a.values.by_units, (uint32_t)u);
+        return Value{h, min((u - h * a.values.units) * VN, a.values.len - VN),
+                     u < a.v.heads * a.values.units};
+    };
+    const bool whole = a.values.len >= VN;
+    dev::Vec<T, N> va, vb;  // a turn's
+    dev::Vec<T, VN> vc;     // of v
+    const auto fetch = [&](int task) {
+        const int t = (int)quotient(a.by_tasks, (uint32_t)task), number = task - t * per;
+        if (number >= values && whole) {
+            const Value f = value(number);
+            if (f.on)
+                vc = dev::load<T, VN>(source(a.v, token0 + t) + f.head * a.v.in_head + f.at);
         }
-    }
-
-    // elements of q and k past the pairs
-    if (!a.rest) return;
-    const int n = tokens * heads * a.rest_units;
-    for (int i = blockIdx.y * kTurnThreads + threadIdx.x; i < n;
-         i += gridDim.y * kTurnThreads) {
-        const int th = (int)quotient(a.by_rest, (uint32_t)i);
-        const int j = i - th * a.rest_units;
-        const int t = (int)quotient(r.by_heads, (uint32_t)th);
-        const int h = th - t * heads;
-        const int64_t tok = token0 + t;
-        if (h < a.q.heads) {
-            if (a.q.in_place) continue;
-            const T *in = static_cast<const T *>(a.q.in) + tok * a.q.in_token +
-                          h * a.q.in_head + 2 * r.pairs;
-            T *out = static_cast<T *>(a.q.out) + tok * a.q.out_token + h * a.q.out_head +
-                     2 * r.pairs;
-            copy_part<T>(a.rest, j, [&](auto n, int at) {
-                dev::store<T, n>(out + at, dev::load<T, n>(in + at));
-            });
+        if (number >= turns) return;
+        const bool key = number >= a.q.turns;
+        const Heads &x = key ? a.k : a.q;
+        const int head = (number - (key ? a.q.turns : 0)) * r.heads_a_wave;
+        if (!l.on || head + l.head >= x.heads) return;
+        const T *in = source(x, token0 + t) + head * x.in_head + (key ? k_in : q_in);
+        va = dev::load<T, N>(in);
+        vb = dev::load<T, N>(in + gap);
+    };
+    const auto copy = [&](int64_t token, const PagePlace &home, int number) {
+        if (number < a.q.copies) {
+            T *out = static_cast<T *>(a.q.out) + token * a.q.out_token;
+            copy_task<T>(a.rest, a.q.heads, number, source(a.q, token), a.q.in_head,
+                         [&](int h, int at, auto v) { dev::store(out + h * a.q.out_head + at, v); });
+            return;
+        }
+        number -= a.q.copies;
+        if (home.page < 0) return;
+        const bool key = number < a.k.copies;
+        const int64_t base = key ? home.page * a.k_page + home.place * a.k_place
+                                 : home.page * a.v_page + home.place * a.v_place;
+        const Heads &x = key ? a.k : a.v;
+        copy_task<T>(key ? a.rest : a.values, x.heads, number - (key ? 0 : a.k.copies),
+                     source(x, token), x.in_head, [&](int h, int at, auto v) {
+                         put_as_is<E4M3>(key ? a.k_cache : a.v_cache,
+                                         base + h * (key ? a.k_head : a.v_head) + at, v,
+                                         key ? a.k_scale : a.v_scale,
+                                         h * (key ? a.k_scale_stride : a.v_scale_stride));
+                     });
+    };
+    // the last wave looks the places up while the first make cosines
+    const int looker = (int)threadIdx.x - ((int)blockDim.x - 64);
+    if (looker >= 0 && looker < tokens) places[looker] = page_place(a.where, token0 + looker);
+    make_turns(r, token0, r.pairs ? tokens : 0, cs, [&] {
+        if (waves.first < tasks) fetch(waves.first);
+    });
+    __syncthreads();
+    for (int task = waves.first; task < tasks; task += waves.count) {
+        const int t = (int)quotient(a.by_tasks, (uint32_t)task), number = task - t * per;
+        const int64_t token = token0 + t;
+        const dev::Vec<T, N> a0 = va, b0 = vb;
+        const dev::Vec<T, VN> c0 = vc;
+        // the next heads are others: what is read here is not written below
+        if (task + waves.count < tasks) fetch(task + waves.count);
+        const PagePlace home = places[t];
+        if (number >= values && whole) {
+            const Value f = value(number);
+            if (home.page < 0 || !f.on) continue;
+            put_as_is<E4M3>(a.v_cache,
+                            home.page * a.v_page + home.place * a.v_place + f.head * a.v_head + f.at,
+                            c0, a.v_scale, f.head * a.v_scale_stride);
+            continue;
+        }
+        if (number >= turns) {
+            copy(token, home, number - turns);
+            continue;
+        }
+        const bool key = number >= a.q.turns;
+        const int head = (number - (key ? a.q.turns : 0)) * r.heads_a_wave;
+        const bool on = l.on && head + l.head < (key ? a.k : a.q).heads;
+        dev::Floats<N> x, y;
+        turn_vector<T, N, PAIRED>(a0, b0, cs + t * r.pairs + pair_of<PAIRED>(l), x, y);
+        if (!key) {
+            T *out = static_cast<T *>(a.q.out) + token * a.q.out_token + head * a.q.out_head + q_out;
+            if (!on) continue;
+            dev::store<T, N>(out, dev::narrow<T, N>(x));
+            dev::store<T, N>(out + gap, dev::narrow<T, N>(y));
         } else {
-            const int kh = h - a.q.heads;
-            const PagePlace p = places[t];
-            if (p.page < 0) continue;
-            const T *in = static_cast<const T *>(a.k.in) + tok * a.k.in_token +
-                          kh * a.k.in_head + 2 * r.pairs;
-            const int64_t base =
-                p.page * a.k_page + p.place * a.k_place + kh * a.k_head + 2 * r.pairs;
-            copy_part<T>(a.rest, j, [&](auto n, int at) {
-                put_as_is<T, n, E4M3>(a.k_cache, base + at, dev::load<T, n>(in + at), a.k_scale,
-                                      kh * a.k_scale_stride);
-            });
+            if (home.page < 0 || !on) continue;
+            const int64_t at = home.page * a.k_page + home.place * a.k_place + head * a.k_head + k_out;
+            const int64_t which = (head + l.head) * a.k_scale_stride;
+            put<T, N, E4M3>(a.k_cache, at, x, a.k_scale, which);
+            put<T, N, E4M3>(a.k_cache, at + gap, y, a.k_scale, which);
         }
     }
 }
 
 // ---- launches --------------------------------------------------------------------
 
-template <int N> Turn turn_of(const bmmc_rotation &x, int heads) {
+template <int N> Turn turn_of(const bmmc_rotation &x) {
     Turn r{};
-    r.by_heads = fast_div((uint32_t)(heads > 0 ? heads : 1));
-    if (x.pairs == 0) {
-        r.by_pairs = r.by_units = fast_div(1);
-        return r;
-    }
+    r.by_pairs = r.by_units = fast_div(1);
+    if (x.pairs == 0) return r;
     r.positions = x.positions;
     r.freqs = x.freqs;
     r.axis_of_pair = x.axis_of_pair;
@@ -407,62 +477,75 @@ template <int N> Turn turn_of(const bmmc_rotation &x, int heads) {
     return r;
 }
 
-Heads heads_of(const bmmc_heads &x) {
+// `rest`: what past the pairs is copied, unless the heads stay where they are.
+Heads heads_of(const bmmc_heads &x, const Turn &r, const Part &rest) {
+    const int32_t heads = (int32_t)x.heads;
     return Heads{x.in, x.out, x.in_batch, x.in_token, x.in_head, x.out_batch, x.out_token,
-                 x.out_head, (int32_t)x.heads,
-                 x.in == x.out};
+                 x.out_head, heads,
+                 r.pairs ? (heads + r.heads_a_wave - 1) / r.heads_a_wave : 0,
+                 x.in == x.out ? 0 : copies_of(rest, heads)};
 }
 
-// Tokens a workgroup takes, and workgroups that share a block's tasks: about
-// as many tokens as LDS holds where that leaves at least four workgroups for
-// each of the 256 compute units, else one token, its heads over several
-// workgroups up to that many.
+// How the tokens are cut: a workgroup takes one token, or as many as its four
+// waves have one task each for and LDS holds cosines for, if that leaves four
+// workgroups for each of the 256 compute units.  32768 tokens of 40 heads of 256
+// bytes (5 tasks): 109 us with one token and four waves, 113 with two tokens,
+// 117 with four; 133 with eight waves, which wait for one another's cosines.
+// Few tokens have their tasks spread over several workgroups, up to as many.
 constexpr int64_t kTurnBlocks = 1024;
 
-int tokens_a_block(int64_t tokens, int pairs) {
-    int n = pairs ? kTurnPairs / pairs : 4;
-    n = n > kTurnTokens ? kTurnTokens : n < 1 ? 1 : n;
-    return tokens / n >= kTurnBlocks ? n : 1;
-}
+struct TurnCut {
+    int tokens_a_block, waves;
+    int64_t blocks;
+    uint32_t shares;
+};
 
-uint32_t shares(int64_t blocks, int64_t tasks) {
-    int64_t most = (tasks + kTurnWaves - 1) / kTurnWaves, want = kTurnBlocks / blocks;
-    if (most > want) most = want;
-    return most < 1 ? 1 : (uint32_t)most;
+TurnCut turn_cut(int64_t tokens, int pairs, int64_t tasks) {
+    int64_t n = std::min<int64_t>(kTurnTokens, kTurnWaves / tasks);
+    if (pairs) n = std::min<int64_t>(n, kTurnPairs / pairs);
+    if (n < 1 || tokens / n < kTurnBlocks) n = 1;
+    TurnCut c;
+    c.tokens_a_block = (int)n;
+    c.waves = (int)std::min<int64_t>(n * tasks, kTurnWaves);
+    c.blocks = (tokens + n - 1) / n;
+    const int64_t most = (n * tasks + c.waves - 1) / c.waves, want = kTurnBlocks / c.blocks;
+    c.shares = (uint32_t)std::max<int64_t>(std::min(most, want), 1);
+    return c;
 }
 
 template <typename T, int N, bool PAIRED>
 int rotary_n(const HeadsArgs &h, const bmmc_rotation &x, hipStream_t s) {
+    const Turn r = turn_of<N>(x);
     TurnHeads a{};
-    int64_t heads = 0;
-    bool place = true;
+    a.rest = part_of<T>(2 * x.pairs, h.head_dim - 2 * x.pairs);
+    int64_t tasks = 0;
     for (int i = 0; i < h.count; ++i) {
-        a.x[i] = heads_of(h.x[i]);
-        heads += h.x[i].heads;
-        place &= a.x[i].in_place != 0;
+        a.x[i] = heads_of(h.x[i], r, a.rest);
+        tasks += a.x[i].turns + a.x[i].copies;
     }
     a.tokens = h.batch * h.tokens;
     a.batch = (int32_t)h.batch;
     a.by_tokens = fast_div((uint32_t)h.tokens);
-    a.rest = place ? 0 : h.head_dim - 2 * x.pairs;
-    a.rest_units = copy_parts<T>(a.rest);
-    a.by_rest = fast_div((uint32_t)(a.rest ? a.rest_units : 1));
-    a.tokens_a_block = tokens_a_block(a.tokens, x.pairs);
-    const Turn r = turn_of<N>(x, (int)heads);
-    const int64_t blocks = (a.tokens + a.tokens_a_block - 1) / a.tokens_a_block;
-    const int64_t tasks = (a.tokens_a_block * heads + r.heads_a_wave - 1) / r.heads_a_wave;
-    return in_launches(blocks, kTurnThreads, [&](uint32_t nb, int64_t b0) {
-        hipLaunchKernelGGL((bmmc_rotary_kernel<T, N, PAIRED>), dim3(nb, shares(blocks, tasks)),
-                           dim3(kTurnThreads), 0, s, a, r, b0);
+    a.by_tasks = fast_div((uint32_t)tasks);
+    const TurnCut cut = turn_cut(a.tokens, x.pairs, tasks);
+    a.tokens_a_block = cut.tokens_a_block;
+    return in_launches(cut.blocks, kTurnThreads, [&](uint32_t nb, int64_t b0) {
+        hipLaunchKernelGGL((bmmc_rotary_kernel<T, N, PAIRED>), dim3(nb, cut.shares),
+                           dim3(64 * cut.waves), 0, s, a, r, b0);
     });
 }
 
 template <typename T, int N, bool PAIRED, bool E4M3>
 int append_n(const AppendArgs &h, hipStream_t s) {
+    const Turn r = turn_of<N>(h.rotation);
     Append a{};
-    a.q = heads_of(h.q);
-    a.k = heads_of(h.k);
-    a.v = heads_of(h.v);
+    a.rest = part_of<T>(2 * r.pairs, h.k_dim - 2 * r.pairs);
+    a.values = part_of<T>(0, h.v_dim);
+    if (h.q.heads) a.q = heads_of(h.q, r, a.rest);
+    a.k = heads_of(h.k, r, a.rest);
+    a.v = heads_of(h.v, Turn{}, a.values);
+    a.k.copies = copies_of(a.rest, h.k.heads);  // k and v have no out of their own
+    a.v.copies = copies_of(a.values, h.v.heads);
     a.k_cache = static_cast<uint8_t *>(h.k_cache.data);
     a.v_cache = static_cast<uint8_t *>(h.v_cache.data);
     a.k_scale = h.k_cache.scale;
@@ -477,24 +560,13 @@ int append_n(const AppendArgs &h, hipStream_t s) {
     a.v_scale_stride = h.v_cache.scale_stride;
     a.where = h.where;
     a.tokens = h.tokens;
-    a.v_dim = h.v_dim;
-    a.v_units = copy_parts<T>(h.v_dim);
-    a.rest = h.k_dim - 2 * h.rotation.pairs;
-    a.rest_units = copy_parts<T>(a.rest);
-    a.by_rest = fast_div((uint32_t)(a.rest ? a.rest_units : 1));
-    a.by_v = fast_div((uint32_t)a.v_units);
-    a.by_v_heads = fast_div((uint32_t)h.v.heads);
-    a.tokens_a_block = tokens_a_block(a.tokens, h.rotation.pairs);
-    const int64_t heads = h.q.heads + h.k.heads;
-    const Turn r = turn_of<N>(h.rotation, (int)heads);
-    const int64_t blocks = (a.tokens + a.tokens_a_block - 1) / a.tokens_a_block;
-    const int64_t turns =
-        r.pairs ? (a.tokens_a_block * heads + r.heads_a_wave - 1) / r.heads_a_wave : 0;
-    const int64_t copies = ((int64_t)a.tokens_a_block * h.v.heads * a.v_units + 63) / 64;
-    return in_launches(blocks, kTurnThreads, [&](uint32_t nb, int64_t b0) {
-        hipLaunchKernelGGL((bmmc_cache_append_kernel<T, N, PAIRED, E4M3>),
-                           dim3(nb, shares(blocks, turns + copies)), dim3(kTurnThreads), 0, s, a,
-                           r, b0);
+    const int64_t tasks = (int64_t)a.q.turns + a.q.copies + a.k.turns + a.k.copies + a.v.copies;
+    a.by_tasks = fast_div((uint32_t)tasks);
+    const TurnCut cut = turn_cut(a.tokens, r.pairs, tasks);
+    a.tokens_a_block = cut.tokens_a_block;
+    return in_launches(cut.blocks, kTurnThreads, [&](uint32_t nb, int64_t b0) {
+        hipLaunchKernelGGL((bmmc_cache_append_kernel<T, N, PAIRED, E4M3>), dim3(nb, cut.shares),
+                           dim3(64 * cut.waves), 0, s, a, r, b0);
     });
 }
 
