@@ -21,8 +21,11 @@ namespace {
 constexpr int kGatherThreads = 256;
 constexpr int kCombineThreads = 128;
 constexpr int kBackwardThreads = 256;
-// Rows of the order that one wave looks through for padding.
-constexpr int kPadRows = 16;
+// Rows of the order that one wave looks through for padding: where there is
+// much, few waves would take long over it; where there is none, many cost time
+// (131072 rows without any: 2% of the backward pass with 4 rows a wave, nothing
+// to be seen with 8).
+constexpr int kPadRows = 8;
 
 // This lane's token and first element; at < 0 without any.  A row that is not
 // whole vectors ends in one that overlaps the vector before it: both write the
@@ -92,30 +95,35 @@ __device__ __forceinline__ void zero_padding(const MoveArgs &a, int64_t wave) {
         const int k = __builtin_ctzll(todo);
         todo &= todo - 1;
         T *out = static_cast<T *>(a.out) + (r0 + k) * a.out_stride;
-        for (int64_t at = (int64_t)lane * N; at < a.dim; at += 64 * N)
-            dev::store<T, N>(out + min(at, a.dim - N), none);
+        dev::by_hint(a.whole_lines, [&](auto nt) {
+            for (int64_t at = (int64_t)lane * N; at < a.dim; at += 64 * N)
+                dev::store<T, N, nt.value>(out + min(at, a.dim - N), none);
+        });
     }
 }
 
 template <typename T, int N, bool WAVE>
 __global__ void __launch_bounds__(kGatherThreads)
-    bmmc_expert_gather_kernel(const MoveArgs a, const Cut c, uint32_t block0) {
+    bmmc_expert_gather_kernel(const MoveArgs a, const Cut c, uint32_t pads, uint32_t block0) {
     const uint32_t block = block0 + blockIdx.x;
-    if (block >= c.parts) {
-        zero_padding<T, N>(
-            a, (int64_t)(block - c.parts) * (kGatherThreads / 64) + (threadIdx.x >> 6));
+    if (block < pads) {
+        zero_padding<T, N>(a, (int64_t)block * (kGatherThreads / 64) + (threadIdx.x >> 6));
         return;
     }
-    const Place p = locate<kGatherThreads, WAVE, N>(c, a.tokens, a.dim, block);
+    const Place p = locate<kGatherThreads, WAVE, N>(c, a.tokens, a.dim, block - pads);
     if (p.at < 0) return;
+    // a layer's input, which the layer before has just written: through the
+    // caches (16384 tokens of 8 choices, 4 KiB a row: 102 us, 114 streamed)
     const dev::Vec<T, N> v =
-        dev::load<T, N>(static_cast<const T *>(a.x) + p.token * a.x_stride + p.at);
+        dev::load<T, N, false>(static_cast<const T *>(a.x) + p.token * a.x_stride + p.at);
     const int32_t *rows = a.rows + p.token * a.choices;
     T *out = static_cast<T *>(a.out) + p.at;
-    for (int k = 0; k < a.choices; ++k) {
-        const int32_t r = rows[k];
-        if (r >= 0 && r < a.capacity) dev::store<T, N>(out + r * a.out_stride, v);
-    }
+    dev::by_hint(a.whole_lines, [&](auto nt) {
+        for (int k = 0; k < a.choices; ++k) {
+            const int32_t r = rows[k];
+            if (r >= 0 && r < a.capacity) dev::store<T, N, nt.value>(out + r * a.out_stride, v);
+        }
+    });
 }
 
 // Adds G choices from k on, their rows' loads in flight together.
@@ -127,9 +135,12 @@ __device__ __forceinline__ void add_rows(const MoveArgs &a, const Place &p, int 
     int32_t row[G];
     choices_at<T, G>(a, p.token * a.choices + k, row, w);
     // a dropped choice reads row 0, which is there, and adds nothing
+    dev::by_hint(a.stream, [&](auto nt) {
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-        v[g] = dev::load<T, N>(static_cast<const T *>(a.x) + max(row[g], 0) * a.x_stride + p.at);
+        for (int g = 0; g < G; ++g)
+            v[g] = dev::load<T, N, nt.value>(static_cast<const T *>(a.x) +
+                                             max(row[g], 0) * a.x_stride + p.at);
+    });
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const dev::Floats<N> f = dev::widen<T, N>(v[g]);
@@ -149,8 +160,10 @@ __global__ void __launch_bounds__(kCombineThreads)
     if (a.choices & 4) add_rows<T, N, 4>(a, p, k, sum), k += 4;
     if (a.choices & 2) add_rows<T, N, 2>(a, p, k, sum), k += 2;
     if (a.choices & 1) add_rows<T, N, 1>(a, p, k, sum);
-    dev::store<T, N>(static_cast<T *>(a.out) + p.token * a.out_stride + p.at,
-                     dev::narrow<T, N>(sum));
+    dev::by_hint(a.whole_lines, [&](auto nt) {
+        dev::store<T, N, nt.value>(static_cast<T *>(a.out) + p.token * a.out_stride + p.at,
+                                   dev::narrow<T, N>(sum));
+    });
 }
 
 // Sums of G values over the 64 lanes of a wave (every lane active), that of
@@ -194,18 +207,23 @@ __device__ __forceinline__ void choices_backward(const MoveArgs &a, int64_t toke
         const dev::Vec<T, N> own = dev::load<T, N, false>(grad + at);
         dev::Vec<T, N> v[G];
         // a dropped choice reads row 0, which is there
+        dev::by_hint(a.stream, [&](auto nt) {
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-            v[g] = dev::load<T, N>(static_cast<const T *>(a.in) +
-                                   max(row[g], 0) * a.in_stride + at);
+            for (int g = 0; g < G; ++g)
+                v[g] = dev::load<T, N, nt.value>(static_cast<const T *>(a.in) +
+                                                 max(row[g], 0) * a.in_stride + at);
+        });
         // every load is under way before the first is waited for
         __builtin_amdgcn_sched_barrier(0);
         const dev::Floats<N> d = dev::widen<T, N>(own);
+        dev::by_hint(a.whole_lines, [&](auto nt) {
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-            if (row[g] >= 0)
-                dev::store<T, N>(static_cast<T *>(a.out) + row[g] * a.out_stride + at,
-                                 dev::narrow<T, N>(d * w[g]));
+            for (int g = 0; g < G; ++g)
+                if (row[g] >= 0)
+                    dev::store<T, N, nt.value>(
+                        static_cast<T *>(a.out) + row[g] * a.out_stride + at,
+                        dev::narrow<T, N>(d * w[g]));
+        });
         // elements that the vector before holds too are summed there alone
         const int first = from - at;
         if (first > 0) {
@@ -246,17 +264,17 @@ __device__ __forceinline__ void choices_backward(const MoveArgs &a, int64_t toke
 
 template <typename T, int N, int WAVES>
 __global__ void __launch_bounds__(kBackwardThreads)
-    bmmc_expert_combine_backward_kernel(const MoveArgs a, uint32_t parts, uint32_t block0) {
+    bmmc_expert_combine_backward_kernel(const MoveArgs a, uint32_t pads, uint32_t block0) {
     constexpr int kWaves = kBackwardThreads / 64;
     __shared__ float sums[kWaves * 8];
     const uint32_t block = block0 + blockIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (block >= parts) {
-        zero_padding<T, N>(a, (int64_t)(block - parts) * kWaves + wave);
+    if (block < pads) {
+        zero_padding<T, N>(a, (int64_t)block * kWaves + wave);
         return;
     }
     // a wave past the last token stays for the workgroup's barriers
-    const int64_t token = (int64_t)block * (kWaves / WAVES) + wave / WAVES;
+    const int64_t token = (int64_t)(block - pads) * (kWaves / WAVES) + wave / WAVES;
     const int part = wave % WAVES;
     float *mine = sums + wave / WAVES * WAVES * 8;
     int k = 0;
@@ -296,13 +314,14 @@ template <typename T, int N> int gather_n(const MoveArgs &a, hipStream_t s) {
     bool fits;
     const bool wave = by_waves<N, kGatherThreads>(a, &c, &fits);
     if (!fits) return BMMC_ERR_UNSUPPORTED;
-    return in_launches(c.parts + pad_blocks(a.capacity), kGatherThreads, [&](uint32_t nb, int64_t b0) {
+    const int64_t pads = pad_blocks(a.capacity);
+    return in_launches(pads + c.parts, kGatherThreads, [&](uint32_t nb, int64_t b0) {
         if (wave)
             hipLaunchKernelGGL((bmmc_expert_gather_kernel<T, N, true>), dim3(nb),
-                               dim3(kGatherThreads), 0, s, a, c, (uint32_t)b0);
+                               dim3(kGatherThreads), 0, s, a, c, (uint32_t)pads, (uint32_t)b0);
         else
             hipLaunchKernelGGL((bmmc_expert_gather_kernel<T, N, false>), dim3(nb),
-                               dim3(kGatherThreads), 0, s, a, c, (uint32_t)b0);
+                               dim3(kGatherThreads), 0, s, a, c, (uint32_t)pads, (uint32_t)b0);
     });
 }
 
@@ -329,12 +348,11 @@ template <typename T, int N> int combine_backward_n(const MoveArgs &a, hipStream
     const int64_t vectors = (a.dim + N - 1) / N;
     const int waves = vectors <= 64 ? 1 : vectors <= 128 ? 2 : 4;
     const int64_t tokens = kBackwardThreads / 64 / waves;  // a workgroup
-    const int64_t parts = (a.tokens + tokens - 1) / tokens;
-    return in_launches(parts + pad_blocks(a.capacity), kBackwardThreads,
-                       [&](uint32_t nb, int64_t b0) {
+    const int64_t parts = (a.tokens + tokens - 1) / tokens, pads = pad_blocks(a.capacity);
+    return in_launches(pads + parts, kBackwardThreads, [&](uint32_t nb, int64_t b0) {
         const auto launch = [&](auto kernel) {
             hipLaunchKernelGGL(kernel, dim3(nb), dim3(kBackwardThreads), 0, s, a,
-                               (uint32_t)parts, (uint32_t)b0);
+                               (uint32_t)pads, (uint32_t)b0);
         };
         if (waves == 1)
             launch(bmmc_expert_combine_backward_kernel<T, N, 1>);
@@ -345,19 +363,41 @@ template <typename T, int N> int combine_backward_n(const MoveArgs &a, hipStream
     });
 }
 
+// Rows of whole cache lines are streamed out, others written through the caches,
+// which put the lines that two rows share together: 16384 tokens of 8 choices
+// gather rows of 4094 bytes in 127 us, 146 streamed; rows of 4096 bytes in 118 us
+// and 102 streamed.
+//
+// Rows by expert that the caches can still hold since they were written are
+// read through them, more are streamed in.  Combine and its backward pass, 8
+// choices of 4 KiB a token: 67 MB of rows 14.0 and 24.2 us cached, 16.0 and 28.0
+// streamed; 98 MB 20.4 and 41.4, 20.5 and 39.1; 134 MB 29.4 and 55.1, 26.7 and 51.6.
+constexpr int64_t kMoveCached = int64_t(96) << 20;
+
+MoveArgs with_hints(MoveArgs a, int type) {
+    constexpr int64_t kLine = 128;
+    const int64_t size = type == BMMC_F32 ? 4 : 2;
+    a.whole_lines = (int64_t)((uintptr_t)a.out % kLine) == 0 &&
+                    a.out_stride * size % kLine == 0 && a.dim * size % kLine == 0;
+    a.stream = a.capacity * a.dim > kMoveCached / size;
+    return a;
+}
+
 // Whole vectors, or single elements for rows of less than one.
 #define BMMC_BY_WIDTH(call, T, a, s)                                                  \
     ((a).dim >= dev::Lanes<T>::N ? call<T, dev::Lanes<T>::N>((a), (s)) : call<T, 1>((a), (s)))
 
 }  // namespace
 
-int launch_expert_gather(const MoveArgs &a, int type, hipStream_t s) {
+int launch_expert_gather(const MoveArgs &args, int type, hipStream_t s) {
+    const MoveArgs a = with_hints(args, type);
     // rows are copied as they are: 16-bit types share one kernel
     return type == BMMC_F32 ? BMMC_BY_WIDTH(gather_n, float, a, s)
                             : BMMC_BY_WIDTH(gather_n, dev::f16_t, a, s);
 }
 
-int launch_expert_combine(const MoveArgs &a, int type, hipStream_t s) {
+int launch_expert_combine(const MoveArgs &args, int type, hipStream_t s) {
+    const MoveArgs a = with_hints(args, type);
     switch (type) {
     case BMMC_F32: return BMMC_BY_WIDTH(combine_n, float, a, s);
     case BMMC_F16: return BMMC_BY_WIDTH(combine_n, dev::f16_t, a, s);
@@ -365,7 +405,8 @@ int launch_expert_combine(const MoveArgs &a, int type, hipStream_t s) {
     }
 }
 
-int launch_expert_combine_backward(const MoveArgs &a, int type, hipStream_t s) {
+int launch_expert_combine_backward(const MoveArgs &args, int type, hipStream_t s) {
+    const MoveArgs a = with_hints(args, type);
     switch (type) {
     case BMMC_F32: return BMMC_BY_WIDTH(combine_backward_n, float, a, s);
     case BMMC_F16: return BMMC_BY_WIDTH(combine_backward_n, dev::f16_t, a, s);

@@ -191,7 +191,7 @@ struct TurnHeads {
     Part rest;
     int64_t tokens;  // of all batch entries
     FastDiv by_tokens, by_tasks;
-    int32_t batch, tokens_a_block;
+    int32_t batch, tokens_a_block, stream;
 };
 
 // This wave's first task and the waves of the workgroups that share its tokens.
@@ -241,8 +241,10 @@ __global__ void __launch_bounds__(kTurnThreads)
         if (!l.on || head + l.head >= x.heads) return;
         const T *in = static_cast<const T *>(x.in) + k.in_batch * x.in_batch +
                       k.in_token * x.in_token + head * x.in_head + lane_in[second];
-        va = dev::load<T, N>(in);
-        vb = dev::load<T, N>(in + gap);
+        dev::by_hint(a.stream, [&](auto nt) {
+            va = dev::load<T, N, nt.value>(in);
+            vb = dev::load<T, N, nt.value>(in + gap);
+        });
     };
     make_turns(r, token0, tokens, cs, [&] {
         if (waves.first < tasks) fetch(waves.first);
@@ -290,7 +292,7 @@ struct Append {
     Part rest, values;
     int64_t tokens;
     FastDiv by_tasks;
-    int32_t k_scale_stride, v_scale_stride, tokens_a_block;
+    int32_t k_scale_stride, v_scale_stride, tokens_a_block, stream;
 };
 
 // Stored 8-bit values: clamped, NaN kept, rounded to nearest, ties to even.
@@ -375,7 +377,10 @@ __global__ void __launch_bounds__(kTurnThreads)
         if (number >= values && whole) {
             const Value f = value(number);
             if (f.on)
-                vc = dev::load<T, VN>(source(a.v, token0 + t) + f.head * a.v.in_head + f.at);
+                dev::by_hint(a.stream, [&](auto nt) {
+                    vc = dev::load<T, VN, nt.value>(source(a.v, token0 + t) +
+                                                    f.head * a.v.in_head + f.at);
+                });
         }
         if (number >= turns) return;
         const bool key = number >= a.q.turns;
@@ -383,8 +388,10 @@ __global__ void __launch_bounds__(kTurnThreads)
         const int head = (number - (key ? a.q.turns : 0)) * r.heads_a_wave;
         if (!l.on || head + l.head >= x.heads) return;
         const T *in = source(x, token0 + t) + head * x.in_head + (key ? k_in : q_in);
-        va = dev::load<T, N>(in);
-        vb = dev::load<T, N>(in + gap);
+        dev::by_hint(a.stream, [&](auto nt) {
+            va = dev::load<T, N, nt.value>(in);
+            vb = dev::load<T, N, nt.value>(in + gap);
+        });
     };
     const auto copy = [&](int64_t token, const PagePlace &home, int number) {
         if (number < a.q.copies) {
@@ -513,6 +520,15 @@ TurnCut turn_cut(int64_t tokens, int pairs, int64_t tasks) {
     return c;
 }
 
+// Heads are a projection's output just written, and are read through the caches
+// where they and what becomes of them fit, streamed beyond (98 MB: 17.7 us, 23.2
+// streamed; 168 to 500 MB: the same within 3%; 672 MB: 115 us, 111 streamed).
+constexpr int64_t kTurnCached = int64_t(128) << 20;
+
+bool streams(int64_t elements, size_t bytes) {
+    return elements * 2 > kTurnCached / (int64_t)bytes;
+}
+
 template <typename T, int N, bool PAIRED>
 int rotary_n(const HeadsArgs &h, const bmmc_rotation &x, hipStream_t s) {
     const Turn r = turn_of<N>(x);
@@ -529,6 +545,7 @@ int rotary_n(const HeadsArgs &h, const bmmc_rotation &x, hipStream_t s) {
     a.by_tasks = fast_div((uint32_t)tasks);
     const TurnCut cut = turn_cut(a.tokens, x.pairs, tasks);
     a.tokens_a_block = cut.tokens_a_block;
+    a.stream = streams(a.tokens * (a.x[0].heads + a.x[1].heads) * h.head_dim, sizeof(T));
     return in_launches(cut.blocks, kTurnThreads, [&](uint32_t nb, int64_t b0) {
         hipLaunchKernelGGL((bmmc_rotary_kernel<T, N, PAIRED>), dim3(nb, cut.shares),
                            dim3(64 * cut.waves), 0, s, a, r, b0);
@@ -564,6 +581,8 @@ int append_n(const AppendArgs &h, hipStream_t s) {
     a.by_tasks = fast_div((uint32_t)tasks);
     const TurnCut cut = turn_cut(a.tokens, r.pairs, tasks);
     a.tokens_a_block = cut.tokens_a_block;
+    a.stream = streams(a.tokens * ((a.q.heads + a.k.heads) * (int64_t)h.k_dim +
+                                   a.v.heads * (int64_t)h.v_dim), sizeof(T));
     return in_launches(cut.blocks, kTurnThreads, [&](uint32_t nb, int64_t b0) {
         hipLaunchKernelGGL((bmmc_cache_append_kernel<T, N, PAIRED, E4M3>), dim3(nb, cut.shares),
                            dim3(64 * cut.waves), 0, s, a, r, b0);

@@ -113,6 +113,8 @@ struct MoveArgs {
     void *out, *grad_weights;
     int64_t x_stride, in_stride, out_stride, tokens, capacity, dim;
     int32_t choices, weights_are_f32;
+    int32_t whole_lines;  // rows of out are whole cache lines
+    int32_t stream;       // rows by expert are more than the caches keep
 };
 int launch_expert_gather(const MoveArgs &a, int type, hipStream_t s);
 int launch_expert_combine(const MoveArgs &a, int type, hipStream_t s);
