@@ -10,19 +10,21 @@
 // per wave and expert in LDS holds how many came before.  Nothing depends on
 // the order in which waves run.
 //
+// Every row counts as padding, slots = -1, until a choice is placed there: the
+// rows are filled before, by the launch that counts or by the one workgroup.
+//
 // Bound by latency: it reads 4 or 8 bytes and writes 8 for each choice, in two
-// launches for many choices.  256 choices of 64 experts take 3.0 us, 131072 of
-// 128 experts 10.9 us.
+// launches for many choices.  256 choices of 64 experts take 3.1 us, 8192 of 64
+// experts 7.8 us, 131072 of 64 experts 9.9 us.
 #include "tokens.h"
 
 namespace bmmc {
 
 namespace {
 
-// Counters per wave and expert fill at most 64 KiB of LDS: 16 waves up to
-// 1024 experts, 8 beyond.
-constexpr int kOrderWideExperts = 1024;
-constexpr int kOrderMaxWaves = 16;
+constexpr int kOrderWaves = 16;  // of a workgroup, but for few choices
+// Rows that one workgroup fills; more take a launch of their own.
+constexpr int64_t kOrderFill = 1 << 15;
 
 __device__ __forceinline__ int32_t expert_at(const OrderArgs &a, int64_t i) {
     if (a.is64) {
@@ -33,10 +35,22 @@ __device__ __forceinline__ int32_t expert_at(const OrderArgs &a, int64_t i) {
     return e >= 0 && e < a.num_experts ? e : -1;
 }
 
+// This workgroup's share of the rows.
+__device__ __forceinline__ void fill_slots(const OrderArgs &a) {
+    for (int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.capacity;
+         r += (int64_t)gridDim.x * blockDim.x)
+        a.slots[r] = -1;
+}
+
+__global__ void __launch_bounds__(256) bmmc_expert_fill_kernel(const OrderArgs a) {
+    fill_slots(a);
+}
+
 // Choices of each expert in each chunk.
-__global__ void __launch_bounds__(kOrderMaxWaves * 64)
-    bmmc_expert_count_kernel(const OrderArgs a) {
+__global__ void __launch_bounds__(kOrderWaves * 64)
+    bmmc_expert_count_kernel(const OrderArgs a, int fill) {
     extern __shared__ int32_t cnt[];
+    if (fill) fill_slots(a);
     const int tid = threadIdx.x;
     for (int e = tid; e < a.num_experts; e += blockDim.x) cnt[e] = 0;
     __syncthreads();
@@ -138,7 +152,8 @@ __device__ __forceinline__ Before sum_chunks(const OrderArgs &a, int e0, int32_t
 // counts come from a.hist.  ROUNDS: choices a lane, kept in registers; 0: as
 // many as there are, read a second time.
 template <int WAVES, int ROUNDS, bool MANY>
-__global__ void __launch_bounds__(WAVES * 64) bmmc_expert_place_kernel(const OrderArgs a) {
+__global__ void __launch_bounds__(WAVES * 64)
+    bmmc_expert_place_kernel(const OrderArgs a, int fill) {
     constexpr int kThreads = WAVES * 64;
     extern __shared__ int32_t cnt[];  // [WAVES][num_experts]
     __shared__ int32_t wsum[WAVES];
@@ -161,6 +176,7 @@ __global__ void __launch_bounds__(WAVES * 64) bmmc_expert_place_kernel(const Ord
             held[r] = r < rounds && i < to ? expert_at(a, i) : -1;
         }
     }
+    if (fill) fill_slots(a);
     for (int i = tid; i < WAVES * E; i += kThreads) cnt[i] = 0;
     __syncthreads();
     if constexpr (ROUNDS > 0) {
@@ -203,16 +219,10 @@ __global__ void __launch_bounds__(WAVES * 64) bmmc_expert_place_kernel(const Ord
                 a.offsets[e] = off;
                 a.counts[e] = b.all;
             }
-            if (e % gridDim.x == blockIdx.x)
-                for (int32_t r = off + b.all; r < off + padded; ++r) a.slots[r] = -1;
         }
     }
     if (blockIdx.x == 0 && tid == 0) a.offsets[E] = start;
-    // rows past the last expert's
-    for (int64_t r = start + (int64_t)blockIdx.x * kThreads + tid; r < a.capacity;
-         r += (int64_t)gridDim.x * kThreads)
-        a.slots[r] = -1;
-    __syncthreads();
+    __syncthreads();  // also orders the fill before the choices' stores
 
     if constexpr (ROUNDS > 0) {
 #pragma unroll
@@ -235,40 +245,39 @@ __global__ void __launch_bounds__(WAVES * 64) bmmc_expert_place_kernel(const Ord
 }
 
 template <int WAVES, int ROUNDS, bool MANY>
-void place(const OrderArgs &a, int blocks, hipStream_t s) {
+void place(const OrderArgs &a, int blocks, int fill, hipStream_t s) {
     hipLaunchKernelGGL((bmmc_expert_place_kernel<WAVES, ROUNDS, MANY>), dim3(blocks),
-                       dim3(WAVES * 64), sizeof(int32_t) * (size_t)a.num_experts * WAVES, s, a);
-}
-
-// Most choices of a lane that stay in registers.
-constexpr int kOrderHeld = 8;
-
-template <int WAVES, bool MANY> void place_by_rounds(const OrderArgs &a, int blocks, hipStream_t s) {
-    const int64_t rounds = (a.chunk + WAVES * 64 - 1) / (WAVES * 64);
-    if (rounds <= 1) return place<WAVES, 1, MANY>(a, blocks, s);
-    if (rounds <= kOrderHeld / 2) return place<WAVES, kOrderHeld / 2, MANY>(a, blocks, s);
-    if (rounds <= kOrderHeld) return place<WAVES, kOrderHeld, MANY>(a, blocks, s);
-    place<WAVES, 0, MANY>(a, blocks, s);
+                       dim3(WAVES * 64), sizeof(int32_t) * (size_t)a.num_experts * WAVES, s, a,
+                       fill);
 }
 
 }  // namespace
 
 int launch_expert_order(const OrderArgs &a, int blocks, hipStream_t s) {
-    const bool wide = a.num_experts > kOrderWideExperts;
+    constexpr int kThreads = kOrderWaves * 64;
+    constexpr int kRounds = (int)(kOrderOneBlockMax / kThreads);
+    const bool apart = a.capacity > kOrderFill * blocks;
+    if (apart)
+        hipLaunchKernelGGL(bmmc_expert_fill_kernel, dim3((uint32_t)((a.capacity + 4095) / 4096)),
+                           dim3(256), 0, s, a);
     if (blocks == 1) {
+        // few waves have less to wait for and to sum: 512 choices of 64 experts
+        // take 8 waves 3.5 us and 16 waves 4.2
         if (a.n <= 4 * 64)
-            place<4, 1, false>(a, 1, s);
-        else if (wide)
-            place_by_rounds<8, false>(a, 1, s);
+            place<4, 1, false>(a, 1, !apart, s);
+        else if (a.n <= 2 * 8 * 64)
+            place<8, 2, false>(a, 1, !apart, s);
         else
-            place_by_rounds<16, false>(a, 1, s);
+            place<kOrderWaves, kRounds, false>(a, 1, !apart, s);
     } else {
-        hipLaunchKernelGGL(bmmc_expert_count_kernel, dim3(blocks), dim3(kOrderMaxWaves * 64),
-                           sizeof(int32_t) * (size_t)a.num_experts, s, a);
-        if (wide)
-            place_by_rounds<8, true>(a, blocks, s);
+        hipLaunchKernelGGL(bmmc_expert_count_kernel, dim3(blocks), dim3(kThreads),
+                           sizeof(int32_t) * (size_t)a.num_experts, s, a, !apart);
+        if (a.chunk <= kThreads)
+            place<kOrderWaves, 1, true>(a, blocks, 0, s);
+        else if (a.chunk <= kOrderOneBlockMax)
+            place<kOrderWaves, kRounds, true>(a, blocks, 0, s);
         else
-            place_by_rounds<16, true>(a, blocks, s);
+            place<kOrderWaves, 0, true>(a, blocks, 0, s);
     }
     return hipGetLastError() == hipSuccess ? BMMC_OK : BMMC_ERR_HIP;
 }

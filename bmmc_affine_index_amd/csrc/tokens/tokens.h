@@ -76,13 +76,16 @@ __host__ __device__ inline PagePlace page_place(const PageTable &t, int64_t toke
 // ---- experts ---------------------------------------------------------------
 
 // How bmmc_expert_order cuts its choices: one workgroup up to
-// kOrderOneBlockMax choices, which it holds in registers (12297 choices took it
-// 17.6 us, reading them twice, and take two launches 9.6 us); else at most
-// kOrderMaxBlocks workgroups of `chunk` choices each, which first count into
-// the workspace.
-constexpr int64_t kOrderOneBlockMax = 8192;
+// kOrderOneBlockMax choices, which it holds in registers (3000 choices of 64
+// experts take it 6.9 us, 4096 8.0 and two launches 7.8, at twice the host's
+// time); else at most kOrderMaxBlocks workgroups of `chunk` choices each, which
+// first count into the workspace: of kOrderMinChunk choices, or twice as many
+// where that makes more than 64 workgroups, whose counts each would have to sum
+// (131072 choices of 256 experts 12.2 and 12.7 us, 327680 15.5 and 18.0; 16384
+// choices 10.4 and 9.0).
+constexpr int64_t kOrderOneBlockMax = 4096;
 constexpr int64_t kOrderMaxBlocks = 256;
-constexpr int64_t kOrderMinChunk = 2048;
+constexpr int64_t kOrderMinChunk = 1024;
 
 struct OrderCut {
     int64_t chunk;
@@ -92,7 +95,8 @@ struct OrderCut {
 inline OrderCut order_cut(int64_t n) {
     if (n <= kOrderOneBlockMax) return OrderCut{n, 1};
     int64_t chunk = (n + kOrderMaxBlocks - 1) / kOrderMaxBlocks;
-    if (chunk < kOrderMinChunk) chunk = kOrderMinChunk;
+    const int64_t least = n > 64 * kOrderMinChunk ? 2 * kOrderMinChunk : kOrderMinChunk;
+    if (chunk < least) chunk = least;
     chunk = (chunk + 63) / 64 * 64;
     return OrderCut{chunk, (int32_t)((n + chunk - 1) / chunk)};
 }

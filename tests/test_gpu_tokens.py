@@ -91,8 +91,8 @@ def test_order_of_skewed_choices(n):
 
 
 @pytest.mark.parametrize("n,count", [
-    (256, 5), (257, 2048), (4096, 1024), (8192, 64), (8193, 64), (9000, 2048), (16384, 9),
-    (16384, 2048), (16385, 9), (30000, 1), (530000, 700), (4300000, 5), (4300000, 1500)])
+    (256, 5), (257, 2048), (1024, 7), (1025, 7), (4096, 1024), (4097, 300), (8192, 64), (8193, 64), (9000, 2048), (16384, 9),
+    (16384, 2048), (16385, 9), (30000, 1), (65536, 30), (65537, 30), (530000, 700), (4300000, 5), (4300000, 1500)])
 def test_order_of_many_lengths(n, count):
     """One workgroup and several, choices held in registers and read twice."""
     experts = torch.randint(-1, count + 1, (n, 1), generator=_gen(n + count))
@@ -100,8 +100,9 @@ def test_order_of_many_lengths(n, count):
 
 
 def test_order_with_wide_padding():
-    experts = torch.randint(0, 7, (20000, 1), generator=_gen(9))
-    _check_order(experts.to(DEV), 7, align=5000)
+    for n, align in ((20000, 5000), (100, 30000), (5000, 200000)):
+        experts = torch.randint(0, 7, (n, 1), generator=_gen(9))
+        _check_order(experts.to(DEV), 7, align=align)
 
 
 def test_order_drops_far_values():
