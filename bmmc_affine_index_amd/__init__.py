@@ -4,7 +4,8 @@ A thin ctypes binding over ``libbmmc.so`` (built from ``csrc/`` by
 ``bmmc_affine_index_amd.build``).  The functions named like the C ABI
 (``bmmc_plan_create``, ``bmmc_execute``, ``bmmc_copy``, ...) only marshal
 arguments; every step of the permutation runs in the library's HIP kernels.
-There is no CPU fallback: if the library is missing, every call raises.
+There is no CPU fallback: if the library is missing, every call raises.  The
+calls on token rows are in tokens.py, bound in C++ (``csrc/binding``).
 
 Matrices are n row masks (``A[r]`` = mask of input bits feeding output bit r;
 bit 0 = least significant index bit), as in include/bmmc.h.

@@ -715,3 +715,63 @@ def test_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, want)), seed
+
+
+def _training_step(x, experts, w, y, positions, freqs):
+    order = bm.expert_order(experts, 16, align=4)
+    q, k = bm.rotary((x.unflatten(1, (8, 64)), x.unflatten(1, (8, 64))), positions, freqs)
+    rows = torch.tanh(bm.expert_gather((q + 0.5 * k).flatten(1), order))
+    out = bm.expert_combine(rows, order, w)
+    return (out, *torch.autograd.grad((out * y).sum(), (x, w)))
+
+
+def test_a_training_step_in_a_graph():
+    """Forward and backward passes captured together, replayed on other inputs
+    with eager steps in between; no eager graph of the leaves is alive while
+    the capture runs."""
+    def inputs(seed):
+        g = _gen(seed)
+        return [torch.randn(300, 512, generator=g).to(DEV).requires_grad_(),
+                torch.randint(-1, 16, (300, 4), generator=g).to(DEV),
+                torch.rand(300, 4, generator=g).to(DEV).requires_grad_(),
+                torch.randn(300, 512, generator=g).to(DEV),
+                torch.randint(0, 5000, (300,), generator=g).to(DEV), _freqs(32).to(DEV)]
+    a = inputs(80)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            _training_step(*a)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = _training_step(*a)
+    for seed in (81, 82, 83):
+        b = inputs(seed)
+        want = [t.detach().clone() for t in _training_step(*b)]
+        with torch.no_grad():
+            for t, u in zip(a, b):
+                t.copy_(u)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want)), seed
+
+
+# --------------------------------------------------------------------------
+# The example
+# --------------------------------------------------------------------------
+
+def test_the_example():
+    """A layer that serves and trains through these calls: sums of at most 512
+    terms in 32 bits, off by at most 512 roundings of the largest value."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(__file__), "..", "examples", "sparse_layer.py")
+    spec = importlib.util.spec_from_file_location("sparse_layer", path)
+    layer = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(layer)
+    device = torch.device(DEV)
+    with torch.no_grad():
+        assert layer.serve(device, torch.float32, 70, 3)[0] <= 512 * U32
+    assert layer.train(device, 70) <= 512 * U32
