@@ -17,7 +17,9 @@ namespace {
 
 // Threads of a workgroup, measured on 16384 tokens of 8 choices, 8 KiB a row:
 // gather 224 us with 256 and 230 with 128, combine 212 and 200; at other sizes
-// (2 to 14 KiB a row) the two differ by up to 3% the same way.
+// (2 to 14 KiB a row) the two differ by up to 3% the same way.  A gather whose
+// waves share choices takes 212 us with 512 threads and 217 with 256, rows of
+// 4 KiB 103 and 100.
 constexpr int kGatherThreads = 256;
 constexpr int kCombineThreads = 128;
 constexpr int kBackwardThreads = 256;
@@ -44,13 +46,14 @@ struct Cut {
 // WAVE: each wave is one token's, so that its row numbers and weights are
 // scalars; else lanes take the vectors of successive tokens in turn, which
 // leaves no lane without work when a row is not a multiple of 64 vectors.
-template <int THREADS, bool WAVE, int N>
+// SHARES waves next to each other have the same place.
+template <int THREADS, bool WAVE, int N, int SHARES = 1>
 __device__ __forceinline__ Place locate(const Cut &c, int64_t tokens, int64_t dim,
                                         uint32_t block) {
     uint32_t token, vec;
     if constexpr (WAVE) {
-        const uint32_t task =
-            block * (THREADS / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const uint32_t task = block * (THREADS / 64 / SHARES) +
+                              __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / SHARES;
         token = quotient(c.by, task);
         vec = (task - token * c.by.d) * 64 + (threadIdx.x & 63);
     } else {
@@ -102,7 +105,8 @@ __device__ __forceinline__ void zero_padding(const MoveArgs &a, int64_t wave) {
     }
 }
 
-template <typename T, int N, bool WAVE>
+// SHARES: waves that share a token's choices, each with the token's row.
+template <typename T, int N, bool WAVE, int SHARES>
 __global__ void __launch_bounds__(kGatherThreads)
     bmmc_expert_gather_kernel(const MoveArgs a, const Cut c, uint32_t pads, uint32_t block0) {
     const uint32_t block = block0 + blockIdx.x;
@@ -110,16 +114,17 @@ __global__ void __launch_bounds__(kGatherThreads)
         zero_padding<T, N>(a, (int64_t)block * (kGatherThreads / 64) + (threadIdx.x >> 6));
         return;
     }
-    const Place p = locate<kGatherThreads, WAVE, N>(c, a.tokens, a.dim, block - pads);
+    const Place p = locate<kGatherThreads, WAVE, N, SHARES>(c, a.tokens, a.dim, block - pads);
     if (p.at < 0) return;
     // a layer's input, which the layer before has just written: through the
     // caches (16384 tokens of 8 choices, 4 KiB a row: 102 us, 114 streamed)
     const dev::Vec<T, N> v =
         dev::load<T, N, false>(static_cast<const T *>(a.x) + p.token * a.x_stride + p.at);
     const int32_t *rows = a.rows + p.token * a.choices;
+    const int share = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % SHARES;
     T *out = static_cast<T *>(a.out) + p.at;
     dev::by_hint(a.whole_lines, [&](auto nt) {
-        for (int k = 0; k < a.choices; ++k) {
+        for (int k = share; k < a.choices; k += SHARES) {
             const int32_t r = rows[k];
             if (r >= 0 && r < a.capacity) dev::store<T, N, nt.value>(out + r * a.out_stride, v);
         }
@@ -287,9 +292,10 @@ __global__ void __launch_bounds__(kBackwardThreads)
 // Whether each wave is one token's: where that leaves at most a fifth of the
 // lanes idle, or where the vectors of all tokens pass the 31 bits of a
 // quotient.  *fits is false where the waves pass them too.
-template <int N, int THREADS> bool by_waves(const MoveArgs &a, Cut *c, bool *fits) {
+template <int N, int THREADS>
+bool by_waves(const MoveArgs &a, int shares, Cut *c, bool *fits) {
     constexpr int64_t kMost = int64_t(1) << 31;
-    constexpr int kWaves = THREADS / 64;
+    const int kWaves = THREADS / 64 / shares;
     const int64_t vectors = (a.dim + N - 1) / N, waves = (vectors + 63) / 64;
     c->vectors = (uint32_t)vectors;
     *fits = a.tokens * waves < kMost - THREADS;
@@ -309,26 +315,38 @@ int64_t pad_blocks(int64_t capacity) {
     return (capacity + kRows - 1) / kRows;
 }
 
+// Waves that share a token's choices in the gather, where rows are whole cache
+// lines (16384 tokens of 8 choices, 8 KiB a row: 217 us, 224 with one wave for all;
+// 4 KiB 100 and 102).  Otherwise one wave writes them all, and the workgroup's
+// waves write next to each other, so that shared lines come together (rows of
+// 4094 bytes: 131 us, 183 with four).
+constexpr int kGatherShares = 4;
+
 template <typename T, int N> int gather_n(const MoveArgs &a, hipStream_t s) {
     Cut c;
     bool fits;
-    const bool wave = by_waves<N, kGatherThreads>(a, &c, &fits);
+    const int shares = a.whole_lines && a.choices >= kGatherShares ? kGatherShares : 1;
+    const bool wave = by_waves<N, kGatherThreads>(a, shares, &c, &fits);
     if (!fits) return BMMC_ERR_UNSUPPORTED;
     const int64_t pads = pad_blocks(a.capacity);
     return in_launches(pads + c.parts, kGatherThreads, [&](uint32_t nb, int64_t b0) {
-        if (wave)
-            hipLaunchKernelGGL((bmmc_expert_gather_kernel<T, N, true>), dim3(nb),
-                               dim3(kGatherThreads), 0, s, a, c, (uint32_t)pads, (uint32_t)b0);
+        const auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3(nb), dim3(kGatherThreads), 0, s, a, c,
+                               (uint32_t)pads, (uint32_t)b0);
+        };
+        if (!wave)
+            launch(bmmc_expert_gather_kernel<T, N, false, 1>);
+        else if (shares == 1)
+            launch(bmmc_expert_gather_kernel<T, N, true, 1>);
         else
-            hipLaunchKernelGGL((bmmc_expert_gather_kernel<T, N, false>), dim3(nb),
-                               dim3(kGatherThreads), 0, s, a, c, (uint32_t)pads, (uint32_t)b0);
+            launch(bmmc_expert_gather_kernel<T, N, true, kGatherShares>);
     });
 }
 
 template <typename T, int N> int combine_n(const MoveArgs &a, hipStream_t s) {
     Cut c;
     bool fits;
-    const bool wave = by_waves<N, kCombineThreads>(a, &c, &fits);
+    const bool wave = by_waves<N, kCombineThreads>(a, 1, &c, &fits);
     if (!fits) return BMMC_ERR_UNSUPPORTED;
     return in_launches(c.parts, kCombineThreads, [&](uint32_t nb, int64_t b0) {
         if (wave)
