@@ -4,10 +4,11 @@
 //   gather    reads T D, writes R D elements
 //   combine   reads up to T K D, writes T D
 //   backward  reads T D + T K D, writes R D
-// They go token by token, so that each token's own row is read or written once
-// however many choices it has: a lane holds one 16-byte vector of the token's
-// row and moves the same columns of all its choices' rows, whose loads are in
-// flight together.
+// They go token by token, so that each token's own row comes from memory or goes
+// there once however many choices it has.  In gather and combine a lane holds one
+// 16-byte vector of the token's row and moves the same columns of its choices'
+// rows, whose loads are in flight together; the backward pass, which sums along
+// the rows, has a wave for each choice.
 #include "device.h"
 #include "tokens.h"
 
@@ -171,122 +172,94 @@ __global__ void __launch_bounds__(kCombineThreads)
     });
 }
 
-// Sums of G values over the 64 lanes of a wave (every lane active), that of
-// value g in the lanes with lane % G == g: while there are several values,
-// each step sends half of them to the lane that keeps that half, 10 exchanges
-// for 8 values against 48 one by one.
-template <int G> __device__ __forceinline__ float wave_sums(float (&v)[G]) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int h = G / 2; h; h /= 2) {
-        const bool upper = lane & h;
-#pragma unroll
-        for (int g = 0; g < h; ++g) {
-            const float keep = upper ? v[g + h] : v[g], send = upper ? v[g] : v[g + h];
-            v[g] = keep + __shfl_xor(send, h, 64);
-        }
-    }
-#pragma unroll
-    for (int d = G; d < 64; d *= 2) v[0] += __shfl_xor(v[0], d, 64);
-    return v[0];
-}
-
-// Gradients of G choices from k on of one token, by WAVES waves: each lane
-// sums its columns, then the lanes, then the waves, in a fixed order.
-// sums[WAVES][8] is the token's.
-template <typename T, int N, int WAVES, int G>
-__device__ __forceinline__ void choices_backward(const MoveArgs &a, int64_t token, int k,
-                                                 int part, float *sums) {
-    const int lane = threadIdx.x & 63;
-    const int dim = (int)a.dim, last = dim - N;
-    const bool on = token < a.tokens;
-    float dot[G], w[G];
-    int32_t row[G];
-    const int64_t i = (on ? token : 0) * a.choices + k;
-    choices_at<T, G>(a, i, row, w);
-#pragma unroll
-    for (int g = 0; g < G; ++g) dot[g] = 0.0f;
-    const T *grad = static_cast<const T *>(a.x) + (on ? token : 0) * a.x_stride;
-    for (int from = (part * 64 + lane) * N; on && from < dim; from += WAVES * 64 * N) {
-        const int at = min(from, last);
-        const dev::Vec<T, N> own = dev::load<T, N, false>(grad + at);
-        dev::Vec<T, N> v[G];
-        // a dropped choice reads row 0, which is there
-        dev::by_hint(a.stream, [&](auto nt) {
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                v[g] = dev::load<T, N, nt.value>(static_cast<const T *>(a.in) +
-                                                 max(row[g], 0) * a.in_stride + at);
-        });
-        // every load is under way before the first is waited for
-        __builtin_amdgcn_sched_barrier(0);
-        const dev::Floats<N> d = dev::widen<T, N>(own);
-        dev::by_hint(a.whole_lines, [&](auto nt) {
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (row[g] >= 0)
-                    dev::store<T, N, nt.value>(
-                        static_cast<T *>(a.out) + row[g] * a.out_stride + at,
-                        dev::narrow<T, N>(d * w[g]));
-        });
-        // elements that the vector before holds too are summed there alone
-        const int first = from - at;
-        if (first > 0) {
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const dev::Floats<N> f = dev::widen<T, N>(v[g]);
-#pragma unroll
-                for (int j = 0; j < N; ++j) dot[g] = j >= first ? fmaf(d[j], f[j], dot[g]) : dot[g];
-            }
-        } else {
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const dev::Floats<N> f = dev::widen<T, N>(v[g]);
-#pragma unroll
-                for (int j = 0; j < N; ++j) dot[g] = fmaf(d[j], f[j], dot[g]);
-            }
-        }
-    }
-    float sum = wave_sums<G>(dot);
-    if constexpr (WAVES > 1) {
-        __syncthreads();  // the last group's sums have been read
-        if (lane < G) sums[part * 8 + lane] = sum;
-        __syncthreads();
-        if (lane < G) {
-            sum = 0.0f;
-            for (int p = 0; p < WAVES; ++p) sum += sums[p * 8 + lane];
-        }
-    }
-    if (on && part == 0 && lane < G) {
-        const int32_t mine = a.rows[i + lane];
-        const float r = mine >= 0 && mine < a.capacity ? sum : 0.0f;
-        if (a.weights_are_f32)
-            static_cast<float *>(a.grad_weights)[i + lane] = r;
-        else
-            static_cast<T *>(a.grad_weights)[i + lane] = (T)r;
-    }
-}
-
-template <typename T, int N, int WAVES>
+// Gradients of one choice by 2^lanes_log2 lanes (WAVE: by a wave, so that its
+// numbers are scalars): grad_in of its row = weight * its token's gradient, and
+// that gradient's product with the row.  The choices of a token are next to each
+// other, so that its gradient comes from memory once and then from the caches.
+// V vectors of a lane of both rows are in flight together.  8192 tokens of 8
+// choices, 4 KiB a row: 102 us; 104 with four waves that each take a part of all 8
+// rows and join their sums, 112 in the order of the rows, which reads and writes
+// in sequence but has each gradient from memory 8 times.
+//
+// Each lane sums its columns, then the lanes are joined, in a fixed order.
+template <typename T, int N, int V, bool WAVE>
 __global__ void __launch_bounds__(kBackwardThreads)
-    bmmc_expert_combine_backward_kernel(const MoveArgs a, uint32_t pads, uint32_t block0) {
-    constexpr int kWaves = kBackwardThreads / 64;
-    __shared__ float sums[kWaves * 8];
-    const uint32_t block = block0 + blockIdx.x;
+    bmmc_expert_combine_backward_kernel(const MoveArgs a, const FastDiv by_choices,
+                                        int lanes_log2, uint32_t pads, uint32_t block0) {
+    uint32_t block = block0 + blockIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (block < pads) {
-        zero_padding<T, N>(a, (int64_t)block * kWaves + wave);
+        zero_padding<T, N>(a, (int64_t)block * (kBackwardThreads / 64) + wave);
         return;
     }
-    // a wave past the last token stays for the workgroup's barriers
-    const int64_t token = (int64_t)(block - pads) * (kWaves / WAVES) + wave / WAVES;
-    const int part = wave % WAVES;
-    float *mine = sums + wave / WAVES * WAVES * 8;
-    int k = 0;
-    for (; k + 8 <= a.choices; k += 8) choices_backward<T, N, WAVES, 8>(a, token, k, part, mine);
-    if (a.choices & 4) choices_backward<T, N, WAVES, 4>(a, token, k, part, mine), k += 4;
-    if (a.choices & 2) choices_backward<T, N, WAVES, 2>(a, token, k, part, mine), k += 2;
-    if (a.choices & 1) choices_backward<T, N, WAVES, 1>(a, token, k, part, mine);
+    block -= pads;
+    uint32_t i;
+    int lane, lanes;
+    if constexpr (WAVE) {
+        i = block * (kBackwardThreads / 64) + wave;
+        lane = threadIdx.x & 63;
+        lanes = 64;
+    } else {
+        lanes = 1 << lanes_log2;
+        i = block * (kBackwardThreads >> lanes_log2) + (threadIdx.x >> lanes_log2);
+        lane = threadIdx.x & (lanes - 1);
+    }
+    if (i >= a.tokens * a.choices) return;
+    const int32_t row = a.rows[i];
+    float dot = 0.0f;
+    if (row >= 0 && row < a.capacity) {
+        const float w = a.weights_are_f32 ? static_cast<const float *>(a.weights)[i]
+                                          : (float)static_cast<const T *>(a.weights)[i];
+        const T *grad =
+            static_cast<const T *>(a.x) + (int64_t)quotient(by_choices, i) * a.x_stride;
+        const T *in = static_cast<const T *>(a.in) + row * a.in_stride;
+        T *out = static_cast<T *>(a.out) + row * a.out_stride;
+        const int dim = (int)a.dim, last = dim - N, step = lanes * N;
+        for (int from = lane * N; from < dim; from += V * step) {
+            dev::Vec<T, N> f[V], d[V];
+            // a vector past the row's end is the last one again
+            dev::by_hint(a.stream, [&](auto nt) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    f[v] = dev::load<T, N, nt.value>(in + min(from + v * step, last));
+            });
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                d[v] = dev::load<T, N, false>(grad + min(from + v * step, last));
+            // every load is under way before the first is waited for
+            __builtin_amdgcn_sched_barrier(0);
+            dev::by_hint(a.whole_lines, [&](auto nt) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (from + v * step < dim)
+                        dev::store<T, N, nt.value>(
+                            out + min(from + v * step, last),
+                            dev::narrow<T, N>(dev::widen<T, N>(d[v]) * w));
+            });
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int want = from + v * step;
+                if (want >= dim) break;
+                const dev::Floats<N> x = dev::widen<T, N>(f[v]), g = dev::widen<T, N>(d[v]);
+                if (want > last) {  // what the vector before holds too is summed there
+#pragma unroll
+                    for (int j = 0; j < N; ++j) dot = j >= want - last ? fmaf(g[j], x[j], dot) : dot;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) dot = fmaf(g[j], x[j], dot);
+                }
+            }
+        }
+    }
+    if constexpr (WAVE)
+        dot = dev::wave_sum(dot);
+    else
+        for (int d = lanes / 2; d; d >>= 1) dot += __shfl_xor(dot, d, 64);
+    if (lane != 0) return;
+    if (a.weights_are_f32)
+        static_cast<float *>(a.grad_weights)[i] = dot;
+    else
+        static_cast<T *>(a.grad_weights)[i] = (T)dot;
 }
 
 // Whether each wave is one token's: where that leaves at most a fifth of the
@@ -358,26 +331,30 @@ template <typename T, int N> int combine_n(const MoveArgs &a, hipStream_t s) {
     });
 }
 
-// Waves of a token: as many as its row has vectors for, at most 4.  8192
-// tokens of 8 choices, 4 KiB a row: 104 us with 4 waves, 114 with one that
-// takes 4 vectors in turn (and 112 row by row in the order, where rows are read
-// and written one after the other but each token's gradient is read 8 times).
+// Lanes of a choice: the power of two that leaves none without a vector, at
+// most a wave; a lane's vectors in flight: as many as the row has, at most 4.
 template <typename T, int N> int combine_backward_n(const MoveArgs &a, hipStream_t s) {
     const int64_t vectors = (a.dim + N - 1) / N;
-    const int waves = vectors <= 64 ? 1 : vectors <= 128 ? 2 : 4;
-    const int64_t tokens = kBackwardThreads / 64 / waves;  // a workgroup
-    const int64_t parts = (a.tokens + tokens - 1) / tokens, pads = pad_blocks(a.capacity);
+    int lanes_log2 = 0;
+    while (lanes_log2 < 6 && (int64_t(2) << lanes_log2) <= vectors) ++lanes_log2;
+    const int64_t a_lane = (vectors + (1 << lanes_log2) - 1) >> lanes_log2;
+    const int64_t choices = kBackwardThreads >> lanes_log2;  // a workgroup
+    const int64_t parts = (a.tokens * a.choices + choices - 1) / choices;
+    const int64_t pads = pad_blocks(a.capacity);
+    const FastDiv by = fast_div((uint32_t)a.choices);
     return in_launches(pads + parts, kBackwardThreads, [&](uint32_t nb, int64_t b0) {
         const auto launch = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, dim3(nb), dim3(kBackwardThreads), 0, s, a,
+            hipLaunchKernelGGL(kernel, dim3(nb), dim3(kBackwardThreads), 0, s, a, by, lanes_log2,
                                (uint32_t)pads, (uint32_t)b0);
         };
-        if (waves == 1)
-            launch(bmmc_expert_combine_backward_kernel<T, N, 1>);
-        else if (waves == 2)
-            launch(bmmc_expert_combine_backward_kernel<T, N, 2>);
+        if (lanes_log2 < 6)
+            launch(bmmc_expert_combine_backward_kernel<T, N, 2, false>);
+        else if (a_lane <= 1)
+            launch(bmmc_expert_combine_backward_kernel<T, N, 1, true>);
+        else if (a_lane <= 2)
+            launch(bmmc_expert_combine_backward_kernel<T, N, 2, true>);
         else
-            launch(bmmc_expert_combine_backward_kernel<T, N, 4>);
+            launch(bmmc_expert_combine_backward_kernel<T, N, 4, true>);
     });
 }
 
