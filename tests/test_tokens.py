@@ -446,3 +446,38 @@ def test_host_tensors_are_refused():
 def test_rotary_axes():
     assert bm.rotary_axes([2, 1, 1]).tolist() == [0, 0, 1, 2]
     assert bm.rotary_axes([1, 3, 2], interleaved=True).tolist() == [0, 1, 2, 1, 2, 1]
+
+
+# --------------------------------------------------------------------------
+# The native calls
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("call", [
+    lambda n: n.order(), lambda n: n.order(torch.zeros(4, 2, dtype=torch.int64), 3, 1),
+    lambda n: n.gather(1, 2, 3, 4, 5, 6), lambda n: n.order([[0, 1]], 3, 1, None),
+    lambda n: n.order(torch.zeros(4, 2, dtype=torch.int64), "3", 1, None),
+    lambda n: n.order(torch.zeros(4, 2, dtype=torch.int64), 2.5, 1, None),
+    lambda n: n.combine(torch.zeros(8, 8), *_order()[2:], [1.0], None, None),
+    lambda n: n.rotary((None,), POS, F, None, False, 1.0, None, False, None)])
+def test_native_calls_count_and_type_their_arguments(call):
+    with pytest.raises(TypeError):
+        call(tk._calls())
+
+
+@pytest.mark.parametrize("call", [
+    lambda n: n.order(torch.zeros(4, 2, dtype=torch.int64), 1 << 40, 1, None),
+    lambda n: n.order(torch.zeros(4, 2, dtype=torch.int64), -(1 << 40), 1, None),
+    lambda n: n.order(torch.zeros(4, 2, dtype=torch.int64), (1 << 32) + 4, 1, None),
+    lambda n: n.order(torch.zeros(4, 2, dtype=torch.int64), 4, 1 << 62, None),
+    lambda n: n.rotary((), POS, F, None, False, 1.0, None, False, None)])
+def test_native_calls_check_wide_numbers(call):
+    with pytest.raises(ValueError):
+        call(tk._calls())
+
+
+def test_another_stream_needs_device_tensors():
+    for call in (lambda: bm.expert_order(torch.zeros(4, 2, dtype=torch.int64), 3, stream=1),
+                 lambda: bm.expert_gather(torch.zeros(4, 8), _order(), stream=1),
+                 lambda: bm.rotary(torch.zeros(4, 2, 8), POS, F, stream=1)):
+        with pytest.raises(ValueError, match="device"):
+            call()
