@@ -3,9 +3,10 @@
 //
 // A decoding step's moves run for 3 to 5 us on the card, so that the call
 // around them is what such a step waits for.  Here a call's checks, new tensors
-// and launch take 5.5 us of host time for expert_combine of 17 tokens (13.9 us
-// with the checks in Python and the call through ctypes), 6.1 us for
-// cache_append of 64 (24.2 us), 12.7 us for an order and its gather (28.6 us).
+// and launch take 4.9 us of host time for expert_combine of 17 tokens (13.9 us
+// with the checks in Python and the call through ctypes), 5.4 us for
+// cache_append of 64 (24.2 us), 10.1 us for an order and its gather (28.6 us); a
+// launch alone takes 2.8 to 3.4 us.
 // Python keeps what is not on that way: autograd, other streams, documentation.
 //
 // The library is opened by the path that Python names, so that this module
@@ -115,15 +116,26 @@ void check_index(const Tensor &x, const char *what) {
 
 // ---- the call --------------------------------------------------------------
 
-void on_device(const Tensor &t) {
-    TORCH_CHECK_VALUE(t.is_cuda(), "tensors must be device tensors");
-    TORCH_CHECK_VALUE(t.get_device() == c10::hip::current_device(),
-                      "tensors must be on the current device");
+const Tensor *pointer(const Tensor &t) { return &t; }
+const Tensor *pointer(const Tensor *t) { return t; }
+
+// Tensors, and pointers to those that may be left out.
+template <typename... T> void on_device(const T &...all) {
+    const Tensor *const ts[] = {pointer(all)...};
+    for (const Tensor *t : ts)
+        TORCH_CHECK_VALUE(!t || t->is_cuda(), "tensors must be device tensors");
+    const auto current = c10::hip::current_device();
+    for (const Tensor *t : ts)
+        TORCH_CHECK_VALUE(!t || t->get_device() == current,
+                          "tensors must be on the current device");
 }
-void on_device(const Tensor *t) {
-    if (t) on_device(*t);
+
+// As at::empty_like, which takes longer over the usual order of dimensions.
+Tensor like(const Tensor &x) {
+    bool falling = true;
+    for (int64_t i = 1; i < x.dim(); ++i) falling &= x.stride(i - 1) >= x.stride(i);
+    return falling ? at::empty(x.sizes(), x.options()) : at::empty_like(x);
 }
-template <typename... T> void on_device(const T &...t) { (on_device(t), ...); }
 
 // A stream's handle, torch's current stream for None.
 void *stream_of(PyObject *o) {
@@ -142,8 +154,6 @@ void check_status(int status, const char *what) {
     }
     throw python_error();
 }
-
-at::TensorOptions int32_on(const Tensor &t) { return t.options().dtype(at::kInt); }
 
 // ---- tokens by expert ------------------------------------------------------
 
@@ -170,15 +180,15 @@ PyObject *py_order(PyObject *, PyObject *const *a, Py_ssize_t) {
                       "the number of experts, the alignment or the order's rows are out of range");
     on_device(experts);
     const int64_t need = lib.expert_order_workspace(n, e);
-    const at::TensorOptions like = int32_on(experts);
+    const at::TensorOptions whole32 = experts.options().dtype(at::kInt);
     const bool flat = experts.dim() != 2;
     // one allocation for the four results
-    const Tensor all = at::empty({2 * e + 1 + n + capacity}, like);
+    const Tensor all = at::empty({2 * e + 1 + n + capacity}, whole32);
     Tensor offsets = part_of(all, 0, {e + 1}), counts = part_of(all, e + 1, {e});
     Tensor rows = part_of(all, 2 * e + 1,
                           {flat ? n : experts.size(0), flat ? 1 : experts.size(1)});
     Tensor slots = part_of(all, 2 * e + 1 + n, {capacity}), work;
-    if (need) work = at::empty({need / 4}, like);
+    if (need) work = at::empty({need / 4}, whole32);
     check_status(lib.expert_order(experts.data_ptr(), index_type(experts), n, e, align,
                                   offsets.data_ptr<int32_t>(), counts.data_ptr<int32_t>(),
                                   rows.data_ptr<int32_t>(), slots.data_ptr<int32_t>(),
@@ -208,13 +218,13 @@ Order order_of(PyObject *r, PyObject *s) {
     return Order{rows, slots, rows.size(0), slots.size(0), (int)rows.size(1)};
 }
 
-Tensor out_of(PyObject *o, int64_t rows, const Tensor &like) {
-    if (o == Py_None) return at::empty({rows, like.size(1)}, like.options());
+Tensor out_of(PyObject *o, int64_t rows, const Tensor &x) {
+    if (o == Py_None) return at::empty({rows, x.size(1)}, x.options());
     const Tensor &out = tensor(o, "out");
     check_matrix(out, "out");
-    TORCH_CHECK_VALUE(out.scalar_type() == like.scalar_type() && out.size(0) == rows &&
-                          out.size(1) == like.size(1),
-                      "out must be [", rows, ", ", like.size(1), "] of the input's type");
+    TORCH_CHECK_VALUE(out.scalar_type() == x.scalar_type() && out.size(0) == rows &&
+                          out.size(1) == x.size(1),
+                      "out must be [", rows, ", ", x.size(1), "] of the input's type");
     TORCH_CHECK_VALUE(!(out.requires_grad() && c10::GradMode::is_enabled()),
                       "out must not ask for a gradient");
     return out;
@@ -405,7 +415,7 @@ PyObject *py_rotary(PyObject *, PyObject *const *a, Py_ssize_t) {
     bmmc_heads heads[2];
     for (Py_ssize_t i = 0; i < count; ++i) {
         PyObject *o = a[6] == Py_None ? Py_None : PyTuple_GET_ITEM(a[6], i);
-        outs[i] = o == Py_None ? at::empty_like(*xs[i]) : tensor(o, "out");
+        outs[i] = o == Py_None ? like(*xs[i]) : tensor(o, "out");
         heads[i] = heads_of(*xs[i], &outs[i], "x");
         on_device(*xs[i], outs[i]);
     }
@@ -503,7 +513,7 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t) {
         TORCH_CHECK_VALUE(q->dim() == 3 && q->scalar_type() == k.scalar_type() &&
                               q->size(0) == tokens && q->size(1) > 0 && q->size(2) == dim,
                           "q must be [tokens, heads, size] as k");
-        q_out = given ? *given : at::empty_like(*q);
+        q_out = given ? *given : like(*q);
         qh = heads_of(*q, &q_out, "q");
         on_device(*q, q_out);
     }
@@ -523,6 +533,23 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t) {
 }
 
 // ---- the module ------------------------------------------------------------
+
+// asks(tensors, None or tuples of them ...): whether one asks for a gradient.
+bool asks(PyObject *o) {
+    if (THPVariable_Check(o)) return THPVariable_Unpack(o).requires_grad();
+    if (!PyTuple_Check(o)) return false;
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(o); ++i)
+        if (asks(PyTuple_GET_ITEM(o, i))) return true;
+    return false;
+}
+PyObject *py_asks(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (c10::GradMode::is_enabled())
+        for (Py_ssize_t i = 0; i < n; ++i)
+            if (asks(a[i])) Py_RETURN_TRUE;
+    Py_RETURN_FALSE;
+    END_HANDLE_TH_ERRORS
+}
 
 // load(path of libbmmc.so, BmmcError)
 PyObject *py_load(PyObject *, PyObject *const *a, Py_ssize_t) {
@@ -571,6 +598,8 @@ PyMethodDef methods[] = {
     method<py_combine_backward, 6>("combine_backward"),
     method<py_rotary, 9>("rotary"),
     method<py_append, 17>("append"),
+    PyMethodDef{"asks", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(py_asks)),
+                METH_FASTCALL, nullptr},
     PyMethodDef{nullptr, nullptr, 0, nullptr},
 };
 

@@ -163,9 +163,17 @@ __global__ void __launch_bounds__(kCombineThreads)
     dev::Floats<N> sum = 0.0f;
     int k = 0;
     for (; k + 8 <= a.choices; k += 8) add_rows<T, N, 8>(a, p, k, sum);
-    if (a.choices & 4) add_rows<T, N, 4>(a, p, k, sum), k += 4;
-    if (a.choices & 2) add_rows<T, N, 2>(a, p, k, sum), k += 2;
-    if (a.choices & 1) add_rows<T, N, 1>(a, p, k, sum);
+    // the loads of the last choices, too, are in flight together
+    switch (a.choices - k) {
+    case 7: add_rows<T, N, 7>(a, p, k, sum); break;
+    case 6: add_rows<T, N, 6>(a, p, k, sum); break;
+    case 5: add_rows<T, N, 5>(a, p, k, sum); break;
+    case 4: add_rows<T, N, 4>(a, p, k, sum); break;
+    case 3: add_rows<T, N, 3>(a, p, k, sum); break;
+    case 2: add_rows<T, N, 2>(a, p, k, sum); break;
+    case 1: add_rows<T, N, 1>(a, p, k, sum); break;
+    default: break;
+    }
     dev::by_hint(a.whole_lines, [&](auto nt) {
         dev::store<T, N, nt.value>(static_cast<T *>(a.out) + p.token * a.out_stride + p.at,
                                    dev::narrow<T, N>(sum));

@@ -132,10 +132,6 @@ def _run(call, args: tuple, stream):
     return got[0]
 
 
-def _asks_gradient(*tensors) -> bool:
-    return _torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-
-
 def _need(ok, what: str) -> None:
     if not ok:
         raise ValueError(what)
@@ -172,12 +168,12 @@ def _check_order(order) -> None:
 def expert_gather(x, order: ExpertOrder, out=None, stream=None):
     """The tokens' rows in the order of their experts: [R, D] from x [T, D],
     each token's row once for each choice, zeros where a row is padding."""
-    call = _calls().gather
+    calls = _calls()
     _check_order(order)
-    if _asks_gradient(x):
+    if calls.asks(x):
         _need(out is None, "out cannot be given where a gradient is asked for")
         return _functions()["gather"].apply(x, order, stream)
-    return _run(call, (x, order.rows, order.slots, out), stream)
+    return _run(calls.gather, (x, order.rows, order.slots, out), stream)
 
 
 def expert_gather_backward(grad, order: ExpertOrder, out=None, stream=None):
@@ -193,12 +189,12 @@ def expert_combine(rows, order: ExpertOrder, weights=None, out=None, stream=None
     sum over its choices of weight times row, in 32 bits and in order of the
     choices, rounded once.  weights is [T, K], float32 or of the rows' type
     (None: ones); dropped choices add nothing, whatever their weight."""
-    call = _calls().combine
+    calls = _calls()
     _check_order(order)
-    if _asks_gradient(rows, weights):
+    if calls.asks(rows, weights):
         _need(out is None, "out cannot be given where a gradient is asked for")
         return _functions()["combine"].apply(rows, order, weights, stream)
-    return _run(call, (rows, order.rows, order.slots, weights, out), stream)
+    return _run(calls.combine, (rows, order.rows, order.slots, weights, out), stream)
 
 
 def expert_combine_backward(grad, rows, order: ExpertOrder, weights, stream=None):
@@ -213,11 +209,9 @@ def expert_combine_backward(grad, rows, order: ExpertOrder, weights, stream=None
 # Rotary positions
 # ---------------------------------------------------------------------------
 
-def _turned(x, positions, freqs, axes, interleaved, scale, out, inverse, stream):
-    many = isinstance(x, (tuple, list))
-    xs = tuple(x) if many else (x,)
-    outs = out if out is None else tuple(out) if many else (out,)
-    got = _run(_calls().rotary, (xs, positions, freqs, axes, interleaved, scale, outs, inverse),
+def _turned(calls, many, xs, positions, freqs, axes, interleaved, scale, out, inverse, stream):
+    outs = None if out is None else tuple(out) if many else (out,)
+    got = _run(calls.rotary, (xs, positions, freqs, axes, interleaved, scale, outs, inverse),
                stream)
     return got if many else got[0]
 
@@ -233,20 +227,23 @@ def rotary(x, positions, freqs, axes=None, interleaved: bool = False, scale: flo
     one axis, or [A, ...] for A axes; axes is int32 [P], None for the first
     axis; a pair of an axis that is not there is not turned.  freqs is float32
     or float64; angles are held in 64 bits.  `out` may be x itself."""
-    _calls()
+    calls = _calls()
     many = isinstance(x, (tuple, list))
-    if _asks_gradient(*(x if many else (x,))):
+    xs = tuple(x) if many else (x,)
+    if calls.asks(xs):
         _need(out is None, "out cannot be given where a gradient is asked for")
         how = positions, freqs, axes, interleaved, scale
-        got = _functions()["rotary"].apply(how, stream, *(x if many else (x,)))
+        got = _functions()["rotary"].apply(how, stream, *xs)
         return got if many else got[0]
-    return _turned(x, positions, freqs, axes, interleaved, scale, out, False, stream)
+    return _turned(calls, many, xs, positions, freqs, axes, interleaved, scale, out, False, stream)
 
 
 def rotary_backward(grad, positions, freqs, axes=None, interleaved: bool = False,
                     scale: float = 1.0, out=None, stream=None):
     """Gradient of rotary's x from that of its result: turned the other way."""
-    return _turned(grad, positions, freqs, axes, interleaved, scale, out, True, stream)
+    many = isinstance(grad, (tuple, list))
+    return _turned(_calls(), many, tuple(grad) if many else (grad,), positions, freqs, axes,
+                   interleaved, scale, out, True, stream)
 
 
 def rotary_axes(sections, interleaved: bool = False, device=None):
@@ -342,14 +339,15 @@ def _functions() -> dict:
         def forward(ctx, how, stream, *xs):
             ctx.how = how
             positions, freqs, axes, interleaved, scale = how
-            return _turned(xs, positions, freqs, axes, interleaved, scale, None, False, stream)
+            return _turned(call, True, xs, positions, freqs, axes, interleaved, scale, None,
+                           False, stream)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, *grads):
             positions, freqs, axes, interleaved, scale = ctx.how
-            got = _turned([adjacent(g) for g in grads], positions, freqs, axes, interleaved,
-                          scale, None, True, None)
+            got = _turned(call, True, tuple(adjacent(g) for g in grads), positions, freqs, axes,
+                          interleaved, scale, None, True, None)
             return (None, None, *got)
 
     _made.update(gather=Gather, combine=Combine, rotary=Rotary)
