@@ -18,9 +18,7 @@ namespace {
 
 // Threads of a workgroup, measured on 16384 tokens of 8 choices, 8 KiB a row:
 // gather 224 us with 256 and 230 with 128, combine 212 and 200; at other sizes
-// (2 to 14 KiB a row) the two differ by up to 3% the same way.  A gather whose
-// waves share choices takes 212 us with 512 threads and 217 with 256, rows of
-// 4 KiB 103 and 100.
+// (2 to 14 KiB a row) the two differ by up to 3% the same way.
 constexpr int kGatherThreads = 256;
 constexpr int kCombineThreads = 128;
 constexpr int kBackwardThreads = 256;
@@ -296,17 +294,27 @@ int64_t pad_blocks(int64_t capacity) {
     return (capacity + kRows - 1) / kRows;
 }
 
-// Waves that share a token's choices in the gather, where rows are whole cache
-// lines (16384 tokens of 8 choices, 8 KiB a row: 217 us, 224 with one wave for all;
-// 4 KiB 100 and 102).  Otherwise one wave writes them all, and the workgroup's
-// waves write next to each other, so that shared lines come together (rows of
-// 4094 bytes: 131 us, 183 with four).
-constexpr int kGatherShares = 4;
+// What the caches can still hold of rows that were written just before.
+constexpr int64_t kMoveCached = int64_t(96) << 20;
+
+// Waves that share a token's choices in the gather.  With few choices for each,
+// a wave's stores end sooner; with one choice for each, tokens that come from
+// memory and not from the caches are waited for.  Measured with one, two and four
+// waves, rows of whole cache lines: tokens of up to 67 MB (8192 x 6 rows of 8 KiB)
+// 75, 73, 67 us, (16384 x 5 of 4 KiB) 63, 61, 56; of 134 MB (16384 x 8 of 8 KiB,
+// with the order) 236, 230, 225, (8192 x 6 of 16 KiB) 171, 162, 179, (8192 x 4)
+// 121, 112, 135.  Where rows share lines, one wave writes them all, and the
+// workgroup's waves write next to each other (16384 x 8 rows of 4094 bytes: 131 us,
+// 183 with four).
+int gather_shares(const MoveArgs &a, int64_t size) {
+    if (!a.whole_lines || a.choices < 4) return 1;
+    return a.choices < 8 && a.tokens * a.dim > kMoveCached / size ? 2 : 4;
+}
 
 template <typename T, int N> int gather_n(const MoveArgs &a, hipStream_t s) {
     Cut c;
     bool fits;
-    const int shares = a.whole_lines && a.choices >= kGatherShares ? kGatherShares : 1;
+    const int shares = gather_shares(a, sizeof(T));
     const bool wave = by_waves<N, kGatherThreads>(a, shares, &c, &fits);
     if (!fits) return BMMC_ERR_UNSUPPORTED;
     const int64_t pads = pad_blocks(a.capacity);
@@ -319,8 +327,10 @@ template <typename T, int N> int gather_n(const MoveArgs &a, hipStream_t s) {
             launch(bmmc_expert_gather_kernel<T, N, false, 1>);
         else if (shares == 1)
             launch(bmmc_expert_gather_kernel<T, N, true, 1>);
+        else if (shares == 2)
+            launch(bmmc_expert_gather_kernel<T, N, true, 2>);
         else
-            launch(bmmc_expert_gather_kernel<T, N, true, kGatherShares>);
+            launch(bmmc_expert_gather_kernel<T, N, true, 4>);
     });
 }
 
@@ -375,8 +385,6 @@ template <typename T, int N> int combine_backward_n(const MoveArgs &a, hipStream
 // read through them, more are streamed in.  Combine and its backward pass, 8
 // choices of 4 KiB a token: 67 MB of rows 14.0 and 24.2 us cached, 16.0 and 28.0
 // streamed; 98 MB 20.4 and 41.4, 20.5 and 39.1; 134 MB 29.4 and 55.1, 26.7 and 51.6.
-constexpr int64_t kMoveCached = int64_t(96) << 20;
-
 MoveArgs with_hints(MoveArgs a, int type) {
     constexpr int64_t kLine = 128;
     const int64_t size = type == BMMC_F32 ? 4 : 2;
