@@ -206,6 +206,39 @@ def test_combine_ignores_what_is_not_held():
                                  w).isnan().cpu().any(1).tolist() == [True, False, True]
 
 
+@pytest.mark.parametrize("case", [  # tokens, choices, width: rows by expert of 98 MiB and more
+    (13000, 6, 4096), (13000, 6, 4095), (14000, 8, 1024), (30000, 2, 1024)], ids=str)
+def test_moves_of_more_than_the_caches_hold(case):
+    """Rows that are streamed, checked on the device: sums in 64 bits."""
+    tokens, choices, width = case
+    g = torch.Generator(device=DEV).manual_seed(width)
+    experts = torch.rand(tokens, 24, device=DEV, generator=g).topk(choices, dim=1).indices
+    experts = torch.where(torch.rand(tokens, choices, device=DEV, generator=g) < 0.1, -1, experts)
+    order = bm.expert_order(experts.contiguous(), 24, align=16)
+    rows, slots = order.rows.long(), order.slots.long()
+    held, at = slots >= 0, slots.clamp(min=0)
+    x = torch.randn(tokens, width, device=DEV, generator=g).to(torch.bfloat16)
+    w = torch.rand(tokens, choices, device=DEV, generator=g)
+    y = bm.expert_gather(x, order)
+    assert torch.equal(y[held], x[at[held] // choices]) and not bool(y[~held].any())
+    y = torch.randn(y.shape, device=DEV, generator=g).to(torch.bfloat16)
+    got = bm.expert_combine(y, order, w)
+    grad_y, grad_w = bm.expert_combine_backward(x, y, order, w)
+    want, size = (torch.zeros(tokens, width, dtype=torch.float64, device=DEV) for _ in range(2))
+    for k in range(choices):
+        one = y[rows[:, k].clamp(min=0)].double() * (rows[:, k] >= 0)[:, None]
+        term = one * w[:, k, None].double()
+        want += term
+        size += term.abs()
+        dots = x.double() * one
+        off = (grad_w[:, k].double() - dots.sum(1)).abs()
+        assert bool((off <= (width + 10) * U32 * dots.abs().sum(1) + U32 * dots.sum(1).abs()).all())
+    u = 2.0 ** -8
+    assert bool(((got.double() - want).abs() <= choices * U32 * size * (1 + u) + u * want.abs()).all())
+    want = x[at // choices].float() * w.reshape(-1)[at][:, None]
+    assert torch.equal(grad_y[held], want.to(torch.bfloat16)[held]) and not bool(grad_y[~held].any())
+
+
 def test_wrong_rows_are_skipped():
     """Rows of an order that point nowhere are skipped, not followed."""
     order, rows, slots = _make_order(40, 4, 8, 0.0, 1, 3)
@@ -423,6 +456,28 @@ def test_rotary_layouts():
     one = bm.rotary(x, positions[0], freqs)
     assert torch.equal(one, bm.rotary(x, positions[:1], freqs))
     assert bm.rotary(x[:0], positions[:, :0], freqs, axes).shape == (0, 50, 6, 40)
+
+
+def test_turns_of_more_than_the_caches_hold():
+    """Heads that are streamed give what parts of them give."""
+    g = torch.Generator(device=DEV).manual_seed(34)
+    both = torch.randn(12000, 28 * 128, device=DEV, generator=g).to(torch.bfloat16)
+    q, k, v = (t.unflatten(1, (-1, 128)) for t in both.split([20 * 128, 4 * 128, 4 * 128], dim=1))
+    positions, freqs = torch.randint(0, 9000, (3, 12000), generator=_gen(35)).to(DEV), _freqs(50).to(DEV)
+    axes = bm.rotary_axes([20, 15, 15], device=DEV)
+    want = [bm.rotary((q[a:a + 1000], k[a:a + 1000]), positions[:, a:a + 1000].contiguous(), freqs, axes)
+            for a in range(0, 12000, 1000)]
+    got = bm.rotary((q, k), positions, freqs, axes)
+    for i in range(2):
+        assert torch.equal(got[i], torch.cat([w[i] for w in want]))
+    caches = [torch.zeros(1500, 8, 4, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    table = torch.randperm(1500, generator=_gen(36)).to(torch.int32).reshape(3, 500).to(DEV)
+    place = torch.arange(12000, device=DEV)
+    out = bm.cache_append(k, v, *caches, table, place % 4000, sequences=(place // 4000).to(torch.int32),
+                          freqs=freqs, axes=axes, turns=positions, q=q)
+    page = table[place // 4000, place % 4000 // 8].long()
+    assert torch.equal(out, got[0]) and torch.equal(caches[0][page, place % 8], got[1])
+    assert torch.equal(caches[1][page, place % 8], v)
 
 
 def test_rotary_of_far_positions():
