@@ -268,9 +268,12 @@ __global__ void __launch_bounds__(kBackwardThreads)
         static_cast<T *>(a.grad_weights)[i] = (T)dot;
 }
 
-// Whether each wave is one token's: where that leaves at most a fifth of the
-// lanes idle, or where the vectors of all tokens pass the 31 bits of a
-// quotient.  *fits is false where the waves pass them too.
+// Whether each wave is one token's: where that leaves at most two fifths of the
+// lanes idle, or where the vectors of all tokens pass the 31 bits of a quotient.
+// 8192 tokens of 8 choices, by waves and by lanes in turn: combine of rows of 8
+// vectors 7.2 and 5.4 us, 25 vectors 8.5 and 7.9, 72 vectors 15.0 and 14.9, 88
+// vectors 17.8 and 17.9; gather 7.7 and 5.1, 8.5 and 8.0, 17.7 and 16.6, 18.6 and
+// 20.0.  *fits is false where the waves pass them too.
 template <int N, int THREADS>
 bool by_waves(const MoveArgs &a, int shares, Cut *c, bool *fits) {
     constexpr int64_t kMost = int64_t(1) << 31;
@@ -278,7 +281,7 @@ bool by_waves(const MoveArgs &a, int shares, Cut *c, bool *fits) {
     const int64_t vectors = (a.dim + N - 1) / N, waves = (vectors + 63) / 64;
     c->vectors = (uint32_t)vectors;
     *fits = a.tokens * waves < kMost - THREADS;
-    if (vectors * 5 >= waves * 64 * 4 || a.tokens * vectors >= kMost - THREADS) {
+    if (vectors * 5 >= waves * 64 * 3 || a.tokens * vectors >= kMost - THREADS) {
         c->by = fast_div((uint32_t)waves);
         c->parts = (uint32_t)((a.tokens * waves + kWaves - 1) / kWaves);
         return true;
