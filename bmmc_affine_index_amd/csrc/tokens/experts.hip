@@ -24,7 +24,7 @@ constexpr int kCombineThreads = 128;
 constexpr int kBackwardThreads = 256;
 // Rows of the order that one wave looks through for padding: where there is
 // much, few waves would take long over it; where there is none, many cost time
-// (131072 rows without any: 2% of the backward pass with 4 rows a wave, nothing
+// (65536 rows without any: 2% of the backward pass with 4 rows a wave, nothing
 // to be seen with 8).
 constexpr int kPadRows = 8;
 
@@ -381,7 +381,7 @@ template <typename T, int N> int combine_backward_n(const MoveArgs &a, hipStream
 
 // Rows of whole cache lines are streamed out, others written through the caches,
 // which put the lines that two rows share together: 16384 tokens of 8 choices
-// gather rows of 4094 bytes in 127 us, 146 streamed; rows of 4096 bytes in 118 us
+// gather rows of 4094 bytes in 131 us, 146 streamed; rows of 4096 bytes in 118 us
 // and 102 streamed.
 //
 // Rows by expert that the caches can still hold since they were written are
