@@ -58,6 +58,60 @@ bool apart(int64_t inner, const int64_t *sizes, const int64_t *strides, int dims
     return true;
 }
 
+// An array's steps, widest first: without those that lead nowhere.
+struct Steps {
+    int64_t inner;  // adjacent elements at each step
+    int dims = 0;
+    int64_t sizes[3], strides[3];
+
+    Steps(int64_t elements, const int64_t *n, const int64_t *s, int count) : inner(elements) {
+        for (int i = 0; i < count; ++i) {
+            if (n[i] <= 1 || s[i] == 0) continue;
+            int at = dims++;
+            for (; at > 0 && strides[at - 1] < s[i]; --at) {
+                sizes[at] = sizes[at - 1];
+                strides[at] = strides[at - 1];
+            }
+            sizes[at] = n[i];
+            strides[at] = s[i];
+        }
+    }
+    // Elements from the first to past the last of one step of the first `from`.
+    __int128 reach(int from) const {
+        __int128 r = inner;
+        for (int i = from; i < dims; ++i) r += (__int128)(sizes[i] - 1) * strides[i];
+        return r;
+    }
+};
+
+__int128 floor_div(__int128 a, int64_t b) { return a / b - (a % b < 0); }
+
+// Whether b, `off` elements from a, has an element that a has too.  Without
+// their i and j widest steps the two are compared for each difference of the
+// next step that brings their stretches together, which is one or none for
+// arrays in step; after `looks` comparisons the answer is yes.
+bool shared(const Steps &a, int i, const Steps &b, int j, __int128 off, int *looks) {
+    if (off >= a.reach(i) || -off >= b.reach(j)) return false;
+    if (i == a.dims && j == b.dims) return true;
+    if (--*looks < 0) return true;
+    const int64_t sa = i < a.dims ? a.strides[i] : 0, sb = j < b.dims ? b.strides[j] : 0;
+    const int64_t step = std::max(sa, sb);
+    const int64_t na = sa == step ? a.sizes[i] : 1, nb = sb == step ? b.sizes[j] : 1;
+    i += sa == step;
+    j += sb == step;
+    const __int128 lo = std::max<__int128>(1 - na, floor_div(-b.reach(j) - off, step) + 1);
+    const __int128 hi = std::min<__int128>(nb - 1, floor_div(a.reach(i) - off - 1, step));
+    for (__int128 k = lo; k <= hi; ++k)
+        if (shared(a, i, b, j, off + k * step, looks)) return true;
+    return false;
+}
+
+bool share(const void *p, const Steps &a, const void *q, const Steps &b, int bytes) {
+    int looks = 256;
+    const __int128 off = ((__int128)(uintptr_t)q - (__int128)(uintptr_t)p) / bytes;
+    return shared(a, 0, b, 0, off, &looks);
+}
+
 Extent matrix(const void *p, int type, int64_t rows, int64_t stride, int64_t dim) {
     return extent(p, element_bytes(type), dim, &rows, &stride, 1);
 }
@@ -119,6 +173,18 @@ int check_heads(const bmmc_heads &x, int64_t batch, int64_t tokens, int dim, int
     for (int i = 0; i < 3; ++i) same &= sizes[i] <= 1 || is[i] == os[i];
     if (!same && meet(e->in, e->out)) return BMMC_ERR_ALIAS;
     return BMMC_OK;
+}
+
+Steps steps_in(const bmmc_heads &x, int64_t batch, int64_t tokens, int dim) {
+    const int64_t sizes[3] = {batch, tokens, x.heads};
+    const int64_t strides[3] = {x.in_batch, x.in_token, x.in_head};
+    return Steps(dim, sizes, strides, 3);
+}
+
+Steps steps_out(const bmmc_heads &x, int64_t batch, int64_t tokens, int dim) {
+    const int64_t sizes[3] = {batch, tokens, x.heads};
+    const int64_t strides[3] = {x.out_batch, x.out_token, x.out_head};
+    return Steps(dim, sizes, strides, 3);
 }
 
 int check_cache(const bmmc_paged_cache &c, int64_t pages, int64_t page_size, int64_t heads,
@@ -300,12 +366,19 @@ int bmmc_rotary(const bmmc_heads *x, int count, int64_t batch, int64_t tokens, i
         const int st = check_heads(x[i], batch, tokens, head_dim, type, true, &e[i]);
         if (st != BMMC_OK) return st;
     }
-    if (count == 2) {
-        // views of one projection turned in place lie between one another
-        if (x[0].out == x[1].out) return BMMC_ERR_ALIAS;
-        for (int i = 0; i < 2; ++i)
-            if (x[i].out != x[i].in && (meet(e[i].out, e[1 - i].in) || meet(e[i].out, e[1 - i].out)))
-                return BMMC_ERR_ALIAS;
+    for (int i = 0; i < count && count == 2; ++i) {
+        const bmmc_heads &mine = x[i], &other = x[1 - i];
+        if (mine.out != mine.in) {
+            if (meet(e[i].out, e[1 - i].in) || meet(e[i].out, e[1 - i].out)) return BMMC_ERR_ALIAS;
+            continue;
+        }
+        // views of one projection turned in place lie between one another, but
+        // what one of them writes the other must neither read nor write
+        const Steps out = steps_out(mine, batch, tokens, head_dim);
+        const int bytes = element_bytes(type);
+        if (share(mine.out, out, other.in, steps_in(other, batch, tokens, head_dim), bytes) ||
+            share(mine.out, out, other.out, steps_out(other, batch, tokens, head_dim), bytes))
+            return BMMC_ERR_ALIAS;
     }
     bmmc::HeadsArgs a{x, count, head_dim, type, batch, tokens};
     return bmmc::launch_rotary(a, *rotation, static_cast<hipStream_t>(stream));

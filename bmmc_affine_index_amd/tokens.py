@@ -226,7 +226,8 @@ def rotary(x, positions, freqs, axes=None, interleaved: bool = False, scale: flo
     pairs are copied.  positions is int32 or int64, of the tokens' shape for
     one axis, or [A, ...] for A axes; axes is int32 [P], None for the first
     axis; a pair of an axis that is not there is not turned.  freqs is float32
-    or float64; angles are held in 64 bits.  `out` may be x itself."""
+    or float64; angles are held in 64 bits.  `out` may be x itself; of a pair, a
+    tensor that is turned in place shares no elements with the other."""
     calls = _calls()
     many = isinstance(x, (tuple, list))
     xs = tuple(x) if many else (x,)

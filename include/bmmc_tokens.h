@@ -146,8 +146,11 @@ typedef struct bmmc_rotation {
 
 /* Turn the heads of `count` (1 or 2) tensors of batch * tokens tokens, heads
  * of head_dim elements of `type`.  Each out is its in (same address and
- * strides, turned in place) or does not overlap it.  The gradient is the same
- * call with inverse. */
+ * strides, turned in place) or does not overlap it.  Of two tensors, one turned
+ * in place may lie between the elements of the other (views of one
+ * projection) but share none with what the other reads or writes; an out of
+ * its own lies clear of the other tensor.  BMMC_ERR_ALIAS otherwise.  The
+ * gradient is the same call with inverse. */
 int bmmc_rotary(const bmmc_heads *x, int count, int64_t batch, int64_t tokens, int head_dim,
                 int type, const bmmc_rotation *rotation, void *stream);
 

@@ -261,6 +261,95 @@ def test_rotary_of_two(host):
     assert status(_heads(out=B), _heads(x=E, out=G)) == ACCEPTED
 
 
+WIDE = dict(in_token=2048, out_token=2048)  # 8 of the 16 heads of a projection's token
+
+
+@pytest.mark.parametrize("q,k,status", [
+    # the same heads turned in place and read for a result of their own
+    (dict(out=A, **WIDE), dict(out=G, **WIDE), bm.ERR_ALIAS),
+    # in place, four of eight heads in common; one element; the next token's first head
+    (dict(out=A, **WIDE), dict(x=A + 1024, out=A + 1024, **WIDE), bm.ERR_ALIAS),
+    (dict(out=A, **WIDE), dict(x=A + 2046, out=A + 2046, **WIDE), bm.ERR_ALIAS),
+    (dict(out=A, **WIDE), dict(x=A + 2304, out=A + 2304, **WIDE), bm.ERR_ALIAS),
+    # in place, and the other's token strides are not the same
+    (dict(out=A, **WIDE), dict(x=A + 2048, out=A + 2048), bm.ERR_ALIAS),
+    # read only by the other: between its tokens, and not quite
+    (dict(out=A, **WIDE), dict(x=A + 2048, out=G, **WIDE), ACCEPTED),
+    (dict(out=A, **WIDE), dict(x=A + 2050, out=G, **WIDE), bm.ERR_ALIAS),
+    (dict(out=A, **WIDE), dict(x=A + 2048, out=G, in_token=0), ACCEPTED),
+    (dict(out=A, **WIDE), dict(x=A, out=G, in_token=0, in_head=0), bm.ERR_ALIAS),
+    # every second head, and head by head before the tokens
+    (dict(out=A, in_head=256, out_head=256, **WIDE),
+     dict(x=A + 256, out=A + 256, in_head=256, out_head=256, **WIDE), ACCEPTED),
+    (dict(out=A, in_head=256, out_head=256, **WIDE),
+     dict(x=A + 254, out=A + 254, in_head=256, out_head=256, **WIDE), bm.ERR_ALIAS),
+    (dict(out=A, in_token=128, out_token=128, in_head=1280, out_head=1280),
+     dict(x=A + 8 * 2560, out=A + 8 * 2560, in_token=128, out_token=128, in_head=1280,
+          out_head=1280), ACCEPTED),
+    (dict(out=A, in_token=128, out_token=128, in_head=1280, out_head=1280),
+     dict(x=A + 7 * 2560, out=A + 7 * 2560, in_token=128, out_token=128, in_head=1280,
+          out_head=1280), bm.ERR_ALIAS)])
+def test_rotary_of_two_that_share_heads(host, q, k, status):
+    """What one tensor reads, another turned in place must not write."""
+    for pair in ((q, k), (k, q)):
+        h = (tk.bmmc_heads * 2)(*(_heads(**p) for p in pair))
+        assert host.bmmc_rotary(h, 2, 1, 10, 128, tk.BF16, ctypes.byref(_turn()), None) == status
+
+
+def test_rotary_of_two_in_batches(host):
+    """Views of [batch, tokens, heads, size] and [batch, heads, tokens, size]."""
+    def status(at, **strides):
+        s = dict({d + n: v for n, v in strides.items() for d in ("in_", "out_")})
+        h = (tk.bmmc_heads * 2)(_heads(out=A, **s), _heads(x=A + at, out=A + at, **s))
+        return host.bmmc_rotary(h, 2, 6, 10, 128, tk.BF16, ctypes.byref(_turn()), None)
+    flat = dict(batch=10 * 2048, token=2048, head=128)
+    assert status(2048, **flat) == ACCEPTED and status(2046, **flat) == bm.ERR_ALIAS
+    loose = dict(batch=10 * 2048 + 999, token=2048, head=128)  # tokens of two entries not in step
+    assert status(2048, **loose) == ACCEPTED and status(2050, **loose) == bm.ERR_ALIAS
+    first = dict(batch=16 * 1280, token=128, head=1280)
+    assert status(8 * 2560, **first) == ACCEPTED and status(8 * 2560 - 2, **first) == bm.ERR_ALIAS
+    inside = dict(batch=128, token=6 * 2048, head=6 * 128)  # the batch within a token's heads
+    assert status(8 * 6 * 256, **inside) == ACCEPTED and status(7 * 6 * 256, **inside) == bm.ERR_ALIAS
+
+
+def test_shared_elements_by_counting(host):
+    """Small arrays at random: refused where an element that one tensor turned in
+    place writes is one that the other reads or writes, and only there."""
+    import itertools
+    import random
+    rng = random.Random(11)
+    seen = {ACCEPTED: 0, bm.ERR_ALIAS: 0}
+
+    def elements(at, strides, sizes):
+        steps = itertools.product(*(range(n) for n in sizes))
+        starts = [at + sum(i * s for i, s in zip(step, strides)) for step in steps]
+        return [x + d for x in starts for d in range(2)]
+    while min(seen.values()) < 400:
+        sizes = [(rng.randint(1, 3), rng.randint(1, 4), rng.randint(1, 3)) for _ in range(2)]
+        sizes[1] = sizes[0][:2] + sizes[1][2:]
+        strides = [tuple(rng.choice([0, 2, 3, 4, 6, 8, 12, 13, 24, 48]) for _ in range(3))
+                   for _ in range(2)]
+        if rng.random() < 0.5:
+            strides[1] = strides[0]
+        at = [400, 400 + rng.randint(-30, 30)]
+        mine, other = (elements(*t) for t in zip(at, strides, sizes))
+        want = bm.ERR_ALIAS if set(mine) & set(other) else ACCEPTED
+        names = ("batch", "token", "head")
+        q, k = (dict({d + n: v for d in ("in_", "out_") for n, v in zip(names, s)},
+                     x=A + 2 * t, out=A + 2 * t, heads=n[2]) for t, s, n in zip(at, strides, sizes))
+        k.update(out=G, out_batch=100, out_token=20, out_head=2)
+
+        def status(*pair):
+            h = (tk.bmmc_heads * 2)(*(_heads(**p) for p in pair))
+            return host.bmmc_rotary(h, len(pair), *sizes[0][:2], 2, tk.BF16,
+                                    ctypes.byref(_turn(pairs=1)), None)
+        if status(q) != ACCEPTED:
+            continue  # heads of one result among each other's are refused for themselves
+        assert len(set(mine)) == len(mine)
+        assert status(q, k) == want and status(k, q) == want
+        seen[want] += 1
+
+
 def _cache(**changes):
     c = dict(data=E, scale=None, page_stride=16 * 1024, place_stride=1024, head_stride=128,
              scale_stride=0, kind=tk.BF16)
