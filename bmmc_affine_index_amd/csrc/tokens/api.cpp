@@ -418,8 +418,16 @@ int bmmc_cache_append(const bmmc_heads *q, const bmmc_heads *k, const bmmc_heads
     for (const Extent &c : {kc, vc})
         if (meet(c, ke.in) || meet(c, ve.in) || (q && (meet(c, qe.in) || meet(c, qe.out))))
             return BMMC_ERR_ALIAS;
-    if (q && !(q->in == q->out) && (meet(qe.out, ke.in) || meet(qe.out, ve.in)))
+    if (q && q->in != q->out && (meet(qe.out, ke.in) || meet(qe.out, ve.in)))
         return BMMC_ERR_ALIAS;
+    // queries turned in place may lie between the keys and values, as in bmmc_rotary
+    if (q && q->in == q->out) {
+        const Steps out = steps_out(*q, 1, tokens, k_dim);
+        const int bytes = element_bytes(type);
+        if (share(q->out, out, k->in, steps_in(*k, 1, tokens, k_dim), bytes) ||
+            share(q->out, out, v->in, steps_in(*v, 1, tokens, v_dim), bytes))
+            return BMMC_ERR_ALIAS;
+    }
     bmmc::AppendArgs a{};
     if (q) a.q = *q;
     a.k = *k;

@@ -279,8 +279,8 @@ def cache_append(k, v, k_cache, v_cache, page_table, positions, sequences=None, 
 
     With freqs, keys are turned on the way as by ``rotary``, by `turns` ([T] or
     [A, T]) or, None, by `positions`; queries q [T, Hq, D], where given, are
-    turned into q_out (None: a new tensor; q itself: in place), which is
-    returned.  float8_e4m3fn caches store value / scale, k_scale and v_scale
+    turned into q_out (None: a new tensor; q itself: in place, where q shares no
+    elements with k and v), which is returned.  float8_e4m3fn caches store value / scale, k_scale and v_scale
     being float32, one value or one for each head; larger values become the
     type's largest.  There is no gradient."""
     return _run(_calls().append,

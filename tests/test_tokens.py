@@ -414,6 +414,29 @@ def test_two_caches_in_one_array(host):
                                   tk.BF16, None) == ACCEPTED
 
 
+@pytest.mark.parametrize("q,k,v,status", [
+    (dict(), dict(x=A + 2048), dict(x=A + 3072), ACCEPTED),  # views of one projection
+    (dict(), dict(x=A), dict(x=A + 3072), bm.ERR_ALIAS),     # the queries are the keys
+    (dict(), dict(x=A + 2048), dict(x=A), bm.ERR_ALIAS),
+    (dict(), dict(x=A + 2046), dict(x=A + 3072), bm.ERR_ALIAS),
+    (dict(), dict(x=A + 2048), dict(x=A + 3074), bm.ERR_ALIAS),  # the next token's first query
+    (dict(), dict(x=A + 2048), dict(x=A + 1024), bm.ERR_ALIAS),
+    (dict(), dict(x=A + 2048, in_token=0), dict(x=A + 2560, in_token=0), ACCEPTED),
+    (dict(), dict(x=A + 4096, in_token=0), dict(x=A + 3072), bm.ERR_ALIAS),
+    # a result of its own keeps clear of both
+    (dict(out=G), dict(x=A), dict(x=A), ACCEPTED),
+    (dict(out=B), dict(x=B + 2048), dict(x=A + 3072), bm.ERR_ALIAS)])
+def test_append_of_queries_in_place(host, q, k, v, status):
+    """Queries turned in place share no elements with the keys and values that
+    are read in the same pass."""
+    token = dict(in_token=2048, out_token=2048)
+    q, k, v = (_heads(**{"out": A, **token, "heads": n, **h}) for h, n in ((q, 8), (k, 4), (v, 4)))
+    args = {**APPEND, "table": D + (1 << 20)}
+    kc, vc = _cache(), _cache(data=E + (1 << 26))
+    assert host.bmmc_cache_append(q, k, v, kc, vc, *args.values(), _turn(), 10, 128, 128, tk.BF16,
+                                  None) == status
+
+
 # --------------------------------------------------------------------------
 # The Python calls' checks
 # --------------------------------------------------------------------------
