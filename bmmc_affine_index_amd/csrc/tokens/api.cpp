@@ -205,6 +205,12 @@ int check_cache(const bmmc_paged_cache &c, int64_t pages, int64_t page_size, int
     return BMMC_OK;
 }
 
+Steps steps_of(const bmmc_paged_cache &c, int64_t pages, int64_t page_size, int64_t heads, int dim) {
+    const int64_t sizes[3] = {pages, page_size, heads};
+    const int64_t strides[3] = {c.page_stride, c.place_stride, c.head_stride};
+    return Steps(dim, sizes, strides, 3);
+}
+
 }  // namespace
 
 extern "C" {
@@ -414,7 +420,12 @@ int bmmc_cache_append(const bmmc_heads *q, const bmmc_heads *k, const bmmc_heads
     if (st == BMMC_OK) st = check_cache(*k_cache, pages, page_size, k->heads, k_dim, type, &kc);
     if (st == BMMC_OK) st = check_cache(*v_cache, pages, page_size, k->heads, v_dim, type, &vc);
     if (st != BMMC_OK) return st;
-    // the two caches may lie in one array; nothing that is read may lie in a cache
+    // the two caches may lie in one array, with no element in both; nothing that
+    // is read may lie in a cache
+    if (pages && share(k_cache->data, steps_of(*k_cache, pages, page_size, k->heads, k_dim),
+                       v_cache->data, steps_of(*v_cache, pages, page_size, k->heads, v_dim),
+                       element_bytes(k_cache->type)))
+        return BMMC_ERR_ALIAS;
     for (const Extent &c : {kc, vc})
         if (meet(c, ke.in) || meet(c, ve.in) || (q && (meet(c, qe.in) || meet(c, qe.out))))
             return BMMC_ERR_ALIAS;

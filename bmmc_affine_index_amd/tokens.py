@@ -270,7 +270,8 @@ def cache_append(k, v, k_cache, v_cache, page_table, positions, sequences=None, 
                  q_out=None, k_scale=None, v_scale=None, stream=None):
     """Append the keys and values of T tokens to a paged cache, in place, in
     one launch.  k [T, H, D] and v [T, H, Dv] may be views; k_cache and v_cache
-    are [pages, places, H, D or Dv] with any strides between places and heads.
+    are [pages, places, H, D or Dv] with any strides between places and heads,
+    and may be views of one array that share no elements.
     Token t is at positions[t] (int32 or int64 [T]) of sequence sequences[t]
     (int32 [T]; None: token t is sequence t's): page page_table[sequence,
     position // places] (int32 [B, pages a sequence]), place position % places.

@@ -184,7 +184,8 @@ typedef struct bmmc_paged_cache {
  * and v->out and the batch strides are not used.  Heads of k and v are equal
  * in number.  q may be turned in place, between the elements of k and v (views
  * of one projection) but sharing none; an out of its own lies clear of both.
- * Nothing that is read or turned lies in a cache.  BMMC_ERR_ALIAS otherwise. */
+ * Nothing that is read or turned lies in a cache, and no element is in both
+ * caches, which may lie in one array.  BMMC_ERR_ALIAS otherwise. */
 int bmmc_cache_append(const bmmc_heads *q, const bmmc_heads *k, const bmmc_heads *v,
                       const bmmc_paged_cache *k_cache, const bmmc_paged_cache *v_cache,
                       int64_t pages, int64_t page_size, const int32_t *table, int64_t batch,

@@ -437,6 +437,37 @@ def test_append_of_queries_in_place(host, q, k, v, status):
                                   None) == status
 
 
+PLACE = 8 * 256  # elements of a place that holds both a key and a value of 8 heads
+
+
+@pytest.mark.parametrize("kc,vc,status", [
+    (dict(), dict(data=E), bm.ERR_ALIAS),                        # one cache for both
+    (dict(), dict(data=E + 63 * 16 * 2048 + 32766), bm.ERR_ALIAS),  # its last element
+    (dict(), dict(data=E + 64 * 16 * 2048), ACCEPTED),
+    # keys and values of a place, and of a head, next to each other
+    (dict(place_stride=PLACE, page_stride=16 * PLACE),
+     dict(place_stride=PLACE, page_stride=16 * PLACE, data=E + PLACE), ACCEPTED),
+    (dict(place_stride=PLACE, page_stride=16 * PLACE),
+     dict(place_stride=PLACE, page_stride=16 * PLACE, data=E + PLACE - 2), bm.ERR_ALIAS),
+    (dict(place_stride=PLACE, page_stride=16 * PLACE, head_stride=256),
+     dict(place_stride=PLACE, page_stride=16 * PLACE, head_stride=256, data=E + 256), ACCEPTED),
+    (dict(place_stride=PLACE, page_stride=16 * PLACE, head_stride=256),
+     dict(place_stride=PLACE, page_stride=16 * PLACE, head_stride=256, data=E + 254), bm.ERR_ALIAS),
+    # keys before values in one layout, the other way round in the other: pages in common
+    (dict(page_stride=32 * 1024), dict(page_stride=16 * 1024, data=E + 16 * 2048), bm.ERR_ALIAS),
+    (dict(E4, head_stride=256, place_stride=PLACE, page_stride=16 * PLACE),
+     dict(E4, head_stride=256, place_stride=PLACE, page_stride=16 * PLACE, data=E + 128), ACCEPTED),
+    (dict(E4), dict(E4, data=E + 16), bm.ERR_ALIAS)])
+def test_caches_that_share_elements(host, kc, vc, status):
+    """A key and a value never go to one address."""
+    def call(pages):
+        args = {**APPEND, "pages": pages}
+        return host.bmmc_cache_append(None, _heads(), _heads(x=A + (1 << 22)), _cache(**kc),
+                                      _cache(**vc), *args.values(), None, 10, 128, 128, tk.BF16, None)
+    assert call(64) == status
+    assert call(0) == ACCEPTED  # caches without pages share nothing
+
+
 # --------------------------------------------------------------------------
 # The Python calls' checks
 # --------------------------------------------------------------------------
