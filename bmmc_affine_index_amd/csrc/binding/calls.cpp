@@ -137,6 +137,12 @@ Tensor like(const Tensor &x) {
     return falling ? at::empty(x.sizes(), x.options()) : at::empty_like(x);
 }
 
+// A caller's tensor has been written: autograd raises where it was saved for a
+// backward pass before.  Inference tensors are never saved and count nothing.
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // A stream's handle, torch's current stream for None.
 void *stream_of(PyObject *o) {
     if (o == Py_None) return c10::hip::getCurrentHIPStream().stream();
@@ -254,6 +260,7 @@ PyObject *py_gather(PyObject *, PyObject *const *a, Py_ssize_t) {
                                        order.choices, order.capacity, x.size(1), data_type(x),
                                        out.data_ptr(), out.stride(0), stream_of(a[4])),
                      "expert_gather");
+    if (a[3] != Py_None) written(out);
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -276,6 +283,7 @@ PyObject *py_combine(PyObject *, PyObject *const *a, Py_ssize_t) {
                                         order.capacity, in.size(1), data_type(in),
                                         out.data_ptr(), out.stride(0), stream_of(a[5])),
                      "expert_combine");
+    if (a[4] != Py_None) written(out);
     return THPVariable_Wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -423,6 +431,8 @@ PyObject *py_rotary(PyObject *, PyObject *const *a, Py_ssize_t) {
         check_status(lib.rotary(heads, (int)count, nd == 4 ? lead[0] : 1, lead[nd - 3], (int)dim,
                                 data_type(x), &r, stream_of(a[8])),
                      "rotary");
+    for (Py_ssize_t i = 0; i < count && a[6] != Py_None; ++i)
+        if (PyTuple_GET_ITEM(a[6], i) != Py_None) written(outs[i]);
     if (count == 1) return Py_BuildValue("(N)", THPVariable_Wrap(outs[0]));
     return Py_BuildValue("NN", THPVariable_Wrap(outs[0]), THPVariable_Wrap(outs[1]));
     END_HANDLE_TH_ERRORS
@@ -527,6 +537,9 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t) {
                                       freqs ? &r : nullptr, tokens, (int)dim, (int)v_dim,
                                       data_type(k), stream_of(a[16])),
                      "cache_append");
+    written(k_cache);
+    written(v_cache);
+    if (given) written(*given);
     if (!q) Py_RETURN_NONE;
     return THPVariable_Wrap(q_out);
     END_HANDLE_TH_ERRORS

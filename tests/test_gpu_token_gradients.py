@@ -1,0 +1,111 @@
+"""GPU tests of the calls on token rows next to torch's autograd: what is written
+in place and what a backward pass needs later are known to it."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import bmmc_affine_index_amd as bm  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _randn(*shape, seed=0):
+    return torch.randn(*shape, generator=_gen(seed)).to(DEV)
+
+
+def _order(tokens=6, choices=2):
+    experts = torch.randint(-1, 5, (tokens, choices), generator=_gen(1))
+    return bm.expert_order(experts.to(DEV), 5, align=2)
+
+
+def _turns(tokens=6, pairs=4):
+    positions = torch.randint(0, 900, (2, tokens), generator=_gen(2)).to(DEV)
+    freqs = (10.0 ** -torch.arange(pairs, dtype=torch.float64)).to(DEV)
+    return positions, freqs, torch.tensor([0, 1] * (pairs // 2), dtype=torch.int32, device=DEV)
+
+
+def _append(k_cache, v_cache, q, q_out, stream=None):
+    positions, freqs, _ = _turns()
+    table = torch.arange(6, dtype=torch.int32, device=DEV)[:, None]
+    bm.cache_append(_randn(6, 2, 8), _randn(6, 2, 8), k_cache, v_cache, table, positions[0] % 4,
+                    freqs=freqs, q=q, q_out=q_out, stream=stream)
+
+
+# --------------------------------------------------------------------------
+# Results written in place
+# --------------------------------------------------------------------------
+
+def _rows():
+    return _order().slots.numel()
+
+
+WRITES = {  # name: (shapes of what is written, the call)
+    "gather": (lambda: [(_rows(), 8)],
+               lambda o, s: bm.expert_gather(_randn(6, 8), _order(), out=o[0], stream=s)),
+    "combine": (lambda: [(6, 8)],
+                lambda o, s: bm.expert_combine(_randn(_rows(), 8), _order(), out=o[0], stream=s)),
+    "gather backward": (lambda: [(6, 8)], lambda o, s: bm.expert_gather_backward(
+        _randn(_rows(), 8), _order(), out=o[0], stream=s)),
+    "rotary": (lambda: [(6, 2, 8)], lambda o, s: bm.rotary(
+        _randn(6, 2, 8), *_turns(), out=o[0], stream=s)),
+    "rotary in place": (lambda: [(6, 2, 8)], lambda o, s: bm.rotary(
+        o[0], *_turns(), out=o[0], stream=s)),
+    "rotary of two in place": (lambda: [(6, 2, 8), (6, 3, 8)], lambda o, s: bm.rotary(
+        tuple(o), *_turns(), out=tuple(o), stream=s)),
+    "rotary backward in place": (lambda: [(6, 2, 8)], lambda o, s: bm.rotary_backward(
+        o[0], *_turns(), out=o[0], stream=s)),
+    "append": (lambda: [(6, 4, 2, 8), (6, 4, 2, 8), (6, 2, 8)],
+               lambda o, s: _append(o[0], o[1], _randn(6, 2, 8), o[2], stream=s)),
+    "append, queries in place": (lambda: [(6, 4, 2, 8), (6, 4, 2, 8), (6, 2, 8)],
+                                 lambda o, s: _append(o[0], o[1], o[2], o[2], stream=s)),
+}
+
+
+@pytest.mark.parametrize("name", WRITES)
+def test_a_saved_tensor_that_is_written_is_noticed(name):
+    """A product keeps its factor for the gradient of the other one."""
+    shapes, call = WRITES[name]
+    for i in range(len(shapes())):
+        for stream in (None, torch.cuda.Stream()):
+            outs = [_randn(*shape, seed=3) for shape in shapes()]
+            w = torch.ones((), device=DEV, requires_grad=True)
+            loss = (outs[i] * w).sum()
+            call(outs, stream)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+            # a view of a larger tensor counts for the whole
+            big = [torch.cat([o, o]) for o in outs]
+            loss = (big[i] * w).sum()
+            call([b[:o.shape[0]] for b, o in zip(big, outs)], stream)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+
+
+@pytest.mark.parametrize("name", WRITES)
+def test_results_in_inference_tensors(name):
+    """Inference tensors have no version to count."""
+    shapes, call = WRITES[name]
+    want = [_randn(*shape, seed=3) for shape in shapes()]
+    call(want, None)
+    with torch.inference_mode():
+        outs = [_randn(*shape, seed=3) for shape in shapes()]
+        call(outs, None)
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_what_is_only_read_is_not_written():
+    order, (positions, freqs, axes) = _order(), _turns()
+    x, rows, w, q = _randn(6, 8), _randn(_rows(), 8), _randn(6, 2), _randn(6, 2, 8)
+    read = [x, rows, w, q, positions, freqs, axes, *order]
+    before = [t._version for t in read]
+    bm.expert_gather(x, order)
+    bm.expert_combine(rows, order, w)
+    bm.expert_combine_backward(x, rows, order, w)
+    bm.rotary((q, q), positions, freqs, axes)
+    assert [t._version for t in read] == before
