@@ -308,50 +308,51 @@ def _functions() -> dict:
     def adjacent(g):
         return g if g.dim() < 1 or g.stride(-1) == 1 else g.contiguous()
 
+    # Index tensors are saved as the inputs are: refilled before the backward
+    # pass they would give the gradient of another map, and torch raises.
     class Gather(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, order, stream):
-            ctx.order = order
-            return _run(call.gather, (x, order.rows, order.slots, None), stream)
+            out = _run(call.gather, (x, order.rows, order.slots, None), stream)
+            ctx.save_for_backward(order.rows, order.slots)
+            return out
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
-            return expert_gather_backward(adjacent(grad), ctx.order), None, None
+            return _run(call.combine, (adjacent(grad), *ctx.saved_tensors, None, None), None), None, None
 
     class Combine(torch.autograd.Function):
         @staticmethod
         def forward(ctx, rows, order, weights, stream):
-            ctx.order = order
-            ctx.weighed = weights is not None
-            if ctx.weighed:
-                ctx.save_for_backward(rows, weights)
-            return _run(call.combine, (rows, order.rows, order.slots, weights, None), stream)
+            out = _run(call.combine, (rows, order.rows, order.slots, weights, None), stream)
+            ctx.save_for_backward(order.rows, order.slots, weights, None if weights is None else rows)
+            return out
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
+            at, slots, weights, rows = ctx.saved_tensors
             grad = adjacent(grad)
-            if not ctx.weighed:
-                return expert_gather(grad, ctx.order), None, None, None
-            rows, weights = ctx.saved_tensors
-            grad_rows, grad_weights = expert_combine_backward(grad, rows, ctx.order, weights)
+            if weights is None:
+                return _run(call.gather, (grad, at, slots, None), None), None, None, None
+            grad_rows, grad_weights = _run(call.combine_backward, (grad, rows, at, slots, weights), None)
             return grad_rows, None, grad_weights, None
 
     class Rotary(torch.autograd.Function):
         @staticmethod
         def forward(ctx, how, stream, *xs):
-            ctx.how = how
-            positions, freqs, axes, interleaved, scale = how
-            return _turned(call, True, xs, positions, freqs, axes, interleaved, scale, None,
-                           False, stream)
+            positions, freqs, axes, *kind = how
+            got = _turned(call, True, xs, positions, freqs, axes, *kind, None, False, stream)
+            ctx.save_for_backward(positions, freqs, axes)
+            ctx.kind = kind
+            return got
 
         @staticmethod
         @once_differentiable
         def backward(ctx, *grads):
-            positions, freqs, axes, interleaved, scale = ctx.how
-            got = _turned(call, True, tuple(adjacent(g) for g in grads), positions, freqs, axes,
-                          interleaved, scale, None, True, None)
+            got = _turned(call, True, tuple(adjacent(g) for g in grads), *ctx.saved_tensors, *ctx.kind,
+                          None, True, None)
             return (None, None, *got)
 
     _made.update(gather=Gather, combine=Combine, rotary=Rotary)

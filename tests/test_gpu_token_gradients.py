@@ -109,3 +109,54 @@ def test_what_is_only_read_is_not_written():
     bm.expert_combine_backward(x, rows, order, w)
     bm.rotary((q, q), positions, freqs, axes)
     assert [t._version for t in read] == before
+
+
+# --------------------------------------------------------------------------
+# What a backward pass needs
+# --------------------------------------------------------------------------
+
+def _graph(name):
+    """(the loss of a call, the tensors that its gradient is made of)."""
+    order, (positions, freqs, axes) = _order(), _turns()
+    if name == "gather":
+        x = _randn(6, 8).requires_grad_()
+        return bm.expert_gather(x, order).square().sum(), [order.rows, order.slots]
+    rows = _randn(_rows(), 8).requires_grad_()
+    if name == "combine":
+        w = _randn(6, 2).requires_grad_()
+        return bm.expert_combine(rows, order, w).square().sum(), [order.rows, order.slots, rows, w]
+    if name == "combine without weights":
+        return bm.expert_combine(rows, order).square().sum(), [order.rows, order.slots]
+    q = _randn(6, 2, 8).requires_grad_()
+    pair = bm.rotary((q, q * 2), positions, freqs, axes)
+    return sum(t.square().sum() for t in pair), [positions, freqs, axes]
+
+
+@pytest.mark.parametrize("name,count", [("gather", 2), ("combine", 4), ("combine without weights", 2),
+                                        ("rotary", 3)])
+def test_a_backward_pass_notices_changed_inputs(name, count):
+    """An order, positions, frequencies or axes that are refilled before the
+    backward pass would give the gradient of another map."""
+    loss, _ = _graph(name)
+    loss.backward()
+    for i in range(count):
+        loss, needed = _graph(name)
+        assert len(needed) == count
+        with torch.no_grad():
+            needed[i].add_(0)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+
+
+def test_a_graph_is_let_go_with_what_it_kept():
+    """Nothing that a backward pass needs outlives the graph, and a second pass
+    over a graph that was not retained raises, as torch's operations do."""
+    import weakref
+    loss, needed = _graph("rotary")
+    loss.backward(retain_graph=True)
+    loss.backward()
+    with pytest.raises(RuntimeError, match="second time"):
+        loss.backward()
+    kept = [weakref.ref(t) for t in needed]
+    del needed
+    assert all(r() is None for r in kept)
