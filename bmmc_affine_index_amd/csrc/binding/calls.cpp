@@ -137,6 +137,13 @@ Tensor like(const Tensor &x) {
     return falling ? at::empty(x.sizes(), x.options()) : at::empty_like(x);
 }
 
+bool asks_gradient(const Tensor &t) { return t.requires_grad() && c10::GradMode::is_enabled(); }
+
+// A caller's tensor that is written has no gradient to ask for: no call makes it.
+void check_written(const Tensor &t, const char *what) {
+    TORCH_CHECK_VALUE(!asks_gradient(t), what, " must not ask for a gradient");
+}
+
 // A caller's tensor has been written: autograd raises where it was saved for a
 // backward pass before.  Inference tensors are never saved and count nothing.
 void written(const Tensor &t) {
@@ -231,8 +238,7 @@ Tensor out_of(PyObject *o, int64_t rows, const Tensor &x) {
     TORCH_CHECK_VALUE(out.scalar_type() == x.scalar_type() && out.size(0) == rows &&
                           out.size(1) == x.size(1),
                       "out must be [", rows, ", ", x.size(1), "] of the input's type");
-    TORCH_CHECK_VALUE(!(out.requires_grad() && c10::GradMode::is_enabled()),
-                      "out must not ask for a gradient");
+    check_written(out, "out");
     return out;
 }
 
@@ -418,15 +424,16 @@ PyObject *py_rotary(PyObject *, PyObject *const *a, Py_ssize_t) {
     r.interleaved = truth(a[4]);
     r.scale = real(a[5]);
     r.inverse = truth(a[7]);
-    on_device(*positions, freqs, axes);
     Tensor outs[2];
     bmmc_heads heads[2];
     for (Py_ssize_t i = 0; i < count; ++i) {
         PyObject *o = a[6] == Py_None ? Py_None : PyTuple_GET_ITEM(a[6], i);
         outs[i] = o == Py_None ? like(*xs[i]) : tensor(o, "out");
+        check_written(outs[i], "out");
         heads[i] = heads_of(*xs[i], &outs[i], "x");
         on_device(*xs[i], outs[i]);
     }
+    on_device(*positions, freqs, axes);
     if (x.numel())
         check_status(lib.rotary(heads, (int)count, nd == 4 ? lead[0] : 1, lead[nd - 3], (int)dim,
                                 data_type(x), &r, stream_of(a[8])),
@@ -485,9 +492,11 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t) {
     TORCH_CHECK_VALUE(dim > 0 && dim <= BMMC_MAX_HEAD_DIM && v_dim > 0 &&
                           v_dim <= BMMC_MAX_HEAD_DIM,
                       "heads may have up to ", BMMC_MAX_HEAD_DIM, " elements");
-    TORCH_CHECK_VALUE(!(c10::GradMode::is_enabled() &&
-                        (k.requires_grad() || v.requires_grad() || (q && q->requires_grad()))),
+    TORCH_CHECK_VALUE(!(asks_gradient(k) || asks_gradient(v) || (q && asks_gradient(*q))),
                       "cache_append has no gradient: call it under no_grad");
+    check_written(k_cache, "k_cache");
+    check_written(v_cache, "v_cache");
+    if (given) check_written(*given, "q_out");
     const bmmc_paged_cache kc = paged(k_cache, k, k_scale, "k_cache");
     const bmmc_paged_cache vc = paged(v_cache, v, v_scale, "v_cache");
     TORCH_CHECK_VALUE(k_cache.size(0) == v_cache.size(0) && k_cache.size(1) == v_cache.size(1) &&

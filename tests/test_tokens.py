@@ -576,6 +576,29 @@ def test_append_calls_refuse(changes):
         _append(**changes)
 
 
+def _asks(*shape, dtype=None):
+    return torch.zeros(*shape, dtype=dtype, requires_grad=True)
+
+
+WRITTEN = [  # calls that write into a tensor `t`, with its shape
+    ((8, 8), lambda t: bm.expert_gather(torch.zeros(4, 8), _order(), out=t)),
+    ((4, 8), lambda t: bm.expert_combine(torch.zeros(8, 8), _order(), out=t)),
+    ((4, 8), lambda t: bm.expert_gather_backward(torch.zeros(8, 8), _order(), out=t)),
+    ((4, 2, 8), lambda t: bm.rotary(torch.zeros(4, 2, 8), POS, F, out=t)),
+    ((4, 2, 8), lambda t: bm.rotary((torch.zeros(4, 2, 8),) * 2, POS, F, out=(None, t))),
+    ((4, 2, 8), lambda t: bm.rotary_backward(torch.zeros(4, 2, 8), POS, F, out=t)),
+    ((4, 2, 8), lambda t: _append(freqs=F, q=torch.zeros(4, 2, 8), q_out=t)),
+    ((3, 4, 2, 8), lambda t: _append(k_cache=t)), ((3, 4, 2, 8), lambda t: _append(v_cache=t))]
+
+
+@pytest.mark.parametrize("shape,call", WRITTEN)
+def test_tensors_that_ask_for_a_gradient_are_not_written(shape, call):
+    with pytest.raises(ValueError, match="must not ask for a gradient"):
+        call(_asks(*shape))
+    with torch.no_grad(), pytest.raises(ValueError, match="device"):  # nothing else is wrong
+        call(_asks(*shape))
+
+
 def test_host_tensors_are_refused():
     """Everything else in order: there is no path for host memory."""
     for call in (lambda: bm.expert_order(torch.zeros(4, 2, dtype=torch.int64), 3),
