@@ -431,9 +431,9 @@ PyObject *py_rotary(PyObject *, PyObject *const *a, Py_ssize_t) {
         outs[i] = o == Py_None ? like(*xs[i]) : tensor(o, "out");
         check_written(outs[i], "out");
         heads[i] = heads_of(*xs[i], &outs[i], "x");
-        on_device(*xs[i], outs[i]);
     }
     on_device(*positions, freqs, axes);
+    for (Py_ssize_t i = 0; i < count; ++i) on_device(*xs[i], outs[i]);
     if (x.numel())
         check_status(lib.rotary(heads, (int)count, nd == 4 ? lead[0] : 1, lead[nd - 3], (int)dim,
                                 data_type(x), &r, stream_of(a[8])),
