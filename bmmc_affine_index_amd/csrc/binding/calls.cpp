@@ -144,6 +144,12 @@ void check_written(const Tensor &t, const char *what) {
     TORCH_CHECK_VALUE(!asks_gradient(t), what, " must not ask for a gradient");
 }
 
+// An input whose gradient no call makes; asking for it would lose it.
+void check_constant(const Tensor *t, const char *what) {
+    TORCH_CHECK_VALUE(!t || !asks_gradient(*t), what,
+                      " has no gradient: detach it, or call under no_grad");
+}
+
 // A caller's tensor has been written: autograd raises where it was saved for a
 // backward pass before.  Inference tensors are never saved and count nothing.
 void written(const Tensor &t) {
@@ -421,6 +427,7 @@ PyObject *py_rotary(PyObject *, PyObject *const *a, Py_ssize_t) {
     TORCH_CHECK_VALUE(positions, "positions are needed");
     const Tensor &freqs = tensor(a[2], "freqs"), *axes = maybe(a[3], "axes");
     bmmc_rotation r = rotation_of(positions, lead, freqs, axes, dim);
+    check_constant(&freqs, "freqs");
     r.interleaved = truth(a[4]);
     r.scale = real(a[5]);
     r.inverse = truth(a[7]);
@@ -494,6 +501,9 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t) {
                       "heads may have up to ", BMMC_MAX_HEAD_DIM, " elements");
     TORCH_CHECK_VALUE(!(asks_gradient(k) || asks_gradient(v) || (q && asks_gradient(*q))),
                       "cache_append has no gradient: call it under no_grad");
+    check_constant(freqs, "freqs");
+    check_constant(k_scale, "k_scale");
+    check_constant(v_scale, "v_scale");
     check_written(k_cache, "k_cache");
     check_written(v_cache, "v_cache");
     if (given) check_written(*given, "q_out");

@@ -228,13 +228,15 @@ def rotary(x, positions, freqs, axes=None, interleaved: bool = False, scale: flo
     pairs are copied.  positions is int32 or int64, of the tokens' shape for
     one axis, or [A, ...] for A axes; axes is int32 [P], None for the first
     axis; a pair of an axis that is not there is not turned.  freqs is float32
-    or float64; angles are held in 64 bits.  `out` may be x itself; of a pair, a
-    tensor that is turned in place shares no elements with the other."""
+    or float64 and has no gradient; angles are held in 64 bits.  `out` may be x
+    itself; of a pair, a tensor that is turned in place shares no elements with
+    the other."""
     calls = _calls()
     many = isinstance(x, (tuple, list))
     xs = tuple(x) if many else (x,)
     if calls.asks(xs):
         _need(out is None, "out cannot be given where a gradient is asked for")
+        _need(not calls.asks(freqs), "freqs has no gradient: detach it, or call under no_grad")
         how = positions, freqs, axes, interleaved, scale
         got = _functions()["rotary"].apply(how, stream, *xs)
         return got if many else got[0]

@@ -599,6 +599,24 @@ def test_tensors_that_ask_for_a_gradient_are_not_written(shape, call):
         call(_asks(*shape))
 
 
+@pytest.mark.parametrize("name,call", [
+    ("freqs", lambda: bm.rotary(torch.zeros(4, 2, 8), POS, _asks(4))),
+    ("freqs", lambda: bm.rotary(_asks(4, 2, 8), POS, _asks(4, dtype=torch.float64))),
+    ("freqs", lambda: bm.rotary((torch.zeros(4, 2, 8), _asks(4, 2, 8)), POS, _asks(4))),
+    ("freqs", lambda: bm.rotary_backward(torch.zeros(4, 2, 8), POS, _asks(4))),
+    ("freqs", lambda: _append(freqs=_asks(4))),
+    ("k_scale", lambda: _append(k_cache=torch.zeros(3, 4, 2, 8).to(F8), k_scale=_asks(2),
+                                v_cache=torch.zeros(3, 4, 2, 8).to(F8), v_scale=torch.ones(2))),
+    ("v_scale", lambda: _append(k_cache=torch.zeros(3, 4, 2, 8).to(F8), k_scale=torch.ones(1),
+                                v_cache=torch.zeros(3, 4, 2, 8).to(F8), v_scale=_asks(1)))])
+def test_gradients_that_are_not_made_are_refused(name, call):
+    """There is no gradient of the frequencies or of a cache's scales."""
+    with pytest.raises(ValueError, match=name + " has no gradient"):
+        call()
+    with torch.no_grad(), pytest.raises(ValueError, match="device"):  # nothing else is wrong
+        call()
+
+
 def test_host_tensors_are_refused():
     """Everything else in order: there is no path for host memory."""
     for call in (lambda: bm.expert_order(torch.zeros(4, 2, dtype=torch.int64), 3),
