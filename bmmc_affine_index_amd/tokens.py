@@ -139,6 +139,11 @@ def _need(ok, what: str) -> None:
         raise ValueError(what)
 
 
+def _constant(calls, what: str, *tensors) -> None:
+    """Refuse an input whose gradient no call makes; asking for it would lose it."""
+    _need(not calls.asks(*tensors), what + " has no gradient: detach it, or call under no_grad")
+
+
 # ---------------------------------------------------------------------------
 # Tokens by expert
 # ---------------------------------------------------------------------------
@@ -180,10 +185,11 @@ def expert_gather(x, order: ExpertOrder, out=None, stream=None):
 
 def expert_gather_backward(grad, order: ExpertOrder, out=None, stream=None):
     """Gradient of expert_gather's x: [T, D], the sum of each token's rows of
-    grad [R, D], in 32 bits."""
-    call = _calls().combine
+    grad [R, D], in 32 bits.  It has no gradient of its own."""
+    calls = _calls()
     _check_order(order)
-    return _run(call, (grad, order.rows, order.slots, None, out), stream)
+    _constant(calls, "grad", grad)
+    return _run(calls.combine, (grad, order.rows, order.slots, None, out), stream)
 
 
 def expert_combine(rows, order: ExpertOrder, weights=None, out=None, stream=None):
@@ -201,10 +207,12 @@ def expert_combine(rows, order: ExpertOrder, weights=None, out=None, stream=None
 
 def expert_combine_backward(grad, rows, order: ExpertOrder, weights, stream=None):
     """Gradients of expert_combine: (of the rows [R, D], of the weights
-    [T, K]) from grad [T, D]."""
-    call = _calls().combine_backward
+    [T, K]) from grad [T, D].  They have no gradients of their own; rows and
+    weights may be the forward pass's, which ask for one."""
+    calls = _calls()
     _check_order(order)
-    return _run(call, (grad, rows, order.rows, order.slots, weights), stream)
+    _constant(calls, "grad", grad)
+    return _run(calls.combine_backward, (grad, rows, order.rows, order.slots, weights), stream)
 
 
 # ---------------------------------------------------------------------------
@@ -236,7 +244,7 @@ def rotary(x, positions, freqs, axes=None, interleaved: bool = False, scale: flo
     xs = tuple(x) if many else (x,)
     if calls.asks(xs):
         _need(out is None, "out cannot be given where a gradient is asked for")
-        _need(not calls.asks(freqs), "freqs has no gradient: detach it, or call under no_grad")
+        _constant(calls, "freqs", freqs)
         how = positions, freqs, axes, interleaved, scale
         got = _functions()["rotary"].apply(how, stream, *xs)
         return got if many else got[0]
@@ -245,10 +253,13 @@ def rotary(x, positions, freqs, axes=None, interleaved: bool = False, scale: flo
 
 def rotary_backward(grad, positions, freqs, axes=None, interleaved: bool = False,
                     scale: float = 1.0, out=None, stream=None):
-    """Gradient of rotary's x from that of its result: turned the other way."""
+    """Gradient of rotary's x from that of its result: turned the other way.  It
+    has no gradient of its own."""
+    calls = _calls()
     many = isinstance(grad, (tuple, list))
-    return _turned(_calls(), many, tuple(grad) if many else (grad,), positions, freqs, axes,
-                   interleaved, scale, out, True, stream)
+    grads = tuple(grad) if many else (grad,)
+    _constant(calls, "grad", grads)
+    return _turned(calls, many, grads, positions, freqs, axes, interleaved, scale, out, True, stream)
 
 
 def rotary_axes(sections, interleaved: bool = False, device=None):

@@ -617,6 +617,25 @@ def test_gradients_that_are_not_made_are_refused(name, call):
         call()
 
 
+@pytest.mark.parametrize("call", [
+    lambda: bm.expert_gather_backward(_asks(8, 8), _order()),
+    lambda: bm.expert_combine_backward(_asks(4, 8), torch.zeros(8, 8), _order(), torch.zeros(4, 2)),
+    lambda: bm.rotary_backward(_asks(4, 2, 8), POS, F),
+    lambda: bm.rotary_backward((torch.zeros(4, 2, 8), _asks(4, 2, 8)), POS, F)])
+def test_gradients_of_gradients_are_refused(call):
+    with pytest.raises(ValueError, match="grad has no gradient"):
+        call()
+    with torch.no_grad(), pytest.raises(ValueError, match="device"):  # nothing else is wrong
+        call()
+
+
+def test_a_backward_call_takes_the_forward_pass_tensors():
+    """Rows and weights that ask for a gradient are what a backward pass is
+    for: only the device is wrong here."""
+    with pytest.raises(ValueError, match="device"):
+        bm.expert_combine_backward(torch.zeros(4, 8), _asks(8, 8), _order(), _asks(4, 2))
+
+
 def test_host_tensors_are_refused():
     """Everything else in order: there is no path for host memory."""
     for call in (lambda: bm.expert_order(torch.zeros(4, 2, dtype=torch.int64), 3),
