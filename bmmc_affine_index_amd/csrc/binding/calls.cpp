@@ -18,6 +18,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -119,9 +120,18 @@ void check_index(const Tensor &x, const char *what) {
 const Tensor *pointer(const Tensor &t) { return &t; }
 const Tensor *pointer(const Tensor *t) { return t; }
 
+// A dual tensor's tangent would be lost: the calls have no forward-mode derivative.
+void check_tangent(const Tensor &t) {
+    TORCH_CHECK_VALUE(!t._fw_grad(0).defined() ||
+                          !c10::AutogradState::get_tls_state().get_fw_grad_mode(),
+                      "there is no forward-mode derivative: unpack the dual tensor");
+}
+
 // Tensors, and pointers to those that may be left out.
 template <typename... T> void on_device(const T &...all) {
     const Tensor *const ts[] = {pointer(all)...};
+    for (const Tensor *t : ts)
+        if (t) check_tangent(*t);
     for (const Tensor *t : ts)
         TORCH_CHECK_VALUE(!t || t->is_cuda(), "tensors must be device tensors");
     const auto current = c10::hip::current_device();
@@ -439,8 +449,7 @@ PyObject *py_rotary(PyObject *, PyObject *const *a, Py_ssize_t) {
         check_written(outs[i], "out");
         heads[i] = heads_of(*xs[i], &outs[i], "x");
     }
-    on_device(*positions, freqs, axes);
-    for (Py_ssize_t i = 0; i < count; ++i) on_device(*xs[i], outs[i]);
+    on_device(x, outs[0], xs[count - 1], outs[count - 1], *positions, freqs, axes);
     if (x.numel())
         check_status(lib.rotary(heads, (int)count, nd == 4 ? lead[0] : 1, lead[nd - 3], (int)dim,
                                 data_type(x), &r, stream_of(a[8])),
@@ -534,8 +543,6 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t) {
         TORCH_CHECK_VALUE(!q && !given && !turns && !axes, "queries, turns and axes go with freqs");
     }
     TORCH_CHECK_VALUE(q || !given, "q_out goes with q");
-    on_device(k, v, k_cache, v_cache, table, positions, sequences, freqs, axes, turns, k_scale,
-              v_scale);
     bmmc_heads qh{};
     Tensor q_out;
     if (q) {
@@ -544,8 +551,9 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t) {
                           "q must be [tokens, heads, size] as k");
         q_out = given ? *given : like(*q);
         qh = heads_of(*q, &q_out, "q");
-        on_device(*q, q_out);
     }
+    on_device(k, v, k_cache, v_cache, table, positions, sequences, freqs, axes, turns, k_scale,
+              v_scale, q, q ? &q_out : nullptr);
     const bmmc_heads kh = heads_of(k, nullptr, "k"), vh = heads_of(v, nullptr, "v");
     if (tokens)
         check_status(lib.cache_append(q ? &qh : nullptr, &kh, &vh, &kc, &vc, k_cache.size(0),
@@ -566,20 +574,23 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t) {
 
 // ---- the module ------------------------------------------------------------
 
-// asks(tensors, None or tuples of them ...): whether one asks for a gradient.
+// asks(tensors, None or tuples of them ...): whether one asks for a gradient;
+// none may have a tangent.
 bool asks(PyObject *o) {
-    if (THPVariable_Check(o)) return THPVariable_Unpack(o).requires_grad();
-    if (!PyTuple_Check(o)) return false;
-    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(o); ++i)
-        if (asks(PyTuple_GET_ITEM(o, i))) return true;
-    return false;
+    if (THPVariable_Check(o)) {
+        check_tangent(THPVariable_Unpack(o));
+        return asks_gradient(THPVariable_Unpack(o));
+    }
+    bool one = false;
+    for (Py_ssize_t i = 0; PyTuple_Check(o) && i < PyTuple_GET_SIZE(o); ++i)
+        one |= asks(PyTuple_GET_ITEM(o, i));
+    return one;
 }
 PyObject *py_asks(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (c10::GradMode::is_enabled())
-        for (Py_ssize_t i = 0; i < n; ++i)
-            if (asks(a[i])) Py_RETURN_TRUE;
-    Py_RETURN_FALSE;
+    bool one = false;
+    for (Py_ssize_t i = 0; i < n; ++i) one |= asks(a[i]);
+    return PyBool_FromLong(one);
     END_HANDLE_TH_ERRORS
 }
 

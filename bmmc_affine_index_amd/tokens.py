@@ -17,9 +17,10 @@ before the work queued on it afterwards.  Shapes, types and strides that the
 kernels do not take raise ValueError; what the library refuses raises
 BmmcError.  The gathers, combines and ``rotary`` take part in autograd when an
 input asks for a gradient, and what a call writes into a tensor that it is given
-(``out``, ``q_out``, the caches) counts as a change in place.  Index tensors are
-data: an expert, a row, a sequence, a position or a page out of range is skipped
-on the device.
+(``out``, ``q_out``, the caches) counts as a change in place.  There are no
+second and no forward-mode derivatives: a tensor that asks for one raises
+ValueError.  Index tensors are data: an expert, a row, a sequence, a position or
+a page out of range is skipped on the device.
 """
 from __future__ import annotations
 

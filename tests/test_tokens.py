@@ -636,6 +636,58 @@ def test_a_backward_call_takes_the_forward_pass_tensors():
         bm.expert_combine_backward(torch.zeros(4, 8), _asks(8, 8), _order(), _asks(4, 2))
 
 
+F8S = {n: torch.zeros(3, 4, 2, 8).to(F8) for n in ("k_cache", "v_cache")}
+SCALES = {n: torch.ones(2) for n in ("k_scale", "v_scale")}
+
+
+@pytest.mark.parametrize("shape,call", [
+    ((4, 8), lambda t: bm.expert_gather(t, _order())),
+    ((8, 8), lambda t: bm.expert_gather(torch.zeros(4, 8), _order(), out=t)),
+    ((8, 8), lambda t: bm.expert_gather_backward(t, _order())),
+    ((8, 8), lambda t: bm.expert_combine(t, _order())),
+    ((8, 8), lambda t: bm.expert_combine(t, _order(), torch.zeros(4, 2))),
+    ((4, 2), lambda t: bm.expert_combine(torch.zeros(8, 8), _order(), t)),
+    ((4, 8), lambda t: bm.expert_combine(torch.zeros(8, 8), _order(), out=t)),
+    ((4, 8), lambda t: bm.expert_combine_backward(t, torch.zeros(8, 8), _order(), torch.zeros(4, 2))),
+    ((8, 8), lambda t: bm.expert_combine_backward(torch.zeros(4, 8), t, _order(), torch.zeros(4, 2))),
+    ((4, 2), lambda t: bm.expert_combine_backward(torch.zeros(4, 8), torch.zeros(8, 8), _order(), t)),
+    ((4, 2, 8), lambda t: bm.rotary(t, POS, F)), ((4, 2, 8), lambda t: bm.rotary(t, POS, F, out=t)),
+    ((4, 2, 8), lambda t: bm.rotary((torch.zeros(4, 2, 8), t), POS, F)),
+    ((4, 2, 8), lambda t: bm.rotary(torch.zeros(4, 2, 8), POS, F, out=t)),
+    ((4, 2, 8), lambda t: bm.rotary_backward(t, POS, F)),
+    ((4,), lambda t: bm.rotary(torch.zeros(4, 2, 8), POS, t)),
+    ((4, 2, 8), lambda t: _append(k=t)), ((4, 2, 8), lambda t: _append(v=t)),
+    ((3, 4, 2, 8), lambda t: _append(k_cache=t)), ((3, 4, 2, 8), lambda t: _append(v_cache=t)),
+    ((4,), lambda t: _append(freqs=t)), ((4, 2, 8), lambda t: _append(freqs=F, q=t)),
+    ((4, 2, 8), lambda t: _append(freqs=F, q=torch.zeros(4, 2, 8), q_out=t)),
+    ((2,), lambda t: _append(**F8S, **{**SCALES, "k_scale": t})),
+    ((2,), lambda t: _append(**F8S, **{**SCALES, "v_scale": t}))])
+def test_tangents_are_refused(shape, call):
+    """There is no forward-mode derivative: a dual tensor's tangent would be lost."""
+    fw = torch.autograd.forward_ad
+    with fw.dual_level():
+        t = fw.make_dual(torch.zeros(shape), torch.ones(shape))
+        for mode in (torch.enable_grad(), torch.no_grad()):
+            with mode, pytest.raises(ValueError, match="forward-mode"):
+                call(t)
+    with pytest.raises(ValueError, match="device"):  # nothing else is wrong
+        call(t)
+
+
+def test_tangents_of_tensors_that_ask_for_a_gradient_are_refused():
+    fw = torch.autograd.forward_ad
+    with fw.dual_level():
+        def dual(*shape, asks=True):
+            return fw.make_dual(torch.zeros(shape, requires_grad=asks), torch.ones(shape))
+        for call in (lambda: bm.expert_gather(dual(4, 8), _order()),
+                     lambda: bm.expert_combine(dual(8, 8), _order()),
+                     lambda: bm.expert_combine(_asks(8, 8), _order(), dual(4, 2, asks=False)),
+                     lambda: bm.rotary((_asks(4, 2, 8), dual(4, 2, 8, asks=False)), POS, F),
+                     lambda: bm.rotary(_asks(4, 2, 8), POS, dual(4, asks=False))):
+            with pytest.raises(ValueError, match="forward-mode"):
+                call()
+
+
 def test_host_tensors_are_refused():
     """Everything else in order: there is no path for host memory."""
     for call in (lambda: bm.expert_order(torch.zeros(4, 2, dtype=torch.int64), 3),
