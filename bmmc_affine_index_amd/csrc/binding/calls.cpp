@@ -95,8 +95,11 @@ int index_type(const Tensor &t) {
     }
 }
 
-// Elements along the last dimension lie next to each other.
-bool adjacent(const Tensor &t) { return t.stride(-1) == 1 || t.size(-1) == 1; }
+// Elements along the last dimension lie next to each other; without elements
+// any stride will do (that of an expanded gradient is 0).
+bool adjacent(const Tensor &t) {
+    return t.stride(-1) == 1 || t.size(-1) == 1 || t.numel() == 0;
+}
 
 void check_matrix(const Tensor &x, const char *what) {
     TORCH_CHECK_VALUE(x.dim() == 2 && data_type(x) >= 0, what,

@@ -160,3 +160,15 @@ def test_a_graph_is_let_go_with_what_it_kept():
     kept = [weakref.ref(t) for t in needed]
     del needed
     assert all(r() is None for r in kept)
+
+
+def test_gradients_of_no_tokens():
+    """A rank without tokens: the gradient of a sum comes with strides of zero."""
+    order = bm.expert_order(torch.zeros(0, 2, dtype=torch.int64, device=DEV), 5)
+    positions, freqs, axes = _turns()
+    x, w, q = (_randn(0, *shape).requires_grad_() for shape in ((8,), (2,), (2, 8)))
+    bm.expert_combine(bm.expert_gather(x, order), order, w).sum().backward()
+    assert x.grad.shape == (0, 8) and w.grad.shape == (0, 2)
+    bm.expert_combine(x, order).sum().backward()
+    sum(t.sum() for t in bm.rotary((q, q), positions[:, :0], freqs, axes)).backward()
+    assert q.grad.shape == (0, 2, 8)

@@ -688,6 +688,20 @@ def test_tangents_of_tensors_that_ask_for_a_gradient_are_refused():
                 call()
 
 
+def test_arrays_without_elements_have_no_strides_to_check():
+    """An expanded gradient of no tokens: only the device is wrong."""
+    none = torch.zeros(()).expand(0, 8)
+    heads = torch.zeros(()).expand(0, 2, 8)
+    order = _order(tokens=0)
+    for call in (lambda: bm.expert_gather(none, order), lambda: bm.expert_combine(none, order),
+                 lambda: bm.expert_gather_backward(none, order),
+                 lambda: bm.expert_combine_backward(none, none, order, torch.zeros(0, 2)),
+                 lambda: bm.rotary_backward(heads, POS[:0], F),
+                 lambda: _append(k=heads, v=heads, positions=POS[:0])):
+        with pytest.raises(ValueError, match="device"):
+            call()
+
+
 def test_host_tensors_are_refused():
     """Everything else in order: there is no path for host memory."""
     for call in (lambda: bm.expert_order(torch.zeros(4, 2, dtype=torch.int64), 3),
