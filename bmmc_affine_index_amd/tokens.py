@@ -340,7 +340,9 @@ def _functions() -> dict:
         @staticmethod
         def forward(ctx, rows, order, weights, stream):
             out = _run(call.combine, (rows, order.rows, order.slots, weights, None), stream)
-            ctx.save_for_backward(order.rows, order.slots, weights, None if weights is None else rows)
+            # the largest array of a layer, kept where the weights' gradient needs it
+            ctx.save_for_backward(order.rows, order.slots, weights,
+                                  rows if ctx.needs_input_grad[2] else None)
             return out
 
         @staticmethod
@@ -350,8 +352,11 @@ def _functions() -> dict:
             grad = adjacent(grad)
             if weights is None:
                 return _run(call.gather, (grad, at, slots, None), None), None, None, None
-            grad_rows, grad_weights = _run(call.combine_backward, (grad, rows, at, slots, weights), None)
-            return grad_rows, None, grad_weights, None
+            if rows is None:  # any row will do: the weights' gradient is not wanted
+                rows = grad.new_empty(1, grad.shape[1]).expand(slots.shape[0], -1)
+            got = _run(call.combine_backward, (grad, rows, at, slots, weights), None)
+            wanted = [g if n else None for g, n in zip(got, ctx.needs_input_grad[::2])]
+            return wanted[0], None, wanted[1], None
 
     class Rotary(torch.autograd.Function):
         @staticmethod

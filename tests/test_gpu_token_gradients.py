@@ -172,3 +172,25 @@ def test_gradients_of_no_tokens():
     bm.expert_combine(x, order).sum().backward()
     sum(t.sum() for t in bm.rotary((q, q), positions[:, :0], freqs, axes)).backward()
     assert q.grad.shape == (0, 2, 8)
+
+
+def test_combine_keeps_rows_only_for_the_weights():
+    """The rows by expert, the largest array of a layer, are kept for the
+    weights' gradient alone; the gradients are the same whoever asks."""
+    import weakref
+    order, w = _order(), _randn(6, 2)
+    leaf, grad = _randn(_rows(), 8), _randn(6, 8)
+    want_rows, want_w = bm.expert_combine_backward(grad, leaf, order, w)
+    for weights_ask in (False, True):
+        x, wx = leaf.clone().requires_grad_(), w.clone().requires_grad_(weights_ask)
+        rows = x * 1.0
+        out = bm.expert_combine(rows, order, wx)
+        kept = weakref.ref(rows)
+        del rows
+        assert (kept() is not None) == weights_ask
+        out.backward(grad)
+        assert torch.equal(x.grad, want_rows)
+        assert torch.equal(wx.grad, want_w) if weights_ask else wx.grad is None
+    wx = w.clone().requires_grad_()
+    bm.expert_combine(leaf, order, wx).backward(grad)
+    assert torch.equal(wx.grad, want_w)
