@@ -1,8 +1,11 @@
 """GPU tests of the calls on token rows in forms that are compiled apart: 8-bit
-caches by type, pairing and width.
+caches by type, pairing and width, and the sums of the weights' gradient.
 
 Tolerances.  A rounding to a type is off by at most half a step, eps / 2 relative
-to the value."""
+to the value; n dependent 32-bit additions or fused multiply-adds are off by at
+most n 2^-24 (1 + n 2^-24) times the sum of the terms' magnitudes."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -109,3 +112,37 @@ def test_8_bit_caches(case, dtype):
     want[at, inside] = turned.clamp(-E4M3_MAX, E4M3_MAX)
     may[at, inside] = slack * (1 + 2.0 ** -4) + 2.0 ** -4 * want[at, inside].abs() + 2.0 ** -10
     assert bool(((kc.cpu().double() - want).abs() <= may).all())
+
+
+# --------------------------------------------------------------------------
+# The weights' gradient
+# --------------------------------------------------------------------------
+
+def _roundings(width, dtype):
+    """On the way of one product to its sum: a lane takes whole vectors in turn,
+    as many lanes as a power of two of them has, at most a wave, and the lanes
+    are joined two by two."""
+    n = 128 // torch.finfo(dtype).bits
+    n = n if width >= n else 1
+    vectors = -(-width // n)
+    lanes = min(64, 1 << (vectors.bit_length() - 1))
+    return -(-vectors // lanes) * n + int(math.log2(lanes)) + 1
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [1, 3, 7, 8, 9, 65, 127, 136, 513, 1001, 2048, 2880, 4100, 8192])
+def test_sums_of_the_weights_gradient(width, dtype):
+    tokens, choices = 60, 5
+    g = _gen(width)
+    experts = torch.rand(tokens, 9, generator=g).topk(choices, dim=1).indices
+    experts = torch.where(torch.rand(tokens, choices, generator=g) < 0.1, -1, experts)
+    order = bm.expert_order(experts.contiguous().to(DEV), 9, align=4)
+    rows = order.rows.cpu().long()
+    x = torch.randn(order.slots.numel(), width, generator=g).to(dtype)
+    grad = torch.randn(tokens, width, generator=g).to(dtype)
+    w = torch.rand(tokens, choices, generator=g)
+    got = bm.expert_combine_backward(grad.to(DEV), x.to(DEV), order, w.to(DEV))[1].cpu().double()
+    terms = grad.double()[:, None] * x.double()[rows.clamp(min=0)] * (rows >= 0)[..., None]
+    bound = _roundings(width, dtype) * U32 * terms.abs().sum(-1)
+    assert bool(((got - terms.sum(-1)).abs() <= bound).all())
+    assert not bool(got[rows < 0].any())
