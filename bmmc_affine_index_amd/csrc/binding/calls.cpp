@@ -3,9 +3,9 @@
 //
 // A decoding step's moves run for 3 to 5 us on the card, so that the call
 // around them is what such a step waits for.  Here a call's checks, new tensors
-// and launch take 4.9 us of host time for expert_combine of 17 tokens (13.9 us
-// with the checks in Python and the call through ctypes), 5.4 us for
-// cache_append of 64 (24.2 us), 10.1 us for an order and its gather (28.6 us); a
+// and launch take 4.8 us of host time for expert_combine of 17 tokens (13.9 us
+// with the checks in Python and the call through ctypes), 5.1 us for
+// cache_append of 64 (24.2 us), 9.3 us for an order and its gather (28.6 us); a
 // launch alone takes 2.8 to 3.4 us.
 // Python keeps what is not on that way: autograd, other streams, documentation.
 //

@@ -154,7 +154,8 @@ ExpertOrder.__doc__ = """Choices sorted by expert, all int32 device tensors:
 offsets [E + 1], the first row of each expert and the end of all rows;
 counts [E], the choices of each expert; rows [T, K], the row of each choice or
 -1 where it is dropped; slots [R], the choice t * K + k at each row or -1
-where the row is padding."""
+where the row is padding.  The moves take both as expert_order made them: a row
+whose choice has been changed in `rows` alone is not written."""
 
 
 def expert_order(experts, num_experts: int, align: int = 1, stream=None) -> ExpertOrder:

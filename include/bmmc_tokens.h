@@ -22,6 +22,10 @@
  * Index arrays are data: the kernels check every entry they use against the
  * sizes given here and skip what lies outside, so a wrong entry never reads or
  * writes out of bounds.
+ *
+ * What a call writes overlaps nothing else that it reads or writes, unless a
+ * function below allows it; rows, heads and caches that overlap are refused
+ * (BMMC_ERR_ALIAS).
  */
 #ifndef BMMC_TOKENS_H
 #define BMMC_TOKENS_H
@@ -80,18 +84,19 @@ int bmmc_expert_order(const void *experts, int index_type, int64_t n, int num_ex
 
 /* out[r] = x[slots[r] / choices], zeros where slots[r] < 0: x is tokens rows
  * of dim elements, out capacity rows.  rows (tokens * choices) and slots
- * (capacity) are bmmc_expert_order's for the tokens' choices in order.  out
- * must not overlap x (BMMC_ERR_ALIAS).  The gradient of x is
- * bmmc_expert_combine of the gradient of out without weights. */
+ * (capacity) are bmmc_expert_order's for the tokens' choices in order; a row
+ * whose choice rows no longer sends there is left as it is.  out must not
+ * overlap x.  The gradient of x is bmmc_expert_combine of the gradient of out
+ * without weights. */
 int bmmc_expert_gather(const void *x, int64_t x_stride, const int32_t *rows,
                        const int32_t *slots, int64_t tokens, int choices, int64_t capacity,
                        int64_t dim, int type, void *out, int64_t out_stride, void *stream);
 
 /* out[t] = sum over k of weights[t, k] * in[rows[t, k]] over the choices that
  * are not dropped, in order of k, held in 32 bits and rounded once; zeros for
- * a token without any.  in is capacity rows, out tokens rows.  weights is
- * tokens * choices values of weight_type (BMMC_F32 or `type`), or NULL for
- * ones. */
+ * a token without any.  in is capacity rows, out tokens rows that do not
+ * overlap it.  weights is tokens * choices values of weight_type (BMMC_F32 or
+ * `type`), or NULL for ones. */
 int bmmc_expert_combine(const void *in, int64_t in_stride, const int32_t *rows,
                         const void *weights, int weight_type, int64_t tokens, int choices,
                         int64_t capacity, int64_t dim, int type, void *out, int64_t out_stride,
@@ -102,7 +107,9 @@ int bmmc_expert_combine(const void *in, int64_t in_stride, const int32_t *rows,
  *                        where slots[r] < 0                (capacity rows)
  *   grad_weights[t, k] = sum over d of grad[t, d] * in[rows[t, k], d], 0 for a
  *                        dropped choice         (tokens * choices, weight_type)
- * in one pass; the sums are held in 32 bits and their order is fixed. */
+ * in one pass; the sums are held in 32 bits and their order is fixed.  grad_in
+ * must not overlap grad or in; as in the gather, a row whose choice rows no
+ * longer sends there is left as it is. */
 int bmmc_expert_combine_backward(const void *grad, int64_t grad_stride, const void *in,
                                  int64_t in_stride, const int32_t *rows, const int32_t *slots,
                                  const void *weights, int weight_type, int64_t tokens,
