@@ -414,18 +414,21 @@ def test_two_caches_in_one_array(host):
                                   tk.BF16, None) == ACCEPTED
 
 
+VAL = A + 2048 + 1024  # the values of a token with 8 heads of queries and 4 of keys before them
+
+
 @pytest.mark.parametrize("q,k,v,status", [
-    (dict(), dict(x=A + 2048), dict(x=A + 3072), ACCEPTED),  # views of one projection
-    (dict(), dict(x=A), dict(x=A + 3072), bm.ERR_ALIAS),     # the queries are the keys
+    (dict(), dict(x=A + 2048), dict(x=VAL), ACCEPTED),        # views of one projection
+    (dict(), dict(x=A), dict(x=VAL), bm.ERR_ALIAS),           # the queries are the keys
     (dict(), dict(x=A + 2048), dict(x=A), bm.ERR_ALIAS),
-    (dict(), dict(x=A + 2046), dict(x=A + 3072), bm.ERR_ALIAS),
-    (dict(), dict(x=A + 2048), dict(x=A + 3074), bm.ERR_ALIAS),  # the next token's first query
+    (dict(), dict(x=A + 2046), dict(x=VAL), bm.ERR_ALIAS),
+    (dict(), dict(x=A + 2048), dict(x=VAL + 2), bm.ERR_ALIAS),  # the next token's first query
     (dict(), dict(x=A + 2048), dict(x=A + 1024), bm.ERR_ALIAS),
     (dict(), dict(x=A + 2048, in_token=0), dict(x=A + 2560, in_token=0), ACCEPTED),
-    (dict(), dict(x=A + 4096, in_token=0), dict(x=A + 3072), bm.ERR_ALIAS),
+    (dict(), dict(x=A + 4096, in_token=0), dict(x=VAL), bm.ERR_ALIAS),
     # a result of its own keeps clear of both
     (dict(out=G), dict(x=A), dict(x=A), ACCEPTED),
-    (dict(out=B), dict(x=B + 2048), dict(x=A + 3072), bm.ERR_ALIAS)])
+    (dict(out=B), dict(x=B + 2048), dict(x=VAL), bm.ERR_ALIAS)])
 def test_append_of_queries_in_place(host, q, k, v, status):
     """Queries turned in place share no elements with the keys and values that
     are read in the same pass."""
