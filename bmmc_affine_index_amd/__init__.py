@@ -631,3 +631,6 @@ def transpose2d(t, stream=None, tune: bool = False):
 from .tokens import (ExpertOrder, cache_append, expert_combine, expert_combine_backward,  # noqa: E402
                      expert_gather, expert_gather_backward, expert_order, rotary, rotary_axes,
                      rotary_backward)
+# What a layer over a paged cache needs next to them (include/bmmc_layer.h).
+from .layer import (ExpertBalance, cache_attention, cache_quantize, cache_read,  # noqa: E402
+                    expert_balance, expert_balance_backward)

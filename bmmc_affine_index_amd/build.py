@@ -36,7 +36,9 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.hip")) +
                   glob.glob(os.path.join(CSRC, "kernels", "*.hip")) +
                   glob.glob(os.path.join(CSRC, "tokens", "*.cpp")) +
-                  glob.glob(os.path.join(CSRC, "tokens", "*.hip")))
+                  glob.glob(os.path.join(CSRC, "tokens", "*.hip")) +
+                  glob.glob(os.path.join(CSRC, "layer", "*.cpp")) +
+                  glob.glob(os.path.join(CSRC, "layer", "*.hip")))
 
 
 def binding_sources():

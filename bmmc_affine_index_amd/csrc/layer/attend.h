@@ -1,0 +1,327 @@
+// attend.h -- what the kernels of the attention over a paged cache share: the
+// sequences and their parts, rows of the cache, and the products' types.
+#pragma once
+
+#include "../tokens/device.h"
+#include "layer.h"
+
+namespace bmmc {
+namespace dev {
+
+constexpr float kNothing = -__builtin_inff();  // the maximum of no score
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+// ---- sequences, tiles and parts ------------------------------------------------
+
+// A sequence's new tokens: rows first .. first + count - 1 of q, the last at
+// place length - 1.  Every number from the arrays is bounded here.
+struct Sequence {
+    int32_t first, count, length, end;  // end: places that are there to be seen
+};
+
+__device__ __forceinline__ Sequence sequence_at(const AttendArgs &x, int32_t s) {
+    const int32_t tokens = (int32_t)x.a.tokens;
+    int32_t from = s, to = s + 1;
+    if (x.a.starts) {
+        from = min(max(x.a.starts[s], 0), tokens);
+        to = min(max(x.a.starts[s + 1], 0), tokens);
+    }
+    const int32_t length = max(x.a.lengths[s], 0);
+    return Sequence{from, max(to - from, 0), length, (int32_t)min((int64_t)length, x.reach)};
+}
+
+__device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) {
+    return (int32_t)(((int64_t)a + b - 1) / b);
+}
+
+__device__ __forceinline__ int32_t tiles_of(const AttendArgs &x, const Sequence &q) {
+    return (int32_t)(((int64_t)q.count * x.group + x.plan.rows - 1) / x.plan.rows);
+}
+
+// The places [from, to) that the tokens at first to last see, from a multiple
+// of 64 on.
+struct Range {
+    int32_t from, to;
+};
+__device__ __forceinline__ Range range_of(const AttendArgs &x, const Sequence &q, int32_t first,
+                                          int32_t last) {
+    Range r{0, min(q.end, last + 1)};
+    if (x.a.window) r.from = (int32_t)max((int64_t)first - x.a.window + 1, (int64_t)0) & ~63;
+    if (r.to < r.from) r.to = r.from;
+    return r;
+}
+
+__device__ __forceinline__ int32_t units_of(const AttendArgs &x, const Sequence &q) {
+    const Range r = range_of(x, q, q.length - q.count, q.length - 1);
+    return ceil_div(r.to - r.from, x.plan.unit);
+}
+
+__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+// A workgroup's piece of work; found is false behind the last.
+struct Piece {
+    bool found;
+    int32_t seq, tile, part, parts;
+    int64_t number;  // of the tile's first part among all parts
+    Sequence q;
+};
+
+// Piece `want` of all parts or, BY_TILE, the want'th tile.  Every wave looks for
+// itself, 64 sequences at a time: a prefix sum over the lanes tells which
+// sequence holds it.
+template <bool BY_TILE> __device__ __forceinline__ Piece find_piece(const AttendArgs &x, int64_t want) {
+    const int lane = threadIdx.x & 63;
+    const int32_t batch = (int32_t)x.a.batch;
+    int32_t each = 0;  // units of a part
+    if (x.plan.target) {
+        int64_t all = 0;
+        for (int32_t s = lane; s < batch; s += 64) {
+            const Sequence q = sequence_at(x, s);
+            all += (int64_t)tiles_of(x, q) * units_of(x, q);
+        }
+        all = wave_sum64(all);
+        const int64_t fair = (all + x.plan.target - 1) / x.plan.target;
+        each = (int32_t)min(max(fair, (int64_t)x.plan.least), (int64_t)1 << 30);
+    }
+    Piece p{};
+    int64_t before = 0, parts_before = 0;
+    for (int32_t s0 = 0; s0 < batch; s0 += 64) {
+        Sequence q{};
+        int32_t tiles = 0, parts = 1;
+        if (s0 + lane < batch) {
+            q = sequence_at(x, s0 + lane);
+            tiles = tiles_of(x, q);
+            if (each) parts = max(ceil_div(units_of(x, q), each), 1);
+        }
+        const int64_t mine = BY_TILE ? tiles : (int64_t)tiles * parts;
+        int64_t upto = mine, parts_upto = (int64_t)tiles * parts;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += o;
+            if (BY_TILE) {
+                const int64_t po = __shfl_up(parts_upto, d, 64);
+                if (lane >= d) parts_upto += po;
+            }
+        }
+        const int64_t from = before + upto - mine;
+        const uint64_t here = __ballot(want >= from && want < from + mine);
+        if (here) {
+            const int l = __ffsll((unsigned long long)here) - 1;
+            const int64_t in = want - __shfl(from, l, 64);
+            p.found = true;
+            p.seq = s0 + l;
+            p.parts = __builtin_amdgcn_readlane(parts, l);
+            p.q.first = __builtin_amdgcn_readlane(q.first, l);
+            p.q.count = __builtin_amdgcn_readlane(q.count, l);
+            p.q.length = __builtin_amdgcn_readlane(q.length, l);
+            p.q.end = __builtin_amdgcn_readlane(q.end, l);
+            if (BY_TILE) {
+                p.tile = __builtin_amdgcn_readfirstlane((int32_t)in);
+                p.number = parts_before + __shfl(parts_upto - (int64_t)tiles * parts, l, 64) +
+                           (int64_t)p.tile * p.parts;
+            } else {
+                p.tile = __builtin_amdgcn_readfirstlane((int32_t)in / p.parts);
+                p.part = __builtin_amdgcn_readfirstlane((int32_t)in - p.tile * p.parts);
+                p.number = want - p.part;
+            }
+            return p;
+        }
+        before += __shfl(upto, 63, 64);
+        parts_before += __shfl(parts_upto, 63, 64);
+    }
+    return p;
+}
+
+// The tokens of a tile and the places of its part that are looked at.
+struct Span {
+    int32_t first, last;  // places of the first and the last token
+    int32_t from, to;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs &x, const Piece &p) {
+    const int64_t row0 = (int64_t)p.tile * x.plan.rows;
+    const int64_t row1 = min(row0 + x.plan.rows, (int64_t)p.q.count * x.group) - 1;
+    const int32_t base = p.q.length - p.q.count;
+    Span s;
+    s.first = base + (int32_t)(row0 / x.group);
+    s.last = base + (int32_t)(row1 / x.group);
+    const Range r = range_of(x, p.q, s.first, s.last);
+    const int64_t step = (int64_t)ceil_div(ceil_div(r.to - r.from, x.plan.unit), p.parts) * x.plan.unit;
+    s.from = (int32_t)min(r.from + p.part * step, (int64_t)r.to);
+    s.to = (int32_t)min(s.from + step, (int64_t)r.to);
+    return s;
+}
+
+// Rows of no sequence, those before the first and behind the last, as zeros; by
+// workgroups of their own.
+template <typename T>
+__device__ __forceinline__ void clear_rest(const AttendArgs &x, int64_t block, int64_t blocks) {
+    if (!x.a.starts) return;
+    const int32_t tokens = (int32_t)x.a.tokens;
+    const int64_t head = min(max(x.a.starts[0], 0), tokens);
+    const int64_t tail = max((int64_t)min(max(x.a.starts[x.a.batch], 0), tokens), head);
+    const int64_t rows = head + tokens - tail;
+    for (int64_t r = block; r < rows * x.a.q_heads; r += blocks) {
+        const int64_t t = r / x.a.q_heads, h = r - t * x.a.q_heads;
+        T *out = static_cast<T *>(x.a.out) + (t < head ? t : t - head + tail) * x.a.out_token +
+                 h * x.a.out_head;
+        for (int i = threadIdx.x; i < x.a.v_dim; i += blockDim.x) out[i] = (T)0.0f;
+    }
+}
+
+// ---- elements --------------------------------------------------------------------
+
+// What stands for a row that is not there: zeros, as long as the longest head.
+__device__ const uint32_t kZeros[BMMC_MAX_HEAD_DIM] = {};
+
+// N elements of a row from element `at` on as they are in memory.  Rows have N
+// elements at least; the last vector of a row that is no whole number of them
+// ends with the row, and a vector past it is that one again: `settle` puts both
+// right when the elements are used, and not before, when they are still on
+// their way.
+template <typename E, int N> struct Raw {
+    static constexpr int kBytes = N * (int)sizeof(E);
+    static constexpr int kWords = kBytes / 4;
+    uint32_t w[kWords];
+};
+template <typename E, int N>
+__device__ __forceinline__ Raw<E, N> fetch(const uint8_t *row, int at, int dim) {
+    typedef typename Vec<uint8_t, Raw<E, N>::kBytes>::raw bytes_t;
+    typedef bytes_t packed_t __attribute__((aligned(sizeof(E))));
+    const bytes_t v =
+        *reinterpret_cast<const packed_t *>(row + min(at, dim - N) * (int)sizeof(E));
+    Raw<E, N> r;
+    __builtin_memcpy(r.w, &v, sizeof(r.w));
+    return r;
+}
+template <typename E, int N>
+__device__ __forceinline__ void settle(Raw<E, N> &r, int at, int dim) {
+    constexpr int W = Raw<E, N>::kWords;
+    if (at + N <= dim) return;
+    if (at >= dim) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) r.w[i] = 0;
+        return;
+    }
+    const int bits = (N - (dim & (N - 1))) * 8 * (int)sizeof(E);  // the same in all lanes
+    if constexpr (W == 4)
+        if (bits & 64) {
+            r.w[0] = r.w[2];
+            r.w[1] = r.w[3];
+            r.w[2] = r.w[3] = 0;
+        }
+    if (W >= 2 && (bits & 32)) {
+#pragma unroll
+        for (int i = 0; i + 1 < W; ++i) r.w[i] = r.w[i + 1];
+        r.w[W - 1] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        r.w[i] = __builtin_amdgcn_alignbit(i + 1 < W ? r.w[i + 1] : 0u, r.w[i], bits & 31);
+}
+
+// The inputs' type: vectors of 8 for the products of 16-bit types, of 4 in 32 bits.
+template <typename T> struct Product {
+    static constexpr int N = 8;
+    typedef T vec __attribute__((ext_vector_type(8)));
+};
+template <> struct Product<float> {
+    static constexpr int N = 4;
+    typedef f4 vec;
+};
+
+// Words of two elements of T (one of float) from a row's raw words.
+template <typename T, typename E, int N>
+__device__ __forceinline__ void expand(const Raw<E, N> &r, uint32_t *w) {
+    if constexpr (sizeof(E) > 1) {
+#pragma unroll
+        for (int i = 0; i < Raw<E, N>::kWords; ++i) w[i] = r.w[i];
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            typedef float f2 __attribute__((ext_vector_type(2)));
+            const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.w[i], false);
+            const f2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)r.w[i], true);
+            const float v[4] = {lo[0], lo[1], hi[0], hi[1]};
+            __builtin_memcpy(w + 4 * i, v, 16);
+        }
+    } else {  // e4m3's values are all values of both 16-bit types
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            if constexpr (__is_same(T, f16_t)) {
+                const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.w[i], 1.0f, false);
+                const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.w[i], 1.0f, true);
+                __builtin_memcpy(w + 2 * i, &lo, 4);
+                __builtin_memcpy(w + 2 * i + 1, &hi, 4);
+            } else {
+                const auto lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i], 1.0f, false);
+                const auto hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[i], 1.0f, true);
+                __builtin_memcpy(w + 2 * i, &lo, 4);
+                __builtin_memcpy(w + 2 * i + 1, &hi, 4);
+            }
+        }
+    }
+}
+
+template <typename T, typename E>
+__device__ __forceinline__ typename Product<T>::vec product_vec(const Raw<E, Product<T>::N> &r) {
+    uint32_t w[Product<T>::N * sizeof(T) / 4];
+    expand<T>(r, w);
+    typename Product<T>::vec v;
+    __builtin_memcpy(&v, w, sizeof(v));
+    return v;
+}
+
+// c += a b of 16 x 16: lane l holds row (a) or column (b) l % 16 and 8 (32 bits:
+// 1) of the inner elements, l / 16 the eighth; c's column is l % 16, its rows 4 (l / 16) + i.
+__device__ __forceinline__ f4 mfma16(Product<f16_t>::vec a, Product<f16_t>::vec b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f4 mfma16(Product<bf16_t>::vec a, Product<bf16_t>::vec b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f4 mfma16(float a, float b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f4 mfma16(Product<float>::vec a, Product<float>::vec b, f4 c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = mfma16(a[i], b[i], c);
+    return c;
+}
+
+// The results of matrix products that a branch parts from their use.  The compiler
+// has been seen to count too few cycles between the two there, so that a result
+// was read before it was written; this waits for all of them.
+__device__ __forceinline__ void wait_for(f4 &x) { asm volatile("s_nop 15" : "+v"(x)); }
+
+// Weights are made as 2^(score - maximum + kLift).  In 16 bits of 5 exponent bits
+// small ones would be lost below 2^-25 of the largest; lifted, below 2^-32.
+template <typename T> constexpr float kLift = __is_same(T, f16_t) ? 7.0f : 0.0f;
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// An unseen maximum counts as 0, so that 2^(-inf - it) is 0 and not NaN.
+__device__ __forceinline__ float settled(float m) { return m == kNothing ? 0.0f : m; }
+
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The row of a place in a cache, in elements; -1 where there is none.
+__device__ __forceinline__ int32_t page_of(const AttendArgs &x, const int32_t *table, int32_t place,
+                                           int32_t end) {
+    if (place >= end) return -1;
+    const int32_t page = table[quotient(x.by_page, (uint32_t)place)];
+    return page >= 0 && page < x.a.pages ? page : -1;
+}
+
+}  // namespace dev
+}  // namespace bmmc

@@ -1,0 +1,345 @@
+// balance.hip -- the balance loss of a router, and its gradient (gfx950).
+//
+// The loss sums p = softmax(logits) over the tokens for each expert, the
+// gradient needs each token's p again: one pass over the logits each, in which
+// a token's row lies in as many lanes of a wave as it has vectors, and its
+// maximum and sums go through exchanges among them.  A lane holds the same
+// experts of all its rows, so that the sums over tokens stay in registers until
+// the end; they leave the workgroup once and are summed by a second launch, in
+// a fixed order.  Choices are counted in LDS by whole numbers, whose order
+// does not matter.
+//
+// Bound by memory: the logits are read once for the loss, once for the gradient.
+#include <algorithm>
+
+#include "../tokens/device.h"
+#include "layer.h"
+
+namespace bmmc {
+
+namespace {
+
+constexpr int kBalanceThreads = 512;
+constexpr int kBalanceWaves = kBalanceThreads / 64;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kColumns = 64;  // experts of a workgroup that sums
+
+// C vectors of a row in each of 1 << shift lanes; past its end what weighs nothing.
+template <typename T, int C>
+__device__ __forceinline__ void load_row(const T *row, int lane, int shift, int experts,
+                                         dev::Vec<T, dev::Lanes<T>::N> (&raw)[C]) {
+    constexpr int N = dev::Lanes<T>::N;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int at = ((c << shift) + lane) * N;
+        if (at + N <= experts) {
+            raw[c] = dev::load<T, N, false>(row + at);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                raw[c].v[i] = at + i < experts ? row[at + i] : (T)-__builtin_inff();
+        }
+    }
+}
+
+__device__ __forceinline__ float over_lanes_max(float v, int shift) {
+    for (int d = 1; d < 1 << shift; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+    return v;
+}
+__device__ __forceinline__ float over_lanes_sum(float v, int shift) {
+    for (int d = 1; d < 1 << shift; d <<= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+// p = softmax of a row.  A maximum that is no number leaves NaN in all of it.
+template <typename T, int C>
+__device__ __forceinline__ void softmax_row(const dev::Vec<T, dev::Lanes<T>::N> (&raw)[C], int shift,
+                                            float (&p)[C * dev::Lanes<T>::N]) {
+    constexpr int N = dev::Lanes<T>::N;
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const dev::Floats<N> x = dev::widen<T, N>(raw[c]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            p[c * N + i] = x[i];
+            top = fmaxf(top, x[i]);
+        }
+    }
+    top = over_lanes_max(top, shift);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C * N; ++i) {
+        p[i] = __builtin_amdgcn_exp2f((p[i] - top) * kLog2e);
+        sum += p[i];
+    }
+    sum = over_lanes_sum(sum, shift);
+    const float by = 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < C * N; ++i) p[i] *= by;
+}
+
+template <typename T, int C>
+__global__ void __launch_bounds__(kBalanceThreads)
+    bmmc_balance_rows_kernel(const BalanceArgs a, int shift) {
+    constexpr int N = dev::Lanes<T>::N;
+    extern __shared__ float part[];  // kBalanceWaves, num_experts; first the counts
+    int32_t *hits = reinterpret_cast<int32_t *>(part);
+    const int E = a.num_experts, tid = threadIdx.x;
+    const int64_t from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.tokens);
+    for (int e = tid; e <= E; e += blockDim.x) hits[e] = 0;
+    if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<uint32_t *>(a.hits + (int64_t)a.blocks * (E + 1)) = 0;
+    __syncthreads();
+    // a choice, and with a token's first the token
+    for (int64_t i = from * a.choices + tid; i < to * a.choices; i += blockDim.x) {
+        const int64_t t = quotient(a.by_choices, (uint32_t)i);
+        if (a.mask && !a.mask[t]) continue;
+        const int64_t e = a.is64 ? static_cast<const int64_t *>(a.experts)[i]
+                                 : (int64_t)static_cast<const int32_t *>(a.experts)[i];
+        if (e >= 0 && e < E) atomicAdd(&hits[e], 1);
+        if (i == t * a.choices) atomicAdd(&hits[E], 1);
+    }
+    __syncthreads();
+    int32_t *hist = a.hits + (int64_t)blockIdx.x * (E + 1);
+    for (int e = tid; e <= E; e += blockDim.x) hist[e] = hits[e];
+    __syncthreads();
+
+    const int lane = tid & 63, in_row = lane & ((1 << shift) - 1), wave = tid >> 6;
+    const int rows = 64 >> shift;
+    float sums[C * N] = {};
+    dev::Vec<T, N> next[C];
+    const int64_t step = (int64_t)rows * kBalanceWaves;
+    const T *logits = static_cast<const T *>(a.logits);
+    const auto counted = [&](int64_t t) { return t < to && (!a.mask || a.mask[t]); };
+    int64_t t = from + (int64_t)wave * rows + (lane >> shift);
+    bool on = counted(t);
+    if (on) load_row<T, C>(logits + t * a.stride, in_row, shift, E, next);
+    // every lane of a wave goes round as often as any: rows of a wave are in step
+    for (int64_t t0 = from + (int64_t)wave * rows; t0 < to; t0 += step, t += step) {
+        dev::Vec<T, N> raw[C];
+        const bool now = on;
+#pragma unroll
+        for (int c = 0; c < C; ++c) raw[c] = next[c];
+        on = counted(t + step);
+        if (on) load_row<T, C>(logits + (t + step) * a.stride, in_row, shift, E, next);
+        float p[C * N];
+        if (!now)
+#pragma unroll
+            for (int c = 0; c < C; ++c) raw[c] = dev::Vec<T, N>{};
+        softmax_row<T, C>(raw, shift, p);
+#pragma unroll
+        for (int i = 0; i < C * N; ++i) sums[i] += now ? p[i] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < C * N; ++i)
+        for (int d = 1 << shift; d < 64; d <<= 1) sums[i] += __shfl_xor(sums[i], d, 64);
+    if (lane < 1 << shift)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int e = ((c << shift) + lane) * N + i;
+                if (e < E) part[wave * E + e] = sums[c * N + i];
+            }
+    __syncthreads();
+    for (int e = tid; e < E; e += blockDim.x) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kBalanceWaves; ++w) s += part[w * E + e];
+        a.sums[(int64_t)blockIdx.x * E + e] = s;
+    }
+}
+
+// The workgroups' sums joined, kColumns experts a workgroup; the last one to end
+// sums the loss, in the experts' order.
+__global__ void __launch_bounds__(1024) bmmc_balance_join_kernel(const BalanceArgs a) {
+    __shared__ double sums[16][kColumns];
+    __shared__ int32_t hits[16][kColumns];
+    __shared__ int32_t tokens, last;
+    const int E = a.num_experts, col = threadIdx.x & 63, row = threadIdx.x >> 6;
+    const int e = blockIdx.x * kColumns + col;
+    if (threadIdx.x == 0) tokens = 0;
+    __syncthreads();
+    int32_t n = 0;
+    for (int b = threadIdx.x; b < a.blocks; b += blockDim.x) n += a.hits[(int64_t)b * (E + 1) + E];
+    if (n) atomicAdd(&tokens, n);
+    double s = 0.0;
+    int32_t h = 0;
+    if (e < E)
+        for (int b = row; b < a.blocks; b += 16) {
+            s += (double)a.sums[(int64_t)b * E + e];
+            h += a.hits[(int64_t)b * (E + 1) + e];
+        }
+    sums[row][col] = s;
+    hits[row][col] = h;
+    __syncthreads();
+    uint32_t *done = reinterpret_cast<uint32_t *>(a.hits + (int64_t)a.blocks * (E + 1));
+    float *losses = reinterpret_cast<float *>(done + 1);
+    if (row == 0) {
+        for (int r = 1; r < 16; ++r) {
+            s += sums[r][col];
+            h += hits[r][col];
+        }
+        double term = 0.0;
+        if (e < E) {
+            const double counted = (double)tokens;
+            const float slope =
+                tokens ? (float)((double)h * E / (counted * counted * a.choices)) : 0.0f;
+            a.counts[e] = h;
+            a.slopes[e] = slope;
+            term = (double)slope * s;
+        }
+#pragma unroll
+        for (int d = 32; d; d >>= 1) term += __shfl_xor(term, d, 64);
+        if (col == 0) {
+            __hip_atomic_store(&losses[blockIdx.x], (float)term, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+            last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                   gridDim.x - 1;
+            if (last) {
+                double all = 0.0;
+                for (uint32_t b = 0; b < gridDim.x; ++b)
+                    all += (double)__hip_atomic_load(&losses[b], __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT);
+                *a.loss = (float)all;
+            }
+        }
+    }
+}
+
+template <typename T, int C>
+__global__ void __launch_bounds__(256) bmmc_balance_backward_kernel(const BalanceArgs a, int shift,
+                                                                    int64_t block0) {
+    constexpr int N = dev::Lanes<T>::N;
+    const int lane = threadIdx.x & 63, in_row = lane & ((1 << shift) - 1), rows = 64 >> shift;
+    const int64_t first = ((block0 + blockIdx.x) * 4 + (threadIdx.x >> 6)) * a.chunk * rows;
+    const int E = a.num_experts;
+    float slope[C * N];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = ((c << shift) + in_row) * N + i;
+            slope[c * N + i] = e < E ? a.slopes[e] : 0.0f;
+        }
+    const float g = *a.grad;
+    const T *logits = static_cast<const T *>(a.logits);
+    dev::Vec<T, N> next[C];
+    const auto counted = [&](int64_t t) { return t < a.tokens && (!a.mask || a.mask[t]); };
+    int64_t t = first + (lane >> shift);
+    bool on = counted(t);
+    if (on) load_row<T, C>(logits + t * a.stride, in_row, shift, E, next);
+    for (int64_t k = 0; k < a.chunk && first + k * rows < a.tokens; ++k, t += rows) {
+        dev::Vec<T, N> raw[C];
+        const bool now = on;
+#pragma unroll
+        for (int c = 0; c < C; ++c) raw[c] = next[c];
+        on = k + 1 < a.chunk && counted(t + rows);
+        if (on) load_row<T, C>(logits + (t + rows) * a.stride, in_row, shift, E, next);
+        if (!now)
+#pragma unroll
+            for (int c = 0; c < C; ++c) raw[c] = dev::Vec<T, N>{};
+        float p[C * N];
+        softmax_row<T, C>(raw, shift, p);
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C * N; ++i) dot += slope[i] * p[i];
+        dot = over_lanes_sum(dot, shift);
+        if (t >= a.tokens) continue;
+        T *out = static_cast<T *>(a.grad_logits) + t * a.grad_stride;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = ((c << shift) + in_row) * N;
+            dev::Floats<N> y;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                y[i] = now ? g * (p[c * N + i] * (slope[c * N + i] - dot)) : 0.0f;
+            const dev::Vec<T, N> z = dev::narrow<T, N>(y);
+            if (at + N <= E) {
+                dev::store<T, N, false>(out + at, z);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (at + i < E) out[at + i] = z.v[i];
+            }
+        }
+    }
+}
+
+// Lanes and vectors a lane of a row.
+struct Cut {
+    int shift, vectors;
+};
+template <typename T> Cut cut_of(int experts) {
+    constexpr int N = dev::Lanes<T>::N;
+    const int all = (experts + N - 1) / N;
+    Cut c{0, 1};
+    while (c.shift < 6 && 1 << c.shift < all) ++c.shift;
+    while (c.vectors << c.shift < all) c.vectors *= 2;
+    return c;
+}
+
+template <typename T, int C> int forward(const BalanceArgs &x, int shift, hipStream_t s) {
+    BalanceArgs a = x;
+    a.chunk = (a.tokens + a.blocks - 1) / a.blocks;
+    const size_t lds = std::max((size_t)kBalanceWaves * a.num_experts, (size_t)a.num_experts + 1) * 4;
+    hipLaunchKernelGGL((bmmc_balance_rows_kernel<T, C>), dim3(a.blocks), dim3(kBalanceThreads), lds, s,
+                       a, shift);
+    hipLaunchKernelGGL(bmmc_balance_join_kernel, dim3((a.num_experts + kColumns - 1) / kColumns),
+                       dim3(1024), 0, s, a);
+    return hipGetLastError() == hipSuccess ? BMMC_OK : BMMC_ERR_HIP;
+}
+
+template <typename T, int C> int backward(const BalanceArgs &x, int shift, hipStream_t s) {
+    BalanceArgs a = x;
+    const int64_t each = 4 * (64 >> shift);  // rows of a workgroup at once
+    // up to four rounds of rows, where that leaves enough workgroups
+    const int64_t rounds = (a.tokens + each - 1) / each;
+    a.chunk = std::max<int64_t>(1, std::min<int64_t>(4, rounds / 2048));
+    return in_launches((rounds + a.chunk - 1) / a.chunk, 256, [&](uint32_t nb, int64_t b0) {
+        hipLaunchKernelGGL((bmmc_balance_backward_kernel<T, C>), dim3(nb), dim3(256), 0, s, a, shift, b0);
+    });
+}
+
+template <typename T, class F> int by_vectors(int experts, F call) {
+    const Cut c = cut_of<T>(experts);
+    switch (c.vectors) {
+    case 1: return call(std::integral_constant<int, 1>(), c.shift);
+    case 2: return call(std::integral_constant<int, 2>(), c.shift);
+    default: break;
+    }
+    // BMMC_MAX_EXPERTS in 32 bits are 8 vectors in each of 64 lanes, in 16 bits 4
+    if constexpr (sizeof(T) == 4)
+        if (c.vectors == 8) return call(std::integral_constant<int, 8>(), c.shift);
+    return call(std::integral_constant<int, 4>(), c.shift);
+}
+
+template <class F> int by_type(int type, F call) {
+    switch (type) {
+    case BMMC_F32: return call(float());
+    case BMMC_F16: return call(dev::f16_t());
+    default: return call(dev::bf16_t());
+    }
+}
+
+}  // namespace
+
+int launch_expert_balance(const BalanceArgs &a, hipStream_t s) {
+    return by_type(a.type, [&](auto type) {
+        typedef decltype(type) T;
+        return by_vectors<T>(a.num_experts, [&](auto c, int shift) {
+            return forward<T, decltype(c)::value>(a, shift, s);
+        });
+    });
+}
+
+int launch_expert_balance_backward(const BalanceArgs &a, hipStream_t s) {
+    return by_type(a.type, [&](auto type) {
+        typedef decltype(type) T;
+        return by_vectors<T>(a.num_experts, [&](auto c, int shift) {
+            return backward<T, decltype(c)::value>(a, shift, s);
+        });
+    });
+}
+
+}  // namespace bmmc

@@ -1,0 +1,391 @@
+// cache.hip -- a paged cache written in 8 bits with scales made on the way, and
+// rows of a cache read back (gfx950).
+//
+// A head of a token is a row with a scale of its own: its largest finite
+// magnitude / 448.  The largest is known only when all of the row has been
+// turned, so a row lies in one wave, 8 elements a lane, and never leaves its
+// registers: loaded, turned (a pair's other half comes from another lane), its
+// largest magnitude found by exchanges among the row's lanes, divided and stored.
+//
+// Bound by memory: each element is read once and written once, in 1 byte.
+// Turns are made once a token, in LDS, as for rotary positions.
+#include "../tokens/turns.h"
+#include "layer.h"
+
+namespace bmmc {
+
+namespace {
+
+constexpr int kPer = 8;  // elements of a row in a lane
+
+// Where a row's lanes are: `lanes` a row, a power of two, and 64 / lanes rows a wave.
+struct RowCut {
+    int32_t shift;  // log2 of lanes
+    __device__ int row() const { return (threadIdx.x & 63) >> shift; }
+    __device__ int at() const { return (threadIdx.x & ((1 << shift) - 1)) * kPer; }
+    __host__ __device__ int rows_a_wave() const { return 64 >> shift; }
+};
+
+RowCut row_cut(int dim) {
+    RowCut c{0};
+    while (kPer << c.shift < dim) ++c.shift;
+    return c;
+}
+
+template <typename T>
+__device__ __forceinline__ dev::Vec<T, kPer> load_part(const T *row, int at, int dim) {
+    if (at + kPer <= dim) return dev::load<T, kPer, false>(row + at);
+    dev::Vec<T, kPer> r;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) r.v[i] = at + i < dim ? row[at + i] : (T)0;
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_part(T *row, int at, int dim, const dev::Vec<T, kPer> &x) {
+    if (at + kPer <= dim) {
+        dev::store<T, kPer, false>(row + at, x);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (at + i < dim) row[at + i] = x.v[i];
+}
+
+// Tensors of a token's rows: q's heads, then k's, then v's.
+struct Rows {
+    const void *in;
+    int64_t token, head;
+};
+
+struct Scaled {
+    uint8_t *data;
+    float *scale;
+    int64_t page, place, head, scale_page, scale_place, scale_head;
+};
+
+Scaled scaled_of(const bmmc_scaled_cache &c) {
+    return Scaled{static_cast<uint8_t *>(c.data), c.scale,       c.page_stride, c.place_stride,
+                  c.head_stride,                  c.scale_page, c.scale_place, c.scale_head};
+}
+
+struct Quantize {
+    Rows q, k, v;
+    void *q_out;
+    int64_t q_out_token, q_out_head;
+    Scaled k_cache, v_cache;
+    PageTable where;
+    FastDiv by_tasks;
+    int64_t tokens;
+    RowCut cut;
+    int32_t q_heads, heads, k_dim, v_dim, tokens_a_block;
+    int32_t q_tasks, k_tasks;  // waves' tasks a token for q and for k
+};
+
+// Elements at .. at + 7 of a row of `dim`, turned.  The row's other lanes hold the
+// rest of it; where pairs are not whole vectors, a pair's other half is read
+// from the row.
+template <typename T, bool PAIRED>
+__device__ __forceinline__ void turn_part(const dev::Vec<T, kPer> &raw, const T *row, bool on, int at,
+                                          int pairs, const float2 *cs, float (&x)[kPer]) {
+    if constexpr (PAIRED) {
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) {
+            if (at + i >= 2 * pairs) continue;
+            const float2 u = cs[(at + i) / 2];
+            const float a = x[i], b = x[i + 1];
+            x[i] = a * u.x - b * u.y;
+            x[i + 1] = b * u.x + a * u.y;
+        }
+    } else {
+        float other[kPer];
+        if ((pairs & (kPer - 1)) == 0) {
+            const int lanes = pairs / kPer;
+            const int from = ((int)threadIdx.x & 63) + (at < pairs ? lanes : -lanes);
+            const float w[kPer] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+            // lanes past the pairs take what they get and do not use it
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) other[i] = __shfl(w[i], from & 63, 64);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int e = at + i;
+                other[i] = on && e < 2 * pairs ? (float)row[e < pairs ? e + pairs : e - pairs] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = at + i;
+            if (e >= 2 * pairs) continue;
+            const float2 u = cs[e < pairs ? e : e - pairs];
+            x[i] = x[i] * u.x + (e < pairs ? -other[i] : other[i]) * u.y;
+        }
+    }
+}
+
+template <typename T, bool PAIRED>
+__global__ void __launch_bounds__(kTurnThreads)
+    bmmc_cache_quantize_kernel(const Quantize a, const Turn r, int64_t block0) {
+    __shared__ float2 cs[kTurnPairs];
+    __shared__ PagePlace places[kTurnTokens];
+    const int64_t token0 = (block0 + blockIdx.x) * a.tokens_a_block;
+    const int tokens = (int)min((int64_t)a.tokens_a_block, a.tokens - token0);
+    const int per = (int)a.by_tasks.d, tasks = tokens * per, waves = blockDim.x >> 6;
+    const int first = (int)(blockIdx.y * waves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+    const int step = (int)gridDim.y * waves;
+    const int at = a.cut.at(), lane_row = a.cut.row(), rows = a.cut.rows_a_wave();
+
+    struct Row {
+        const T *in;
+        int t, kind, head;  // kind: 0 q, 1 k, 2 v
+        bool on;
+    };
+    const auto locate = [&](int task) {
+        const int t = (int)quotient(a.by_tasks, (uint32_t)task);
+        int number = task - t * per;
+        const int kind = number < a.q_tasks ? 0 : number < a.q_tasks + a.k_tasks ? 1 : 2;
+        number -= kind == 0 ? 0 : kind == 1 ? a.q_tasks : a.q_tasks + a.k_tasks;
+        const Rows &x = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+        const int head = number * rows + lane_row;
+        return Row{static_cast<const T *>(x.in) + (token0 + t) * x.token + head * x.head, t, kind,
+                   head, head < (kind == 0 ? a.q_heads : a.heads)};
+    };
+    dev::Vec<T, kPer> next{};
+    const auto fetch = [&](int task) {
+        const Row w = locate(task);
+        const int dim = w.kind == 2 ? a.v_dim : a.k_dim;
+        next = dev::Vec<T, kPer>{};
+        if (w.on && at < dim) next = load_part<T>(w.in, at, dim);
+    };
+    const int looker = (int)threadIdx.x - ((int)blockDim.x - 64);
+    if (looker >= 0 && looker < tokens) places[looker] = page_place(a.where, token0 + looker);
+    make_turns(r, token0, r.pairs ? tokens : 0, cs, [&] {
+        if (first < tasks) fetch(first);
+    });
+    __syncthreads();
+    for (int task = first; task < tasks; task += step) {
+        const Row w = locate(task);
+        const dev::Vec<T, kPer> raw = next;
+        if (task + step < tasks) fetch(task + step);
+        const int dim = w.kind == 2 ? a.v_dim : a.k_dim;
+        float x[kPer];
+        const dev::Floats<kPer> wide = dev::widen<T, kPer>(raw);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) x[i] = wide[i];
+        if (w.kind != 2 && r.pairs)
+            turn_part<T, PAIRED>(raw, w.in, w.on, at, r.pairs, cs + w.t * r.pairs, x);
+        if (w.kind == 0) {
+            if (!w.on || at >= dim) continue;
+            dev::Floats<kPer> y;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) y[i] = x[i];
+            store_part<T>(static_cast<T *>(a.q_out) + (token0 + w.t) * a.q_out_token +
+                              w.head * a.q_out_head,
+                          at, dim, dev::narrow<T, kPer>(y));
+            continue;
+        }
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const float m = fabsf(x[i]);
+            if (m < __builtin_inff()) most = fmaxf(most, m);  // neither infinities nor NaN
+        }
+        for (int d = 1; d < 1 << a.cut.shift; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
+        const float scale = most == 0.0f ? 1.0f : fmaxf(most / 448.0f, 0x1p-126f);
+        const PagePlace home = places[w.t];
+        if (home.page < 0 || !w.on || at >= dim) continue;
+        const Scaled &c = w.kind == 1 ? a.k_cache : a.v_cache;
+        uint8_t *out = c.data + home.page * c.page + home.place * c.place + w.head * c.head;
+        if (at == 0)
+            c.scale[home.page * c.scale_page + home.place * c.scale_place + w.head * c.scale_head] =
+                scale;
+        if (at + kPer <= dim) {
+            dev::Floats<kPer> y;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) y[i] = x[i];
+            store_e4m3<kPer>(out + at, y, scale);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (at + i < dim) store_e4m3<1>(out + at + i, dev::Floats<1>{x[i]}, scale);
+        }
+    }
+}
+
+template <typename T, bool PAIRED> int quantize(const QuantizeArgs &h, hipStream_t s) {
+    const Turn r = turn_of<1>(h.rotation);
+    Quantize a{};
+    a.q = Rows{h.q.in, h.q.in_token, h.q.in_head};
+    a.k = Rows{h.k.in, h.k.in_token, h.k.in_head};
+    a.v = Rows{h.v.in, h.v.in_token, h.v.in_head};
+    a.q_out = h.q.out;
+    a.q_out_token = h.q.out_token;
+    a.q_out_head = h.q.out_head;
+    a.k_cache = scaled_of(h.k_cache);
+    a.v_cache = scaled_of(h.v_cache);
+    a.where = h.where;
+    a.tokens = h.tokens;
+    a.cut = row_cut(std::max(h.k_dim, h.v_dim));
+    a.q_heads = (int32_t)h.q.heads;
+    a.heads = (int32_t)h.k.heads;
+    a.k_dim = h.k_dim;
+    a.v_dim = h.v_dim;
+    const int rows = a.cut.rows_a_wave();
+    a.q_tasks = (a.q_heads + rows - 1) / rows;
+    a.k_tasks = (a.heads + rows - 1) / rows;
+    const int64_t tasks = a.q_tasks + 2 * a.k_tasks;
+    a.by_tasks = fast_div((uint32_t)tasks);
+    const TurnCut cut = turn_cut(a.tokens, r.pairs, tasks);
+    a.tokens_a_block = cut.tokens_a_block;
+    return in_launches(cut.blocks, kTurnThreads, [&](uint32_t nb, int64_t b0) {
+        hipLaunchKernelGGL((bmmc_cache_quantize_kernel<T, PAIRED>), dim3(nb, cut.shares),
+                           dim3(64 * cut.waves), 0, s, a, r, b0);
+    });
+}
+
+template <typename T> int quantize_t(const QuantizeArgs &h, hipStream_t s) {
+    return h.rotation.interleaved ? quantize<T, true>(h, s) : quantize<T, false>(h, s);
+}
+
+// ---- rows read back ------------------------------------------------------------------
+
+constexpr int kReadTokens = 8;  // of a workgroup, where there are many
+constexpr int kReadAhead = 4;   // rows a lane has on their way
+
+struct Read {
+    void *k_out, *v_out;
+    int64_t k_token, k_head, v_token, v_head;
+    Scaled k_cache, v_cache;
+    PageTable where;
+    FastDiv by_rows;
+    int64_t tokens;
+    RowCut cut;
+    int32_t heads, k_dim, v_dim, tokens_a_block;
+};
+
+template <typename E> __device__ __forceinline__ dev::Floats<kPer> widened(const dev::Vec<E, kPer> &x) {
+    if constexpr (sizeof(E) == 1) {
+        uint32_t w[2];
+        __builtin_memcpy(w, &x.v, 8);
+        dev::Floats<kPer> y;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
+            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+            y[4 * i] = lo[0];
+            y[4 * i + 1] = lo[1];
+            y[4 * i + 2] = hi[0];
+            y[4 * i + 3] = hi[1];
+        }
+        return y;
+    } else {
+        return dev::widen<E, kPer>(x);
+    }
+}
+
+template <typename T, typename E>
+__global__ void __launch_bounds__(256) bmmc_cache_read_kernel(const Read a, int64_t block0) {
+    __shared__ PagePlace places[kReadTokens];
+    const int64_t token0 = (block0 + blockIdx.x) * a.tokens_a_block;
+    const int tokens = (int)min((int64_t)a.tokens_a_block, a.tokens - token0);
+    if ((int)threadIdx.x < tokens) places[threadIdx.x] = page_place(a.where, token0 + threadIdx.x);
+    __syncthreads();
+    const int at = a.cut.at(), each = a.cut.rows_a_wave() * 4;  // rows of a workgroup at once
+    const int mine = (int)(threadIdx.x >> 6) * a.cut.rows_a_wave() + a.cut.row();
+    const int rows = tokens * 2 * a.heads;
+    for (int base = (int)blockIdx.y * each * kReadAhead; base < rows;
+         base += (int)gridDim.y * each * kReadAhead) {
+        dev::Vec<E, kPer> x[kReadAhead];
+        float scale[kReadAhead];
+#pragma unroll
+        for (int j = 0; j < kReadAhead; ++j) {
+            const int row = base + j * each + mine;
+            x[j] = dev::Vec<E, kPer>{};
+            scale[j] = 1.0f;
+            if (row >= rows) continue;
+            const int t = (int)quotient(a.by_rows, (uint32_t)row);
+            int head = row - t * 2 * a.heads;
+            const bool key = head < a.heads;
+            head -= key ? 0 : a.heads;
+            const int dim = key ? a.k_dim : a.v_dim;
+            const PagePlace home = places[t];
+            if (home.page < 0 || at >= dim) continue;
+            const Scaled &c = key ? a.k_cache : a.v_cache;
+            x[j] = load_part<E>(reinterpret_cast<const E *>(c.data) + home.page * c.page +
+                                    home.place * c.place + head * c.head,
+                                at, dim);
+            if (sizeof(E) == 1)
+                scale[j] = c.scale[home.page * c.scale_page + home.place * c.scale_place +
+                                   head * c.scale_head];
+        }
+#pragma unroll
+        for (int j = 0; j < kReadAhead; ++j) {
+            const int row = base + j * each + mine;
+            if (row >= rows) continue;
+            const int t = (int)quotient(a.by_rows, (uint32_t)row);
+            int head = row - t * 2 * a.heads;
+            const bool key = head < a.heads;
+            head -= key ? 0 : a.heads;
+            const int dim = key ? a.k_dim : a.v_dim;
+            if (at >= dim) continue;
+            T *out = key ? static_cast<T *>(a.k_out) + (token0 + t) * a.k_token + head * a.k_head
+                         : static_cast<T *>(a.v_out) + (token0 + t) * a.v_token + head * a.v_head;
+            if constexpr (sizeof(E) == 1)
+                store_part<T>(out, at, dim, dev::narrow<T, kPer>(widened<E>(x[j]) * scale[j]));
+            else
+                store_part<T>(out, at, dim, x[j]);
+        }
+    }
+}
+
+template <typename T, typename E> int read(const ReadArgs &h, hipStream_t s) {
+    Read a{};
+    a.k_out = h.k.out;
+    a.v_out = h.v.out;
+    a.k_token = h.k.out_token;
+    a.k_head = h.k.out_head;
+    a.v_token = h.v.out_token;
+    a.v_head = h.v.out_head;
+    a.k_cache = scaled_of(h.k_cache);
+    a.v_cache = scaled_of(h.v_cache);
+    a.where = h.where;
+    a.tokens = h.tokens;
+    a.cut = row_cut(std::max(h.k_dim, h.v_dim));
+    a.heads = (int32_t)h.k.heads;
+    a.k_dim = h.k_dim;
+    a.v_dim = h.v_dim;
+    a.by_rows = fast_div((uint32_t)(2 * h.k.heads));
+    a.tokens_a_block = h.tokens >= 2048 * kReadTokens ? kReadTokens : 1;
+    const int64_t blocks = (a.tokens + a.tokens_a_block - 1) / a.tokens_a_block;
+    // a token's rows are shared by workgroups where there are few tokens
+    const int64_t passes = (a.tokens_a_block * 2 * h.k.heads - 1) /
+                               (a.cut.rows_a_wave() * 4 * kReadAhead) + 1;
+    const uint32_t shares = (uint32_t)std::max<int64_t>(1, std::min(passes, 2048 / blocks));
+    return in_launches(blocks, 256 * shares, [&](uint32_t nb, int64_t b0) {
+        hipLaunchKernelGGL((bmmc_cache_read_kernel<T, E>), dim3(nb, shares), dim3(256), 0, s, a, b0);
+    });
+}
+
+template <typename T> int read_t(const ReadArgs &h, hipStream_t s) {
+    return h.k_cache.type == BMMC_E4M3 ? read<T, uint8_t>(h, s) : read<T, T>(h, s);
+}
+
+}  // namespace
+
+int launch_cache_quantize(const QuantizeArgs &a, hipStream_t s) {
+    switch (a.type) {
+    case BMMC_F32: return quantize_t<float>(a, s);
+    case BMMC_F16: return quantize_t<dev::f16_t>(a, s);
+    default: return quantize_t<dev::bf16_t>(a, s);
+    }
+}
+
+int launch_cache_read(const ReadArgs &a, hipStream_t s) {
+    switch (a.type) {
+    case BMMC_F32: return read_t<float>(a, s);
+    case BMMC_F16: return read_t<dev::f16_t>(a, s);
+    default: return read_t<dev::bf16_t>(a, s);
+    }
+}
+
+}  // namespace bmmc
