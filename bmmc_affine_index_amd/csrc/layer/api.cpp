@@ -92,10 +92,10 @@ int check_attention_sizes(const bmmc_attention &a) {
 }
 
 int64_t workspace_floats(const bmmc_attention &a, const AttendPlan &p) {
-    return p.target ? p.parts * a.heads * p.rows * (int64_t)a.v_dim : 0;
+    return 2 * (int64_t)p.shares * a.heads * p.rows * a.v_dim;
 }
 int64_t workspace_states(const bmmc_attention &a, const AttendPlan &p) {
-    return p.target ? p.parts * a.heads * p.rows : 0;
+    return 2 * (int64_t)p.shares * a.heads * p.rows;
 }
 
 }  // namespace
@@ -149,13 +149,14 @@ int bmmc_cache_attention(const bmmc_attention *a, const bmmc_scaled_cache *k_cac
     x.by_page = fast_div((uint32_t)a->page_size);
     x.rows_scaled = by_place(*k_cache, a->pages, a->page_size) ||
                     by_place(*v_cache, a->pages, a->page_size);
-    x.reach = std::min(a->table_width * a->page_size, kMaxIndex);
+    // places and the tiles behind them stay in 32 bits
+    x.reach = std::min(a->table_width * a->page_size, kMaxIndex - 4096);
     x.a.window = std::min(a->window, kMaxIndex);
     x.partial = static_cast<float *>(workspace);
     x.state = reinterpret_cast<float2 *>(x.partial + workspace_floats(*a, x.plan));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    st = launch_attend_few(x, s);
-    return st == BMMC_OK && x.plan.target ? launch_attend_join(x, s) : st;
+    st = x.plan.rows > 16 ? launch_attend_many(x, s) : launch_attend_few(x, s);
+    return st == BMMC_OK && x.plan.shares ? launch_attend_join(x, s) : st;
 }
 
 int bmmc_cache_quantize(const bmmc_heads *q, const bmmc_heads *k, const bmmc_heads *v,

@@ -14,6 +14,15 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
+// What all lanes of a wave know to be the same, in scalar registers.
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ int64_t uniform(int64_t v) { return (int64_t)uniform((uint64_t)v); }
+
 // ---- sequences, tiles and parts ------------------------------------------------
 
 // A sequence's new tokens: rows first .. first + count - 1 of q, the last at
@@ -54,9 +63,10 @@ __device__ __forceinline__ Range range_of(const AttendArgs &x, const Sequence &q
     return r;
 }
 
+// Units of a sequence's tiles, each taken for as long as its last.
 __device__ __forceinline__ int32_t units_of(const AttendArgs &x, const Sequence &q) {
     const Range r = range_of(x, q, q.length - q.count, q.length - 1);
-    return ceil_div(r.to - r.from, x.plan.unit);
+    return max(ceil_div(r.to - r.from, x.plan.unit), 1);
 }
 
 __device__ __forceinline__ int64_t wave_sum64(int64_t v) {
@@ -65,97 +75,114 @@ __device__ __forceinline__ int64_t wave_sum64(int64_t v) {
     return v;
 }
 
-// A workgroup's piece of work; found is false behind the last.
-struct Piece {
+// Units of all tiles, by every wave for itself.
+__device__ __forceinline__ int64_t all_units(const AttendArgs &x) {
+    int64_t all = 0;
+    for (int32_t s = threadIdx.x & 63; s < (int32_t)x.a.batch; s += 64) {
+        const Sequence q = sequence_at(x, s);
+        all += (int64_t)tiles_of(x, q) * units_of(x, q);
+    }
+    return uniform(wave_sum64(all));
+}
+
+// Units [first(w), first(w + 1)) are share w's.
+__device__ __forceinline__ int64_t first_of(const AttendArgs &x, int64_t all, int64_t w) {
+    return all * w / x.plan.shares;
+}
+__device__ __forceinline__ int32_t share_of(const AttendArgs &x, int64_t all, int64_t unit) {
+    return (int32_t)(((unit + 1) * x.plan.shares - 1) / all);
+}
+
+// A tile of a sequence, and its first unit among all.
+struct Tile {
     bool found;
-    int32_t seq, tile, part, parts;
-    int64_t number;  // of the tile's first part among all parts
+    int32_t seq, tile, units;
+    int64_t first;
     Sequence q;
 };
 
-// Piece `want` of all parts or, BY_TILE, the want'th tile.  Every wave looks for
-// itself, 64 sequences at a time: a prefix sum over the lanes tells which
-// sequence holds it.
-template <bool BY_TILE> __device__ __forceinline__ Piece find_piece(const AttendArgs &x, int64_t want) {
+// The tile that holds unit `want` of all or, BY_TILE, the want'th.  Every wave
+// looks for itself, 64 sequences at a time: a prefix sum over the lanes tells
+// which sequence holds it.
+template <bool BY_TILE> __device__ __forceinline__ Tile find_tile(const AttendArgs &x, int64_t want) {
     const int lane = threadIdx.x & 63;
     const int32_t batch = (int32_t)x.a.batch;
-    int32_t each = 0;  // units of a part
-    if (x.plan.target) {
-        int64_t all = 0;
-        for (int32_t s = lane; s < batch; s += 64) {
-            const Sequence q = sequence_at(x, s);
-            all += (int64_t)tiles_of(x, q) * units_of(x, q);
-        }
-        all = wave_sum64(all);
-        const int64_t fair = (all + x.plan.target - 1) / x.plan.target;
-        each = (int32_t)min(max(fair, (int64_t)x.plan.least), (int64_t)1 << 30);
-    }
-    Piece p{};
-    int64_t before = 0, parts_before = 0;
+    Tile t{};
+    int64_t before = 0, units_before = 0;
     for (int32_t s0 = 0; s0 < batch; s0 += 64) {
         Sequence q{};
-        int32_t tiles = 0, parts = 1;
+        int32_t tiles = 0, units = 1;
         if (s0 + lane < batch) {
             q = sequence_at(x, s0 + lane);
             tiles = tiles_of(x, q);
-            if (each) parts = max(ceil_div(units_of(x, q), each), 1);
+            units = units_of(x, q);
         }
-        const int64_t mine = BY_TILE ? tiles : (int64_t)tiles * parts;
-        int64_t upto = mine, parts_upto = (int64_t)tiles * parts;
+        const int64_t work = (int64_t)tiles * units, mine = BY_TILE ? tiles : work;
+        int64_t upto = mine, units_upto = work;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int64_t o = __shfl_up(upto, d, 64);
             if (lane >= d) upto += o;
             if (BY_TILE) {
-                const int64_t po = __shfl_up(parts_upto, d, 64);
-                if (lane >= d) parts_upto += po;
+                const int64_t uo = __shfl_up(units_upto, d, 64);
+                if (lane >= d) units_upto += uo;
             }
         }
         const int64_t from = before + upto - mine;
         const uint64_t here = __ballot(want >= from && want < from + mine);
         if (here) {
             const int l = __ffsll((unsigned long long)here) - 1;
-            const int64_t in = want - __shfl(from, l, 64);
-            p.found = true;
-            p.seq = s0 + l;
-            p.parts = __builtin_amdgcn_readlane(parts, l);
-            p.q.first = __builtin_amdgcn_readlane(q.first, l);
-            p.q.count = __builtin_amdgcn_readlane(q.count, l);
-            p.q.length = __builtin_amdgcn_readlane(q.length, l);
-            p.q.end = __builtin_amdgcn_readlane(q.end, l);
-            if (BY_TILE) {
-                p.tile = __builtin_amdgcn_readfirstlane((int32_t)in);
-                p.number = parts_before + __shfl(parts_upto - (int64_t)tiles * parts, l, 64) +
-                           (int64_t)p.tile * p.parts;
-            } else {
-                p.tile = __builtin_amdgcn_readfirstlane((int32_t)in / p.parts);
-                p.part = __builtin_amdgcn_readfirstlane((int32_t)in - p.tile * p.parts);
-                p.number = want - p.part;
-            }
-            return p;
+            const int64_t in = want - uniform(__shfl(from, l, 64));
+            const int64_t start = BY_TILE ? units_before + __shfl(units_upto - work, l, 64)
+                                          : __shfl(from, l, 64);
+            t.found = true;
+            t.seq = s0 + l;
+            t.units = __builtin_amdgcn_readlane(units, l);
+            t.q.first = __builtin_amdgcn_readlane(q.first, l);
+            t.q.count = __builtin_amdgcn_readlane(q.count, l);
+            t.q.length = __builtin_amdgcn_readlane(q.length, l);
+            t.q.end = __builtin_amdgcn_readlane(q.end, l);
+            t.tile = __builtin_amdgcn_readfirstlane((int32_t)(BY_TILE ? in : in / t.units));
+            t.first = uniform(start) + (int64_t)t.tile * t.units;
+            return t;
         }
-        before += __shfl(upto, 63, 64);
-        parts_before += __shfl(parts_upto, 63, 64);
+        before += uniform(__shfl(upto, 63, 64));
+        units_before += uniform(__shfl(units_upto, 63, 64));
     }
-    return p;
+    return t;
 }
 
-// The tokens of a tile and the places of its part that are looked at.
+// The tile after t; not found behind the last.
+__device__ __forceinline__ void next_tile(const AttendArgs &x, Tile &t) {
+    t.first += t.units;
+    if (++t.tile < tiles_of(x, t.q)) return;
+    t.tile = 0;
+    for (++t.seq; t.seq < (int32_t)x.a.batch; ++t.seq) {
+        const Sequence q = sequence_at(x, t.seq);
+        t.q = Sequence{uniform(q.first), uniform(q.count), uniform(q.length), uniform(q.end)};
+        if (t.q.count) {
+            t.units = units_of(x, t.q);
+            return;
+        }
+    }
+    t.found = false;
+}
+
+// The tokens of a tile, and the places that units [from, to) of it look at.
 struct Span {
     int32_t first, last;  // places of the first and the last token
     int32_t from, to;
 };
-__device__ __forceinline__ Span span_of(const AttendArgs &x, const Piece &p) {
-    const int64_t row0 = (int64_t)p.tile * x.plan.rows;
-    const int64_t row1 = min(row0 + x.plan.rows, (int64_t)p.q.count * x.group) - 1;
-    const int32_t base = p.q.length - p.q.count;
+__device__ __forceinline__ Span span_of(const AttendArgs &x, const Tile &t, int32_t from, int32_t to) {
+    const int64_t row0 = (int64_t)t.tile * x.plan.rows;
+    const int64_t row1 = min(row0 + x.plan.rows, (int64_t)t.q.count * x.group) - 1;
+    const int32_t base = t.q.length - t.q.count;
     Span s;
-    s.first = base + (int32_t)(row0 / x.group);
-    s.last = base + (int32_t)(row1 / x.group);
-    const Range r = range_of(x, p.q, s.first, s.last);
-    const int64_t step = (int64_t)ceil_div(ceil_div(r.to - r.from, x.plan.unit), p.parts) * x.plan.unit;
-    s.from = (int32_t)min(r.from + p.part * step, (int64_t)r.to);
-    s.to = (int32_t)min(s.from + step, (int64_t)r.to);
+    s.first = base + (int32_t)quotient(x.by_group, (uint32_t)row0);
+    s.last = base + (int32_t)quotient(x.by_group, (uint32_t)row1);
+    const Range r = range_of(x, t.q, s.first, s.last);
+    s.from = (int32_t)min(r.from + (int64_t)from * x.plan.unit, (int64_t)r.to);
+    s.to = (int32_t)min(r.from + (int64_t)to * x.plan.unit, (int64_t)r.to);
     return s;
 }
 
@@ -179,13 +206,12 @@ __device__ __forceinline__ void clear_rest(const AttendArgs &x, int64_t block, i
 // ---- elements --------------------------------------------------------------------
 
 // What stands for a row that is not there: zeros, as long as the longest head.
-__device__ const uint32_t kZeros[BMMC_MAX_HEAD_DIM] = {};
+__device__ const uint32_t __attribute__((aligned(16))) kZeros[BMMC_MAX_HEAD_DIM] = {};
 
-// N elements of a row from element `at` on as they are in memory.  Rows have N
+// N elements of a row from element `at` on, zeros past its end.  Rows have N
 // elements at least; the last vector of a row that is no whole number of them
-// ends with the row, and a vector past it is that one again: `settle` puts both
-// right when the elements are used, and not before, when they are still on
-// their way.
+// ends with the row, and `settle` shifts it into its place when the elements are
+// used, and not before, when they are still on their way.
 template <typename E, int N> struct Raw {
     static constexpr int kBytes = N * (int)sizeof(E);
     static constexpr int kWords = kBytes / 4;
@@ -195,8 +221,19 @@ template <typename E, int N>
 __device__ __forceinline__ Raw<E, N> fetch(const uint8_t *row, int at, int dim) {
     typedef typename Vec<uint8_t, Raw<E, N>::kBytes>::raw bytes_t;
     typedef bytes_t packed_t __attribute__((aligned(sizeof(E))));
-    const bytes_t v =
-        *reinterpret_cast<const packed_t *>(row + min(at, dim - N) * (int)sizeof(E));
+    const uint8_t *from = row + min(at, dim - N) * (int)sizeof(E);
+    if (at >= dim) from = reinterpret_cast<const uint8_t *>(kZeros);
+    const bytes_t v = *reinterpret_cast<const packed_t *>(from);
+    Raw<E, N> r;
+    __builtin_memcpy(r.w, &v, sizeof(r.w));
+    return r;
+}
+// The same of a row that reaches past the vector.
+template <typename E, int N>
+__device__ __forceinline__ Raw<E, N> fetch_whole(const uint8_t *row, int at) {
+    typedef typename Vec<uint8_t, Raw<E, N>::kBytes>::raw bytes_t;
+    typedef bytes_t packed_t __attribute__((aligned(sizeof(E))));
+    const bytes_t v = *reinterpret_cast<const packed_t *>(row + at * (int)sizeof(E));
     Raw<E, N> r;
     __builtin_memcpy(r.w, &v, sizeof(r.w));
     return r;
@@ -204,12 +241,7 @@ __device__ __forceinline__ Raw<E, N> fetch(const uint8_t *row, int at, int dim) 
 template <typename E, int N>
 __device__ __forceinline__ void settle(Raw<E, N> &r, int at, int dim) {
     constexpr int W = Raw<E, N>::kWords;
-    if (at + N <= dim) return;
-    if (at >= dim) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) r.w[i] = 0;
-        return;
-    }
+    if (at + N <= dim || at >= dim) return;
     const int bits = (N - (dim & (N - 1))) * 8 * (int)sizeof(E);  // the same in all lanes
     if constexpr (W == 4)
         if (bits & 64) {
@@ -225,6 +257,17 @@ __device__ __forceinline__ void settle(Raw<E, N> &r, int at, int dim) {
 #pragma unroll
     for (int i = 0; i < W; ++i)
         r.w[i] = __builtin_amdgcn_alignbit(i + 1 < W ? r.w[i + 1] : 0u, r.w[i], bits & 31);
+}
+
+// A number that the compiler does not know to be the same each time: what hangs
+// on it is made where it is used, and not kept in registers from tile to tile.
+__device__ __forceinline__ int kept(int v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+__device__ __forceinline__ int kept_lane(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 // The inputs' type: vectors of 8 for the products of 16-bit types, of 4 in 32 bits.
@@ -277,6 +320,22 @@ __device__ __forceinline__ typename Product<T>::vec product_vec(const Raw<E, Pro
     typename Product<T>::vec v;
     __builtin_memcpy(&v, w, sizeof(v));
     return v;
+}
+
+// Bit i: whether the token at place p sees place t + i, by p - t.
+__device__ __forceinline__ uint64_t seen_of(int32_t ahead, int64_t window) {
+    uint64_t see = ahead < 0 ? 0 : ahead >= 63 ? ~uint64_t(0) : (uint64_t(2) << ahead) - 1;
+    const int64_t from = (int64_t)ahead - window + 1;
+    if (window && from > 0) see = from > 63 ? 0 : see & ~((uint64_t(1) << from) - 1);
+    return see;
+}
+
+// One element of a row.
+template <typename T, typename E> __device__ __forceinline__ float element_of(const E *p) {
+    if constexpr (sizeof(E) == 1)
+        return __builtin_amdgcn_cvt_f32_fp8((int)*p, 0);
+    else
+        return (float)*p;
 }
 
 // c += a b of 16 x 16: lane l holds row (a) or column (b) l % 16 and 8 (32 bits:

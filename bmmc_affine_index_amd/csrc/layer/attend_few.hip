@@ -41,20 +41,6 @@ template <typename E> __device__ __forceinline__ bool has_nonfinite(uint32_t w) 
     }
 }
 
-// A number that the compiler does not know to be the same each time: what hangs
-// on it is made where it is used, and not kept in registers from tile to tile.
-__device__ __forceinline__ int kept(int v) {
-    asm volatile("" : "+s"(v));
-    return v;
-}
-
-template <typename T, typename E> __device__ __forceinline__ float element_of(const E *p) {
-    if constexpr (sizeof(E) == 1)
-        return __builtin_amdgcn_cvt_f32_fp8((int)*p, 0);
-    else
-        return (float)*p;
-}
-
 // DP: the heads' elements, padded; KB: blocks of 16 keys a wave's tile.  AHEAD: a
 // tile's keys are fetched while the one before is worked on, and its values
 // while its keys are; longer heads leave no registers for that.
@@ -100,349 +86,381 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int64_t block = block0 + blockIdx.x, heads = x.a.heads;
-    if (block >= x.plan.parts * heads) {
-        clear_rest<T>(x, block - x.plan.parts * heads, kClearBlocks);
+    const int64_t blocks = (x.plan.shares ? x.plan.shares : x.plan.tiles) * heads;
+    if (block >= blocks) {
+        clear_rest<T>(x, block - blocks, kClearBlocks);
         return;
     }
     const int64_t number = block / heads;
     const int head = (int)(block - number * heads);
-    const Piece piece = find_piece<false>(x, number);
-    if (!piece.found) return;
-    const Span span = span_of(x, piece);
-    const int32_t *table = x.a.table + (int64_t)piece.seq * x.a.table_stride;
+    Tile tile;
+    int64_t unit, stop;  // of all: this workgroup's
+    if (x.plan.shares) {
+        const int64_t all = all_units(x);
+        unit = first_of(x, all, number);
+        stop = first_of(x, all, number + 1);
+        if (unit >= stop) return;
+        tile = find_tile<false>(x, unit);
+    } else {
+        tile = find_tile<true>(x, number);
+        unit = tile.first;
+        stop = tile.first + tile.units;
+    }
     typename F::PerWave &mine = main_lds.wave[wave];
 
-    // this lane's row
-    const int64_t row = (int64_t)piece.tile * 16 + n;
-    const bool on = row < (int64_t)piece.q.count * x.group;
-    const int32_t token = (int32_t)quotient(x.by_group, (uint32_t)row);
-    const int32_t place = piece.q.length - piece.q.count + token;
-    vec_t q[F::kQueriesInLds ? 1 : NK];
-    {
-        const int64_t h = (int64_t)head * x.group + (row - (int64_t)token * x.group);
-        const uint8_t *in = reinterpret_cast<const uint8_t *>(kZeros);
-        if (on)
-            in = reinterpret_cast<const uint8_t *>(
-                static_cast<const T *>(x.a.q) +
-                (piece.q.first + (int64_t)token) * x.a.q_token + h * x.a.q_head);
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            if (F::kQueriesInLds && (k & (kFewWaves - 1)) != wave) continue;
-            Raw<T, CE> r = fetch<T, CE>(in, (k * 4 + g) * CE, x.a.k_dim);
-            settle(r, (k * 4 + g) * CE, x.a.k_dim);
-            if constexpr (F::kQueriesInLds)
-                *reinterpret_cast<u4 *>(&main_lds.q[(k * 64 + lane) * 4]) =
-                    u4{r.w[0], r.w[1], r.w[2], r.w[3]};
-            else
-                q[k] = product_vec<T>(r);
-        }
-        if constexpr (F::kQueriesInLds) __syncthreads();
-    }
+    while (tile.found && unit < stop) {
+        const int32_t unit0 = (int32_t)(unit - tile.first);
+        const int32_t unit1 = (int32_t)min(stop - tile.first, (int64_t)tile.units);
+        const Span span = span_of(x, tile, unit0, unit1);
+        const int32_t *table = x.a.table + (int64_t)tile.seq * x.a.table_stride;
 
-    // lanes 0 to 31 look after the keys, 32 to 63 after the values of a tile
-    const int kl = lane & 31, half = lane >> 5;
-    const uint8_t *base = static_cast<const uint8_t *>(half ? x.v.data : x.k.data);
-    const int64_t by_page = half ? x.v.page_stride : x.k.page_stride;
-    const int64_t by_place = half ? x.v.place_stride : x.k.place_stride;
-    const int64_t by_head = (half ? x.v.head_stride : x.k.head_stride) * head;
-    const bool scaled = kNarrow && x.rows_scaled;
-    const auto look = [&](int32_t t) {
-        return kl < KT ? page_of(x, table, t + kl, span.to) : -1;
-    };
-    float scale_next = 0.0f;
-    const auto put = [&](int32_t page, int32_t t, int which) {
-        const int32_t in = t + kl - (int32_t)quotient(x.by_page, (uint32_t)(t + kl)) * (int32_t)x.by_page.d;
-        if (kl < KT)
-            mine.at[which][half][kl] =
-                page < 0 ? reinterpret_cast<const uint8_t *>(kZeros)
-                         : base + (page * by_page + in * by_place + by_head) * (int64_t)sizeof(E);
-        if (scaled) {
-            const bmmc_scaled_cache &c = half ? x.v : x.k;
-            scale_next = page < 0 ? 0.0f
-                                  : c.scale[page * c.scale_page + in * c.scale_place + head * c.scale_head];
+        // this lane's row
+        const int64_t row = (int64_t)tile.tile * 16 + n;
+        const bool on = row < (int64_t)tile.q.count * x.group;
+        const int32_t token = (int32_t)quotient(x.by_group, (uint32_t)row);
+        const int32_t place = tile.q.length - tile.q.count + token;
+        vec_t q[F::kQueriesInLds ? 1 : NK];
+        {
+            const int64_t h = (int64_t)head * x.group + (row - (int64_t)token * x.group);
+            const uint8_t *in = reinterpret_cast<const uint8_t *>(kZeros);
+            if (on)
+                in = reinterpret_cast<const uint8_t *>(
+                    static_cast<const T *>(x.a.q) +
+                    (tile.q.first + (int64_t)token) * x.a.q_token + h * x.a.q_head);
+            const int dim = kept(x.a.k_dim);
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+                if (F::kQueriesInLds && (k & (kFewWaves - 1)) != wave) continue;
+                Raw<T, CE> r = fetch<T, CE>(in, (k * 4 + g) * CE, dim);
+                if (dim & (CE - 1)) settle(r, (k * 4 + g) * CE, dim);
+                if constexpr (F::kQueriesInLds)
+                    *reinterpret_cast<u4 *>(&main_lds.q[(k * 64 + lane) * 4]) =
+                        u4{r.w[0], r.w[1], r.w[2], r.w[3]};
+                else
+                    q[k] = product_vec<T>(r);
+            }
+            if constexpr (F::kQueriesInLds) __syncthreads();
         }
-        wave_fence();
-    };
-    Raw<E, CE> kr[AHEAD ? KB : 1][KG];
-    Raw<E, VE> vr[VK][AHEAD ? VG : 1];
-    const auto load_keys = [&](int which, int b, int k0) {
-        const uint8_t *in = mine.at[which][0][b * 16 + n];
-#pragma unroll
-        for (int k = 0; k < KG; ++k)
-            kr[AHEAD ? b : 0][k] = fetch<E, CE>(in, ((k0 + k) * 4 + g) * CE, x.a.k_dim);
-    };
-    const auto load_values = [&](int which, int v) {
-#pragma unroll
-        for (int j = 0; j < VK; ++j)
-            vr[j][AHEAD ? v : 0] = fetch<E, VE>(mine.at[which][1][(j >> 2) * 16 + g * 4 + (j & 3)],
-                                                (v * 16 + n) * VE, x.a.v_dim);
-    };
-    const auto load_all_keys = [&](int which) {
-#pragma unroll
-        for (int b = 0; b < KB; ++b) load_keys(which, b, 0);
-    };
-    const auto load_all_values = [&](int which) {
-#pragma unroll
-        for (int v = 0; v < VG; ++v) load_values(which, v);
-    };
 
-    float c = x.a.scale * 1.4426950408889634f, by_value = 1.0f;
-    if (kNarrow && !scaled) {
-        c *= x.k.scale[head * x.k.scale_head];
-        by_value = x.v.scale[head * x.v.scale_head];
-    }
-    f4 o[VG][VE];
+        // lanes 0 to 31 look after the keys, 32 to 63 after the values of a tile
+        const int kl = lane & 31, half = lane >> 5;
+        const uint8_t *base = static_cast<const uint8_t *>(half ? x.v.data : x.k.data);
+        const int64_t by_page = half ? x.v.page_stride : x.k.page_stride;
+        const int64_t by_place = half ? x.v.place_stride : x.k.place_stride;
+        const int64_t by_head = (half ? x.v.head_stride : x.k.head_stride) * head;
+        const bool scaled = kNarrow && x.rows_scaled;
+        const auto look = [&](int32_t t) {
+            return kl < KT ? page_of(x, table, t + kl, span.to) : -1;
+        };
+        float scale_next = 0.0f;
+        const auto put = [&](int32_t page, int32_t t, int which) {
+            const int32_t in = t + kl - (int32_t)quotient(x.by_page, (uint32_t)(t + kl)) * (int32_t)x.by_page.d;
+            if (kl < KT)
+                mine.at[which][half][kl] =
+                    page < 0 ? reinterpret_cast<const uint8_t *>(kZeros)
+                             : base + (page * by_page + in * by_place + by_head) * (int64_t)sizeof(E);
+            if (scaled) {
+                const bmmc_scaled_cache &c = half ? x.v : x.k;
+                scale_next = page < 0 ? 0.0f
+                                      : c.scale[page * c.scale_page + in * c.scale_place + head * c.scale_head];
+            }
+            wave_fence();
+        };
+        Raw<E, CE> kr[AHEAD ? KB : 1][KG];
+        Raw<E, VE> vr[VK][AHEAD ? VG : 1];
+        const auto load_keys = [&](int which, int b, int k0) {
+            const uint8_t *in = mine.at[which][0][b * 16 + n];
+            if (x.a.k_dim == DP) {
 #pragma unroll
-    for (int v = 0; v < VG; ++v)
+                for (int k = 0; k < KG; ++k)
+                    kr[AHEAD ? b : 0][k] = fetch_whole<E, CE>(in, ((k0 + k) * 4 + g) * CE);
+                return;
+            }
+            const int dim = kept(x.a.k_dim);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) o[v][e] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = kNothing, l = 0.0f;
+            for (int k = 0; k < KG; ++k)
+                kr[AHEAD ? b : 0][k] = fetch<E, CE>(in, ((k0 + k) * 4 + g) * CE, dim);
+        };
+        const auto load_values = [&](int which, int v) {
+            const int dim = kept(x.a.v_dim);
+#pragma unroll
+            for (int j = 0; j < VK; ++j) {
+                const uint8_t *in = mine.at[which][1][(j >> 2) * 16 + g * 4 + (j & 3)];
+                vr[j][AHEAD ? v : 0] = fetch<E, VE>(in, (v * 16 + n) * VE, dim);
+            }
+        };
+        const auto load_all_keys = [&](int which) {
+#pragma unroll
+            for (int b = 0; b < KB; ++b) load_keys(which, b, 0);
+        };
+        const auto load_all_values = [&](int which) {
+#pragma unroll
+            for (int v = 0; v < VG; ++v) load_values(which, v);
+        };
 
-    const int32_t step = kFewWaves * KT;
-    int32_t t = span.from + wave * KT;
-    int which = 0;
-    int32_t page = -1, page_next = -1;
-    if (t < span.to) {
-        page = look(t);
-        put(page, t, 0);
-        if (AHEAD) {
-            load_all_keys(0);
-            load_all_values(0);
+        float c = x.a.scale * 1.4426950408889634f, by_value = 1.0f;
+        if (kNarrow && !scaled) {
+            c *= x.k.scale[head * x.k.scale_head];
+            by_value = x.v.scale[head * x.v.scale_head];
         }
-        if (t + step < span.to) page_next = look(t + step);
-    }
-    for (; t < span.to; t += step) {
-        const uint32_t seen = (uint32_t)__ballot(page >= 0);  // the keys' lanes
-        f4 s[KB];
+        f4 o[VG][VE];
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-            s[b] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int v = 0; v < VG; ++v)
 #pragma unroll
-            for (int k0 = 0; k0 < NK; k0 += KG) {
-                if (!AHEAD) {
-                    __builtin_amdgcn_sched_barrier(0);  // no more than this in registers
-                    load_keys(which, b, k0);
-                }
-                Raw<E, CE> *const at = kr[AHEAD ? b : 0];
-                if (x.a.k_dim != DP) {
-                    const int dim = kept(x.a.k_dim);
+            for (int e = 0; e < VE; ++e) o[v][e] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        float m = kNothing, l = 0.0f;
+
+        const int32_t step = kFewWaves * KT;
+        int32_t t = span.from + wave * KT;
+        int which = 0;
+        int32_t page = -1, page_next = -1;
+        if (t < span.to) {
+            page = look(t);
+            put(page, t, 0);
+            if (AHEAD) {
+                load_all_keys(0);
+                load_all_values(0);
+            }
+            if (t + step < span.to) page_next = look(t + step);
+        }
+        for (; t < span.to; t += step) {
+            const uint32_t seen = (uint32_t)__ballot(page >= 0);  // the keys' lanes
+            f4 s[KB];
 #pragma unroll
-                    for (int k = 0; k < KG; ++k) settle(at[k], ((k0 + k) * 4 + g) * CE, dim);
-                }
+            for (int b = 0; b < KB; ++b) {
+                s[b] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < KG; ++k) {
-                    vec_t qk;
-                    if constexpr (F::kQueriesInLds) {
-                        const u4 w =
-                            *reinterpret_cast<const u4 *>(&main_lds.q[((k0 + k) * 64 + lane) * 4]);
-                        __builtin_memcpy(&qk, &w, 16);
-                    } else {
-                        qk = q[k];
+                for (int k0 = 0; k0 < NK; k0 += KG) {
+                    if (!AHEAD) {
+                        __builtin_amdgcn_sched_barrier(0);  // no more than this in registers
+                        load_keys(which, b, k0);
                     }
-                    s[b] = mfma16(product_vec<T>(at[k]), qk, s[b]);
-                }
-            }
-            wait_for(s[b]);
-        }
-        if (scaled) {
-            if (kl < KT) mine.scale[half][kl] = scale_next;
-            wave_fence();
-        }
-        const bool more = t + step < span.to;
-        if (more) {
-            page = page_next;
-            put(page, t + step, which ^ 1);
-            if (AHEAD) load_all_keys(which ^ 1);
-            if (t + 2 * step < span.to) page_next = look(t + 2 * step);
-        }
+                    Raw<E, CE> *const at = kr[AHEAD ? b : 0];
+                    if (x.a.k_dim & (CE - 1)) {
+                        const int dim = kept(x.a.k_dim);
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-            f4 by{c, c, c, c};
-            if (scaled) by *= *reinterpret_cast<const f4 *>(&mine.scale[0][b * 16 + g * 4]);
-            s[b] *= by;
-        }
-        // the tile has keys that are not there, or that some rows do not see
-        const bool parted = t + KT - 1 > span.first ||
-                            (x.a.window && t <= span.last - x.a.window);
-        if (parted || ~seen << (32 - KT)) {
+                        for (int k = 0; k < KG; ++k) settle(at[k], ((k0 + k) * 4 + g) * CE, dim);
+                    }
+#pragma unroll
+                    for (int k = 0; k < KG; ++k) {
+                        vec_t qk;
+                        if constexpr (F::kQueriesInLds) {
+                            const u4 w =
+                                *reinterpret_cast<const u4 *>(&main_lds.q[((k0 + k) * 64 + lane) * 4]);
+                            __builtin_memcpy(&qk, &w, 16);
+                        } else {
+                            qk = q[k];
+                        }
+                        s[b] = mfma16(product_vec<T>(at[k]), qk, s[b]);
+                    }
+                }
+                wait_for(s[b]);
+            }
+            if (scaled) {
+                if (kl < KT) mine.scale[half][kl] = scale_next;
+                wave_fence();
+            }
+            const bool more = t + step < span.to;
+            if (more) {
+                page = page_next;
+                put(page, t + step, which ^ 1);
+                if (AHEAD) load_all_keys(which ^ 1);
+                if (t + 2 * step < span.to) page_next = look(t + 2 * step);
+            }
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                f4 by{c, c, c, c};
+                if (scaled) by *= *reinterpret_cast<const f4 *>(&mine.scale[0][b * 16 + g * 4]);
+                s[b] *= by;
+            }
+            // the tile has keys that are not there, or that some rows do not see
+            const bool parted = t + KT - 1 > span.first ||
+                                (x.a.window && t <= span.last - x.a.window);
+            if (parted || ~seen << (32 - KT)) {
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = b * 16 + g * 4 + i;
+                        const bool see = (seen >> key & 1u) && t + key <= place &&
+                                         (!x.a.window || t + key > place - x.a.window);
+                        if (!see) s[b][i] = kNothing;
+                    }
+            }
+            float top = kNothing;
 #pragma unroll
             for (int b = 0; b < KB; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = b * 16 + g * 4 + i;
-                    const bool see = (seen >> key & 1u) && t + key <= place &&
-                                     (!x.a.window || t + key > place - x.a.window);
-                    if (!see) s[b][i] = kNothing;
-                }
-        }
-        float top = kNothing;
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[b][i]);
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float m_new = fmaxf(m, top);
-        if (__any(m_new != m)) {
-            const float down = exp2_of(m - settled(m_new));
-            l *= down;
-#pragma unroll
-            for (int v = 0; v < VG; ++v)
-#pragma unroll
-                for (int e = 0; e < VE; ++e) o[v][e] *= down;
-            m = m_new;
-        }
-        const float base = settled(m) - kLift<T>;
-        float p[VK];
-#pragma unroll
-        for (int b = 0; b < KB; ++b) {
-            f4 by{1.0f, 1.0f, 1.0f, 1.0f};
-            if (scaled) by = *reinterpret_cast<const f4 *>(&mine.scale[1][b * 16 + g * 4]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float w = exp2_of(s[b][i] - base);
-                l += w;
-                p[b * 4 + i] = scaled ? w * by[i] : w;
-            }
-        }
-        // a value that is no number must not reach rows that do not see its key
-        bool odd = false;
-        if (parted) {
-#pragma unroll
-            for (int v = 0; v < VG; ++v) {
-                if (!AHEAD) load_values(which, v);
-#pragma unroll
-                for (int j = 0; j < VK; ++j)
-#pragma unroll
-                    for (int i = 0; i < Raw<E, VE>::kWords; ++i)
-                        odd |= has_nonfinite<E>(vr[j][AHEAD ? v : 0].w[i]);
-            }
-            odd = __any(odd);
-        }
-        if (odd) {
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = b * 16 + g * 4 + i;
-                    const bool see = (seen >> key & 1u) && t + key <= place &&
-                                     (!x.a.window || t + key > place - x.a.window);
-                    mine.p[key][n] = see ? p[b * 4 + i] : -1.0f;
-                }
-            wave_fence();
-            for (int key = 0; key < KT; ++key) {
-                const float w = mine.p[key][n];
-                if (w == -1.0f) continue;
-                const E *in = reinterpret_cast<const E *>(mine.at[which][1][key]);
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, s[b][i]);
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float m_new = fmaxf(m, top);
+            if (__any(m_new != m)) {
+                const float down = exp2_of(m - settled(m_new));
+                l *= down;
 #pragma unroll
                 for (int v = 0; v < VG; ++v)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            const int d = (v * 16 + 4 * g + i) * VE + e;
-                            if (d < x.a.v_dim) o[v][e][i] += w * element_of<T, E>(in + d);
-                        }
+                    for (int e = 0; e < VE; ++e) o[v][e] *= down;
+                m = m_new;
             }
-            wave_fence();
-        } else {
-            vec_t pv;
-            if constexpr (sizeof(T) == 2)
+            const float base = settled(m) - kLift<T>;
+            float p[VK];
 #pragma unroll
-                for (int j = 0; j < VK; ++j) pv[j] = (T)p[j];
+            for (int b = 0; b < KB; ++b) {
+                f4 by{1.0f, 1.0f, 1.0f, 1.0f};
+                if (scaled) by = *reinterpret_cast<const f4 *>(&mine.scale[1][b * 16 + g * 4]);
 #pragma unroll
-            for (int v = 0; v < VG; ++v) {
-                constexpr int kWords = VE * (int)sizeof(T) / 4;
-                const int at = AHEAD ? v : 0;
-                if (!AHEAD) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    load_values(which, v);
+                for (int i = 0; i < 4; ++i) {
+                    const float w = exp2_of(s[b][i] - base);
+                    l += w;
+                    p[b * 4 + i] = scaled ? w * by[i] : w;
                 }
-                if (x.a.v_dim != DP) {
+            }
+            // a value that is no number must not reach rows that do not see its key
+            bool odd = false;
+            if (parted) {
+#pragma unroll
+                for (int v = 0; v < VG; ++v) {
+                    if (!AHEAD) load_values(which, v);
+#pragma unroll
+                    for (int j = 0; j < VK; ++j)
+#pragma unroll
+                        for (int i = 0; i < Raw<E, VE>::kWords; ++i)
+                            odd |= has_nonfinite<E>(vr[j][AHEAD ? v : 0].w[i]);
+                }
+                odd = __any(odd);
+            }
+            if (odd) {
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = b * 16 + g * 4 + i;
+                        const bool see = (seen >> key & 1u) && t + key <= place &&
+                                         (!x.a.window || t + key > place - x.a.window);
+                        mine.p[key][n] = see ? p[b * 4 + i] : -1.0f;
+                    }
+                wave_fence();
+                for (int key = 0; key < KT; ++key) {
+                    const float w = mine.p[key][n];
+                    if (w == -1.0f) continue;
                     const int dim = kept(x.a.v_dim);
+                    const E *in = reinterpret_cast<const E *>(mine.at[which][1][key]);
 #pragma unroll
-                    for (int j = 0; j < VK; ++j) settle(vr[j][at], (v * 16 + n) * VE, dim);
+                    for (int v = 0; v < VG; ++v)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int e = 0; e < VE; ++e) {
+                                const int d = (v * 16 + 4 * g + i) * VE + e;
+                                if (d < dim) o[v][e][i] += w * element_of<T, E>(in + d);
+                            }
                 }
-                uint32_t w[VK][kWords];
+                wave_fence();
+            } else {
+                vec_t pv;
+                if constexpr (sizeof(T) == 2)
 #pragma unroll
-                for (int j = 0; j < VK; ++j) expand<T>(vr[j][at], w[j]);
+                    for (int j = 0; j < VK; ++j) pv[j] = (T)p[j];
 #pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    if constexpr (sizeof(T) == 4) {
+                for (int v = 0; v < VG; ++v) {
+                    constexpr int kWords = VE * (int)sizeof(T) / 4;
+                    const int at = AHEAD ? v : 0;
+                    if (!AHEAD) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        load_values(which, v);
+                    }
+                    if (x.a.v_dim & (VE - 1)) {
+                        const int dim = kept(x.a.v_dim);
 #pragma unroll
-                        for (int j = 0; j < VK; ++j)
-                            o[v][e] = mfma16(__builtin_bit_cast(float, w[j][e]), p[j], o[v][e]);
-                    } else {
-                        uint32_t keys[4];
+                        for (int j = 0; j < VK; ++j) settle(vr[j][at], (v * 16 + n) * VE, dim);
+                    }
+                    uint32_t w[VK][kWords];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            keys[j] = __builtin_amdgcn_perm(w[2 * j + 1][e / 2], w[2 * j][e / 2],
-                                                            e & 1 ? 0x07060302u : 0x05040100u);
-                        vec_t a;
-                        __builtin_memcpy(&a, keys, 16);
-                        o[v][e] = mfma16(a, pv, o[v][e]);
+                    for (int j = 0; j < VK; ++j) expand<T>(vr[j][at], w[j]);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                            for (int j = 0; j < VK; ++j)
+                                o[v][e] = mfma16(__builtin_bit_cast(float, w[j][e]), p[j], o[v][e]);
+                        } else {
+                            uint32_t keys[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                keys[j] = __builtin_amdgcn_perm(w[2 * j + 1][e / 2], w[2 * j][e / 2],
+                                                                e & 1 ? 0x07060302u : 0x05040100u);
+                            vec_t a;
+                            __builtin_memcpy(&a, keys, 16);
+                            o[v][e] = mfma16(a, pv, o[v][e]);
+                        }
                     }
                 }
             }
+            which ^= 1;
+            if (AHEAD && more) load_all_values(which);
         }
-        which ^= 1;
-        if (AHEAD && more) load_all_values(which);
-    }
 
-    // the waves joined
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    __syncthreads();  // the addresses' part of LDS is free
-    if (g == 0) {
-        joined.m[wave][n] = m;
-        joined.l[wave][n] = l;
-    }
-#pragma unroll
-    for (int v = 0; v < VG; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < VE; e += 4)
-                *reinterpret_cast<f4 *>(&joined.o[wave][n][(v * 16 + 4 * g + i) * VE + e]) =
-                    f4{o[v][e][i], o[v][e + 1][i], o[v][e + 2][i], o[v][e + 3][i]};
-    __syncthreads();
-    const int r = threadIdx.x >> 4, col = threadIdx.x & 15;
-    const int64_t out_row = (int64_t)piece.tile * 16 + r;
-    if (out_row >= (int64_t)piece.q.count * x.group) return;
-    float top = kNothing;
-#pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) top = fmaxf(top, joined.m[w][r]);
-    float by[kFewWaves], sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) {
-        by[w] = exp2_of(joined.m[w][r] - settled(top));
-        sum += joined.l[w][r] * by[w];
-        by[w] *= by_value;
-    }
-    const bool whole = piece.parts == 1;
-    const int64_t slot = ((number * heads + head) * 16 + r);
-    const int32_t tok = (int32_t)quotient(x.by_group, (uint32_t)out_row);
-    T *out = static_cast<T *>(x.a.out) + (piece.q.first + (int64_t)tok) * x.a.out_token +
-             ((int64_t)head * x.group + (out_row - (int64_t)tok * x.group)) * x.a.out_head;
-    if (!whole && col == 0) x.state[slot] = make_float2(top, sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    for (int d = col * 4; d < x.a.v_dim; d += 64) {
-        f4 y{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int w = 0; w < kFewWaves; ++w)
-            y += by[w] * *reinterpret_cast<const f4 *>(&joined.o[w][r][d]);
-        if (whole) {
-            y = sum == 0.0f ? f4{0.0f, 0.0f, 0.0f, 0.0f} : y * inv;
-            if (d + 4 <= x.a.v_dim) {
-                Floats<4> z = y;
-                store<T, 4, false>(out + d, narrow<T, 4>(z));
-            } else {
-                for (int i = 0; i < x.a.v_dim - d; ++i) out[d + i] = (T)y[i];
-            }
-        } else {
-            float *to = x.partial + slot * x.a.v_dim + d;
-            for (int i = 0; i < min(4, x.a.v_dim - d); ++i) to[i] = y[i];
+        // the waves joined
+        l += __shfl_xor(l, 16, 64);
+        l += __shfl_xor(l, 32, 64);
+        __syncthreads();  // the addresses' part of LDS is free
+        if (g == 0) {
+            joined.m[wave][n] = m;
+            joined.l[wave][n] = l;
         }
+#pragma unroll
+        for (int v = 0; v < VG; ++v)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < VE; e += 4)
+                    *reinterpret_cast<f4 *>(&joined.o[wave][n][(v * 16 + 4 * g + i) * VE + e]) =
+                        f4{o[v][e][i], o[v][e + 1][i], o[v][e + 2][i], o[v][e + 3][i]};
+        __syncthreads();
+        const int r = threadIdx.x >> 4, col = threadIdx.x & 15;
+        const int64_t out_row = (int64_t)tile.tile * 16 + r;
+        if (out_row < (int64_t)tile.q.count * x.group) {
+            float top = kNothing;
+#pragma unroll
+            for (int w = 0; w < kFewWaves; ++w) top = fmaxf(top, joined.m[w][r]);
+            float by[kFewWaves], sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kFewWaves; ++w) {
+                by[w] = exp2_of(joined.m[w][r] - settled(top));
+                sum += joined.l[w][r] * by[w];
+                by[w] *= by_value;
+            }
+            const bool whole = unit0 == 0 && unit1 == tile.units;
+            const int64_t slot = ((number * 2 + (unit0 == 0)) * heads + head) * 16 + r;
+            const int32_t tok = (int32_t)quotient(x.by_group, (uint32_t)out_row);
+            T *out = static_cast<T *>(x.a.out) + (tile.q.first + (int64_t)tok) * x.a.out_token +
+                     ((int64_t)head * x.group + (out_row - (int64_t)tok * x.group)) * x.a.out_head;
+            if (!whole && col == 0) x.state[slot] = make_float2(top, sum);
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            for (int d = col * 4; d < x.a.v_dim; d += 64) {
+                f4 y{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int w = 0; w < kFewWaves; ++w)
+                    y += by[w] * *reinterpret_cast<const f4 *>(&joined.o[w][r][d]);
+                if (whole) {
+                    y = sum == 0.0f ? f4{0.0f, 0.0f, 0.0f, 0.0f} : y * inv;
+                    if (d + 4 <= x.a.v_dim) {
+                        Floats<4> z = y;
+                        store<T, 4, false>(out + d, narrow<T, 4>(z));
+                    } else {
+                        for (int i = 0; i < x.a.v_dim - d; ++i) out[d + i] = (T)y[i];
+                    }
+                } else {
+                    float *to = x.partial + slot * x.a.v_dim + d;
+                    for (int i = 0; i < min(4, x.a.v_dim - d); ++i) to[i] = y[i];
+                }
+            }
+        }
+        unit = tile.first + unit1;
+        if (unit < stop) next_tile(x, tile);
+        __syncthreads();  // LDS is used again
     }
 }
 
@@ -453,39 +471,65 @@ __global__ void __launch_bounds__(256) bmmc_attend_join_kernel(const AttendArgs 
     const int64_t block = block0 + blockIdx.x, heads = x.a.heads;
     const int64_t at = block / heads;
     const int head = (int)(block - at * heads);
-    const Piece piece = find_piece<true>(x, at);
-    if (!piece.found || piece.parts == 1) return;
+    const Tile tile = find_tile<true>(x, at);
+    if (!tile.found) return;
     const int r = blockIdx.y * 4 + wave;
-    const int64_t row = (int64_t)piece.tile * x.plan.rows + r;
-    if (row >= (int64_t)piece.q.count * x.group) return;
-    // parts past the plan's are of starts that fall, and were not made
-    const int parts = (int)max(min((int64_t)piece.parts, x.plan.parts - piece.number), (int64_t)0);
-    const int64_t step = heads * x.plan.rows;
-    const int64_t slot = (piece.number * heads + head) * x.plan.rows + r;
-    float top = kNothing;
-    for (int i = lane; i < parts; i += 64) top = fmaxf(top, x.state[slot + i * step].x);
+    const int64_t row = (int64_t)tile.tile * x.plan.rows + r;
+    if (row >= (int64_t)tile.q.count * x.group) return;
+    const int64_t all = all_units(x);
+    const int32_t share0 = share_of(x, all, tile.first);
+    const int32_t share1 = share_of(x, all, tile.first + tile.units - 1);
+    if (share0 == share1) return;  // the tile was one workgroup's
+    // A lane for each share; those without a unit have made nothing, and the first
+    // holds the tile's begin.
+    const auto slot_of = [&](int32_t share) {
+        return (((int64_t)share * 2 + (share == share0)) * heads + head) * x.plan.rows + r;
+    };
+    const auto state_of = [&](int32_t share) {
+        const bool made = share <= share1 && first_of(x, all, share) < first_of(x, all, share + 1);
+        return made ? x.state[slot_of(share)] : make_float2(kNothing, 0.0f);
+    };
+    float2 state = state_of(share0 + lane);
+    float top = state.x;
+    for (int32_t s = share0 + 64; s <= share1; s += 64) top = fmaxf(top, state_of(s + lane).x);
 #pragma unroll
     for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-    float sum = 0.0f;
-    for (int i = lane; i < parts; i += 64) {
-        const float2 s = x.state[slot + i * step];
-        sum += s.y * exp2_of(s.x - settled(top));
+    const int dim = x.a.v_dim;
+    float sum = 0.0f, y[8] = {};
+    for (int32_t s = share0; s <= share1; s += 64) {
+        if (s > share0) state = state_of(s + lane);
+        const float by = exp2_of(state.x - settled(top));
+        sum += state.y * by;
+        uint64_t left = __ballot(by != 0.0f);
+        while (left) {
+            // four parts at a time are on their way
+            constexpr int kAhead = 4;
+            float in[kAhead][8], weight[kAhead];
+            int count = 0;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int l = left ? __ffsll((unsigned long long)left) - 1 : 0;
+                weight[k] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, by), l));
+                if (!left) break;
+                left &= left - 1;
+                ++count;
+                const float *from = x.partial + slot_of(s + l) * dim;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j * 64 + lane < dim) in[k][j] = from[j * 64 + lane];
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (k < count)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j * 64 + lane < dim) y[j] += weight[k] * in[k][j];
+        }
     }
     sum = wave_sum(sum);
-    const int32_t token = (int32_t)(row / x.group);
-    T *out = static_cast<T *>(x.a.out) + (piece.q.first + (int64_t)token) * x.a.out_token +
+    const int32_t token = (int32_t)quotient(x.by_group, (uint32_t)row);
+    T *out = static_cast<T *>(x.a.out) + (tile.q.first + (int64_t)token) * x.a.out_token +
              ((int64_t)head * x.group + (row - (int64_t)token * x.group)) * x.a.out_head;
-    const int dim = x.a.v_dim;
-    float y[8] = {};
-    for (int i = 0; i < parts; ++i) {
-        const float m = x.state[slot + i * step].x;
-        if (m == kNothing) continue;
-        const float by = exp2_of(m - settled(top));
-        const float *in = x.partial + (slot + i * step) * dim;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j * 64 + lane < dim) y[j] += by * in[j * 64 + lane];
-    }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (j * 64 + lane < dim) out[j * 64 + lane] = (T)(sum == 0.0f ? 0.0f : y[j] / sum);
@@ -495,7 +539,8 @@ template <typename T, typename E, int DP, int KB, bool AHEAD>
 int few(const AttendArgs &x, hipStream_t s) {
     using F = Few<T, E, DP, KB, AHEAD>;
     const auto kernel = bmmc_attend_few_kernel<T, E, DP, KB, AHEAD>;
-    const int64_t blocks = x.plan.parts * x.a.heads + (x.a.clear_rest && x.a.starts ? kClearBlocks : 0);
+    const int64_t blocks = (x.plan.shares ? x.plan.shares : x.plan.tiles) * x.a.heads +
+                           (x.a.clear_rest && x.a.starts ? kClearBlocks : 0);
     return in_launches(blocks, 64 * kFewWaves, [&](uint32_t nb, int64_t b0) {
         hipLaunchKernelGGL(kernel, dim3(nb), dim3(64 * kFewWaves), F::kLds, s, x, b0);
     });

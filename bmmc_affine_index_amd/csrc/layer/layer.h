@@ -15,16 +15,16 @@ namespace bmmc {
 // rows over the keys that any of them sees; a unit is as many keys as a
 // workgroup takes at once.
 //
-// Few rows leave few workgroups, so the keys of a tile are cut into parts that
-// run at the same time and are joined afterwards: into as many as make the
-// parts of all sequences about `target`, by the lengths on the device, so that
-// a long sequence among short ones has more of them.
+// Few rows leave few workgroups, so the units of all tiles, one after the other,
+// are cut into as many equal shares as run at the same time: a workgroup takes
+// one of them, be it a part of a tile or several tiles.  Where it ends inside a
+// tile, what it has of the tile goes to the workspace, and a second launch joins
+// the parts.  The lengths are on the device, and so are the shares: a long
+// sequence among short ones is spread over many.
 struct AttendPlan {
     int32_t rows, unit;   // of a tile; keys of a step
-    int32_t target;       // parts of all sequences; 0: each tile is one part
-    int32_t least;        // units a part at least
-    int64_t tiles;        // tiles at most
-    int64_t parts;        // parts at most
+    int32_t shares;       // of a key head; 0: each tile is one workgroup's
+    int64_t tiles;        // at most
 };
 
 struct AttendArgs {
@@ -35,8 +35,10 @@ struct AttendArgs {
     int32_t group;
     int32_t rows_scaled;  // scales by place, not by head alone
     int64_t reach;        // places the table has
-    float *partial;       // parts, heads, rows, v_dim
-    float2 *state;        // parts, heads, rows: maximum and sum
+    // Of each share: a tile's end that it begins with, and one's begin that it ends
+    // with; [shares, 2, heads, rows, v_dim] and [shares, 2, heads, rows]
+    float *partial;
+    float2 *state;  // maximum and sum
 };
 
 constexpr int kClearBlocks = 32;  // workgroups that clear rows of no sequence
@@ -44,6 +46,7 @@ constexpr int kClearBlocks = 32;  // workgroups that clear rows of no sequence
 // How a call is cut; sizes alone tell.
 AttendPlan attend_plan(const bmmc_attention &a);
 int launch_attend_few(const AttendArgs &a, hipStream_t s);
+int launch_attend_many(const AttendArgs &a, hipStream_t s);
 int launch_attend_join(const AttendArgs &a, hipStream_t s);
 
 // ---- the cache --------------------------------------------------------------

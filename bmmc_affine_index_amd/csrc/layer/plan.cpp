@@ -8,8 +8,7 @@ namespace bmmc {
 
 namespace {
 
-// Workgroups that keep the card busy: two or three on each of its 256 compute units.
-constexpr int64_t kBusy = 1024;
+constexpr int64_t kUnits = 256;  // compute units
 
 }  // namespace
 
@@ -19,16 +18,17 @@ AttendPlan attend_plan(const bmmc_attention &a) {
     const bool wide = a.type == BMMC_F32;
     const int dim = std::max(a.k_dim, a.v_dim);
     AttendPlan p{};
-    p.rows = 16;
+    const bool many = !wide && dim <= 256 && a.tokens * group > 32 * filled;
+    p.rows = many ? 128 : 16;
     // four waves, of 16 keys each where long rows of 32 bits leave no registers for 32
-    p.unit = wide && dim > 64 ? 64 : 128;
+    p.unit = many || (wide && dim > 64) ? 64 : 128;
     p.tiles = a.starts ? a.tokens * group / p.rows + filled
                        : a.tokens * ((group + p.rows - 1) / p.rows);
-    p.least = 1;
+    // workgroups of a compute unit, by the registers that a head's elements take
+    const int64_t busy = kUnits * (dim <= 64 ? 3 : dim <= 128 ? 2 : 1);
     const int64_t reach = a.table_width * a.page_size;
-    if (p.tiles * a.heads < 2 * kBusy && reach > p.unit)
-        p.target = (int32_t)std::max<int64_t>(kBusy / a.heads, 1);
-    p.parts = p.tiles + p.target;
+    if (p.tiles * a.heads < 4 * busy && reach > p.unit)
+        p.shares = (int32_t)std::max<int64_t>(busy / a.heads, 1);
     return p;
 }
 

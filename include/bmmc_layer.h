@@ -55,7 +55,8 @@ typedef struct bmmc_scaled_cache {
  * key head h' = h / (q_heads / heads) and a_j = scale <q[t, h], k[j, h']>
  *     out[t, h] = sum of exp(a_j) v[j, h'] / sum of exp(a_j)
  * over them, and zeros where there is none of any weight.  What a place that is
- * not seen holds does not matter, be it a NaN.  A place that is seen counts
+ * not seen holds does not matter, be it a NaN; places from 2^31 - 4097 on are not
+ * seen.  A place that is seen counts
  * whatever its weight: an infinity or a NaN in its value shows.
  *
  * Scores, sums and the running maximum are in 32 bits; the weights of one

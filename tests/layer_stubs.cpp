@@ -5,6 +5,7 @@
 namespace bmmc {
 
 int launch_attend_few(const AttendArgs &, hipStream_t) { return BMMC_ERR_HIP; }
+int launch_attend_many(const AttendArgs &, hipStream_t) { return BMMC_ERR_HIP; }
 int launch_attend_join(const AttendArgs &, hipStream_t) { return BMMC_ERR_HIP; }
 int launch_cache_quantize(const QuantizeArgs &, hipStream_t) { return BMMC_ERR_HIP; }
 int launch_cache_read(const ReadArgs &, hipStream_t) { return BMMC_ERR_HIP; }
