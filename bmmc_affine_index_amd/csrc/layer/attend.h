@@ -208,6 +208,9 @@ __device__ __forceinline__ void clear_rest(const AttendArgs &x, int64_t block, i
 // What stands for a row that is not there: zeros, as long as the longest head.
 __device__ const uint32_t __attribute__((aligned(16))) kZeros[BMMC_MAX_HEAD_DIM] = {};
 
+// Rows are in global memory, which the compiler is told: their addresses come from
+// LDS, and loads through generic addresses would wait for LDS as well.
+//
 // N elements of a row from element `at` on, zeros past its end.  Rows have N
 // elements at least; the last vector of a row that is no whole number of them
 // ends with the row, and `settle` shifts it into its place when the elements are
@@ -223,7 +226,7 @@ __device__ __forceinline__ Raw<E, N> fetch(const uint8_t *row, int at, int dim) 
     typedef bytes_t packed_t __attribute__((aligned(sizeof(E))));
     const uint8_t *from = row + min(at, dim - N) * (int)sizeof(E);
     if (at >= dim) from = reinterpret_cast<const uint8_t *>(kZeros);
-    const bytes_t v = *reinterpret_cast<const packed_t *>(from);
+    const bytes_t v = *(const __attribute__((address_space(1))) packed_t *)from;
     Raw<E, N> r;
     __builtin_memcpy(r.w, &v, sizeof(r.w));
     return r;
@@ -233,7 +236,7 @@ template <typename E, int N>
 __device__ __forceinline__ Raw<E, N> fetch_whole(const uint8_t *row, int at) {
     typedef typename Vec<uint8_t, Raw<E, N>::kBytes>::raw bytes_t;
     typedef bytes_t packed_t __attribute__((aligned(sizeof(E))));
-    const bytes_t v = *reinterpret_cast<const packed_t *>(row + at * (int)sizeof(E));
+    const bytes_t v = *(const __attribute__((address_space(1))) packed_t *)(row + at * (int)sizeof(E));
     Raw<E, N> r;
     __builtin_memcpy(r.w, &v, sizeof(r.w));
     return r;
@@ -332,10 +335,11 @@ __device__ __forceinline__ uint64_t seen_of(int32_t ahead, int64_t window) {
 
 // One element of a row.
 template <typename T, typename E> __device__ __forceinline__ float element_of(const E *p) {
+    const auto *q = (const __attribute__((address_space(1))) E *)p;
     if constexpr (sizeof(E) == 1)
-        return __builtin_amdgcn_cvt_f32_fp8((int)*p, 0);
+        return __builtin_amdgcn_cvt_f32_fp8((int)*q, 0);
     else
-        return (float)*p;
+        return (float)*q;
 }
 
 // c += a b of 16 x 16: lane l holds row (a) or column (b) l % 16 and 8 (32 bits:
@@ -374,12 +378,28 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// The row of a place in a cache, in elements; -1 where there is none.
-__device__ __forceinline__ int32_t page_of(const AttendArgs &x, const int32_t *table, int32_t place,
+// The table's entry for a place before `end` (the last one for those behind it), as
+// it is: looked at later, by page_of, so that nothing waits for it here.
+__device__ __forceinline__ int32_t entry_of(const AttendArgs &x, const int32_t *table, int32_t place,
+                                            int32_t end) {
+    return table[quotient(x.by_page, (uint32_t)min(place, end - 1))];
+}
+// The page of a place, -1 where there is none.
+__device__ __forceinline__ int32_t page_of(const AttendArgs &x, int32_t entry, int32_t place,
                                            int32_t end) {
-    if (place >= end) return -1;
-    const int32_t page = table[quotient(x.by_page, (uint32_t)place)];
-    return page >= 0 && page < x.a.pages ? page : -1;
+    return place < end && entry >= 0 && entry < x.a.pages ? entry : -1;
+}
+
+// The largest of a lane's number and those of the lanes 16 (32) away.
+__device__ __forceinline__ float max_over_16(float v) {
+    const uint32_t w = __builtin_bit_cast(uint32_t, v);
+    const auto both = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
+}
+__device__ __forceinline__ float max_over_32(float v) {
+    const uint32_t w = __builtin_bit_cast(uint32_t, v);
+    const auto both = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
 }
 
 }  // namespace dev

@@ -149,11 +149,11 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
         const int64_t by_place = half ? x.v.place_stride : x.k.place_stride;
         const int64_t by_head = (half ? x.v.head_stride : x.k.head_stride) * head;
         const bool scaled = kNarrow && x.rows_scaled;
-        const auto look = [&](int32_t t) {
-            return kl < KT ? page_of(x, table, t + kl, span.to) : -1;
-        };
+        const auto look = [&](int32_t t) { return entry_of(x, table, t + kl, span.to); };
         float scale_next = 0.0f;
-        const auto put = [&](int32_t page, int32_t t, int which) {
+        // Rows of the tile at t into LDS; bits of the keys that are there
+        const auto put = [&](int32_t entry, int32_t t, int which) {
+            const int32_t page = kl < KT ? page_of(x, entry, t + kl, span.to) : -1;
             const int32_t in = t + kl - (int32_t)quotient(x.by_page, (uint32_t)(t + kl)) * (int32_t)x.by_page.d;
             if (kl < KT)
                 mine.at[which][half][kl] =
@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                                       : c.scale[page * c.scale_page + in * c.scale_place + head * c.scale_head];
             }
             wave_fence();
+            return (uint32_t)__ballot(page >= 0);  // the keys' lanes
         };
         Raw<E, CE> kr[AHEAD ? KB : 1][KG];
         Raw<E, VE> vr[VK][AHEAD ? VG : 1];
@@ -213,18 +214,25 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
         const int32_t step = kFewWaves * KT;
         int32_t t = span.from + wave * KT;
         int which = 0;
-        int32_t page = -1, page_next = -1;
+        // What is on its way, in this order: the table's entries for the tile after the
+        // next, the next tile's keys, its values.  A wait for the first leaves the others.
+        int32_t entry = -1;
+        uint32_t seen = 0;
         if (t < span.to) {
-            page = look(t);
-            put(page, t, 0);
-            if (AHEAD) {
-                load_all_keys(0);
-                load_all_values(0);
-            }
-            if (t + step < span.to) page_next = look(t + step);
+            seen = put(look(t), t, 0);
+            entry = look(t + step);
+            __builtin_amdgcn_sched_barrier(0);
+            if (AHEAD) load_all_keys(0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (AHEAD) load_all_values(0);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        // the queries are here before the loop, in which nothing waits for them
+        if constexpr (!F::kQueriesInLds)
+#pragma unroll
+            for (int k = 0; k < NK; ++k) asm volatile("" : "+v"(q[k]));
         for (; t < span.to; t += step) {
-            const uint32_t seen = (uint32_t)__ballot(page >= 0);  // the keys' lanes
+            const uint32_t there = seen;
             f4 s[KB];
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
@@ -260,13 +268,13 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                 if (kl < KT) mine.scale[half][kl] = scale_next;
                 wave_fence();
             }
-            const bool more = t + step < span.to;
-            if (more) {
-                page = page_next;
-                put(page, t + step, which ^ 1);
-                if (AHEAD) load_all_keys(which ^ 1);
-                if (t + 2 * step < span.to) page_next = look(t + 2 * step);
-            }
+            // behind the last tile there are rows of zeros: a loop without branches
+            // around its loads, or the compiler would wait for all of them at once
+            seen = put(entry, t + step, which ^ 1);
+            entry = look(t + 2 * step);
+            __builtin_amdgcn_sched_barrier(0);
+            if (AHEAD) load_all_keys(which ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 f4 by{c, c, c, c};
@@ -276,24 +284,22 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
             // the tile has keys that are not there, or that some rows do not see
             const bool parted = t + KT - 1 > span.first ||
                                 (x.a.window && t <= span.last - x.a.window);
-            if (parted || ~seen << (32 - KT)) {
+            uint32_t see = there;
+            if (parted || ~there << (32 - KT)) {
+                see &= (uint32_t)seen_of(place - t, x.a.window);
+                const uint32_t lane_sees = see >> 4 * g;
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = b * 16 + g * 4 + i;
-                        const bool see = (seen >> key & 1u) && t + key <= place &&
-                                         (!x.a.window || t + key > place - x.a.window);
-                        if (!see) s[b][i] = kNothing;
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        if (!(lane_sees & 1u << (b * 16 + i))) s[b][i] = kNothing;
             }
             float top = kNothing;
 #pragma unroll
             for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, s[b][i]);
-            top = fmaxf(top, __shfl_xor(top, 16, 64));
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            top = max_over_32(max_over_16(top));
             const float m_new = fmaxf(m, top);
             if (__any(m_new != m)) {
                 const float down = exp2_of(m - settled(m_new));
@@ -337,9 +343,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int key = b * 16 + g * 4 + i;
-                        const bool see = (seen >> key & 1u) && t + key <= place &&
-                                         (!x.a.window || t + key > place - x.a.window);
-                        mine.p[key][n] = see ? p[b * 4 + i] : -1.0f;
+                        mine.p[key][n] = see >> key & 1u ? p[b * 4 + i] : -1.0f;
                     }
                 wave_fence();
                 for (int key = 0; key < KT; ++key) {
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                 }
             }
             which ^= 1;
-            if (AHEAD && more) load_all_values(which);
+            if (AHEAD) load_all_values(which);
         }
 
         // the waves joined

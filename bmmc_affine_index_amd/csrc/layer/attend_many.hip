@@ -34,13 +34,6 @@ __device__ __forceinline__ f16x mfma32(Product<bf16_t>::vec a, Product<bf16_t>::
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// The larger of a lane's number and that of the lane 32 away.
-__device__ __forceinline__ float max_of_halves(float v) {
-    const auto both = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v),
-                                                       __builtin_bit_cast(uint32_t, v), false, false);
-    return fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
-}
-
 // The order of a block's N products and EACH reads from LDS for each of them: reads
 // for AHEAD products come first, so that no product waits for its own.
 template <int N, int EACH, int AHEAD> __device__ __forceinline__ void reads_ahead() {
@@ -180,12 +173,11 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
             }
         }
 
-        const auto look = [&](int32_t t) {
-            return looks && t < span.to ? page_of(x, table, t + key_row, span.to) : -1;
-        };
+        const auto look = [&](int32_t t) { return entry_of(x, table, t + key_row, span.to); };
         float scale_next = 0.0f;
-        const auto put = [&](int32_t page, int32_t t, int which) {
+        const auto put = [&](int32_t entry, int32_t t, int which) {
             if (!looks) return;
+            const int32_t page = page_of(x, entry, t + key_row, span.to);
             const int32_t in =
                 t + key_row - (int32_t)quotient(x.by_page, (uint32_t)(t + key_row)) * (int32_t)x.by_page.d;
             lds.row[which][of_values][key_row] =
@@ -283,15 +275,15 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
         float m = kNothing, l = 0.0f;
         int32_t t = span.from;
         int which = 0;
-        int32_t page_next = -1;
+        int32_t entry = -1;  // of the tile after the next
         if (t < span.to) {
             put(look(t), t, 0);
             __syncthreads();
             load(0);
-            page_next = look(t + kKeys);
+            entry = look(t + kKeys);
             store(t, 0);
-            put(page_next, t + kKeys, 1);
-            page_next = look(t + 2 * kKeys);
+            put(entry, t + kKeys, 1);
+            entry = look(t + 2 * kKeys);
             __syncthreads();
         }
         // the queries are here before the loop, in which nothing waits for them
@@ -348,7 +340,7 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-                top = max_of_halves(top) * c;
+                top = max_over_32(top) * c;
                 // Weights may grow to 2^8 before the sums are brought down to a new
                 // maximum, which both types hold
                 if (__any(top > m + 8.0f)) {
@@ -438,8 +430,8 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                 if (t + 2 * kKeys < span.to) {
                     // the slot's readers are this tile's loads, odd values and masks
                     __syncthreads();
-                    put(page_next, t + 2 * kKeys, which);
-                    page_next = look(t + 3 * kKeys);
+                    put(entry, t + 2 * kKeys, which);
+                    entry = look(t + 3 * kKeys);
                 }
             }
             __syncthreads();
