@@ -91,8 +91,10 @@ int check_attention_sizes(const bmmc_attention &a) {
     return check_pages(a.pages, a.page_size, a.table, a.batch, a.table_width, a.table_stride);
 }
 
+int32_t pitch_of(const bmmc_attention &a) { return (a.v_dim + 3) / 4 * 4; }
+
 int64_t workspace_floats(const bmmc_attention &a, const AttendPlan &p) {
-    return 2 * (int64_t)p.shares * a.heads * p.rows * a.v_dim;
+    return 2 * (int64_t)p.shares * a.heads * p.rows * pitch_of(a);
 }
 int64_t workspace_states(const bmmc_attention &a, const AttendPlan &p) {
     return 2 * (int64_t)p.shares * a.heads * p.rows;
@@ -106,7 +108,7 @@ int64_t bmmc_cache_attention_workspace(const bmmc_attention *a) {
     if (!a || check_attention_sizes(*a) != BMMC_OK) return -1;
     if (a->tokens == 0) return 0;
     const AttendPlan p = attend_plan(*a);
-    return workspace_floats(*a, p) * 4 + workspace_states(*a, p) * 8;
+    return workspace_floats(*a, p) * 4 + workspace_states(*a, p) * 8 + p.shares * 16;
 }
 
 int bmmc_cache_attention(const bmmc_attention *a, const bmmc_scaled_cache *k_cache,
@@ -152,8 +154,14 @@ int bmmc_cache_attention(const bmmc_attention *a, const bmmc_scaled_cache *k_cac
     // places and the tiles behind them stay in 32 bits
     x.reach = std::min(a->table_width * a->page_size, kMaxIndex - 4096);
     x.a.window = std::min(a->window, kMaxIndex);
+    x.pitch = pitch_of(*a);
     x.partial = static_cast<float *>(workspace);
     x.state = reinterpret_cast<float2 *>(x.partial + workspace_floats(*a, x.plan));
+    x.begun = reinterpret_cast<int4 *>(x.state + workspace_states(*a, x.plan));
+    x.by_shares = fast_div((uint32_t)std::max(x.plan.shares, 1));
+    // however the sequences lie, none has more tiles than all rows make
+    x.few_units = (double)std::max<int64_t>(a->batch, 1) * (double)x.plan.tiles *
+                      ((double)x.reach / x.plan.unit + 2) < 2147483648.0;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     st = x.plan.rows > 16 ? launch_attend_many(x, s) : launch_attend_few(x, s);
     return st == BMMC_OK && x.plan.shares ? launch_attend_join(x, s) : st;

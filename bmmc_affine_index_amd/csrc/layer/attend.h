@@ -69,30 +69,6 @@ __device__ __forceinline__ int32_t units_of(const AttendArgs &x, const Sequence 
     return max(ceil_div(r.to - r.from, x.plan.unit), 1);
 }
 
-__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
-}
-
-// Units of all tiles, by every wave for itself.
-__device__ __forceinline__ int64_t all_units(const AttendArgs &x) {
-    int64_t all = 0;
-    for (int32_t s = threadIdx.x & 63; s < (int32_t)x.a.batch; s += 64) {
-        const Sequence q = sequence_at(x, s);
-        all += (int64_t)tiles_of(x, q) * units_of(x, q);
-    }
-    return uniform(wave_sum64(all));
-}
-
-// Units [first(w), first(w + 1)) are share w's.
-__device__ __forceinline__ int64_t first_of(const AttendArgs &x, int64_t all, int64_t w) {
-    return all * w / x.plan.shares;
-}
-__device__ __forceinline__ int32_t share_of(const AttendArgs &x, int64_t all, int64_t unit) {
-    return (int32_t)(((unit + 1) * x.plan.shares - 1) / all);
-}
-
 // A tile of a sequence, and its first unit among all.
 struct Tile {
     bool found;
@@ -101,55 +77,158 @@ struct Tile {
     Sequence q;
 };
 
-// The tile that holds unit `want` of all or, BY_TILE, the want'th.  Every wave
-// looks for itself, 64 sequences at a time: a prefix sum over the lanes tells
-// which sequence holds it.
-template <bool BY_TILE> __device__ __forceinline__ Tile find_tile(const AttendArgs &x, int64_t want) {
+// Sums over the lanes before this one and, of all, in *total.
+template <typename W> __device__ __forceinline__ W sum_before(W v, W *total) {
     const int lane = threadIdx.x & 63;
-    const int32_t batch = (int32_t)x.a.batch;
-    Tile t{};
-    int64_t before = 0, units_before = 0;
-    for (int32_t s0 = 0; s0 < batch; s0 += 64) {
-        Sequence q{};
-        int32_t tiles = 0, units = 1;
-        if (s0 + lane < batch) {
-            q = sequence_at(x, s0 + lane);
-            tiles = tiles_of(x, q);
-            units = units_of(x, q);
-        }
-        const int64_t work = (int64_t)tiles * units, mine = BY_TILE ? tiles : work;
-        int64_t upto = mine, units_upto = work;
+    W upto = v;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t o = __shfl_up(upto, d, 64);
-            if (lane >= d) upto += o;
-            if (BY_TILE) {
-                const int64_t uo = __shfl_up(units_upto, d, 64);
-                if (lane >= d) units_upto += uo;
-            }
-        }
-        const int64_t from = before + upto - mine;
-        const uint64_t here = __ballot(want >= from && want < from + mine);
+    for (int d = 1; d < 64; d <<= 1) {
+        const W o = __shfl_up(upto, d, 64);
+        if (lane >= d) upto += o;
+    }
+    *total = uniform(__shfl(upto, 63, 64));
+    return upto - v;
+}
+
+// 64 sequences, one a lane.
+struct Sequences {
+    Sequence q;
+    int32_t tiles, units;
+};
+__device__ __forceinline__ Sequences sequences_from(const AttendArgs &x, int32_t s) {
+    Sequences r{};
+    r.units = 1;
+    if (s < (int32_t)x.a.batch) {
+        r.q = sequence_at(x, s);
+        r.tiles = tiles_of(x, r.q);
+        r.units = units_of(x, r.q);
+    }
+    return r;
+}
+
+// The tile that is number `in` of lane l's, or holds its unit `in`.
+template <bool BY_TILE>
+__device__ __forceinline__ Tile tile_in(const Sequences &r, int l, int32_t s0, int64_t start, int64_t in) {
+    Tile t;
+    t.found = true;
+    t.seq = s0 + l;
+    t.units = __builtin_amdgcn_readlane(r.units, l);
+    t.q.first = __builtin_amdgcn_readlane(r.q.first, l);
+    t.q.count = __builtin_amdgcn_readlane(r.q.count, l);
+    t.q.length = __builtin_amdgcn_readlane(r.q.length, l);
+    t.q.end = __builtin_amdgcn_readlane(r.q.end, l);
+    if (BY_TILE)
+        t.tile = (int32_t)in;
+    else if (in >> 31)
+        t.tile = uniform((int32_t)(in / t.units));
+    else
+        t.tile = uniform((int32_t)((uint32_t)in / (uint32_t)t.units));
+    t.first = start + (int64_t)t.tile * t.units;
+    return t;
+}
+
+// The want'th tile of all.  Every wave looks for itself, 64 sequences at a time: a
+// prefix sum over the lanes tells which of them holds it.
+__device__ __forceinline__ Tile find_tile(const AttendArgs &x, int64_t want) {
+    for (int32_t s0 = 0; s0 < (int32_t)x.a.batch; s0 += 64) {
+        const Sequences r = sequences_from(x, s0 + (threadIdx.x & 63));
+        int64_t all;
+        const int64_t before = sum_before((int64_t)r.tiles, &all);
+        const uint64_t here = __ballot(want >= before && want < before + r.tiles);
         if (here) {
             const int l = __ffsll((unsigned long long)here) - 1;
-            const int64_t in = want - uniform(__shfl(from, l, 64));
-            const int64_t start = BY_TILE ? units_before + __shfl(units_upto - work, l, 64)
-                                          : __shfl(from, l, 64);
-            t.found = true;
-            t.seq = s0 + l;
-            t.units = __builtin_amdgcn_readlane(units, l);
-            t.q.first = __builtin_amdgcn_readlane(q.first, l);
-            t.q.count = __builtin_amdgcn_readlane(q.count, l);
-            t.q.length = __builtin_amdgcn_readlane(q.length, l);
-            t.q.end = __builtin_amdgcn_readlane(q.end, l);
-            t.tile = __builtin_amdgcn_readfirstlane((int32_t)(BY_TILE ? in : in / t.units));
-            t.first = uniform(start) + (int64_t)t.tile * t.units;
-            return t;
+            // its units are its own: it is no part of a share
+            return tile_in<true>(r, l, s0, 0, want - uniform(__shfl(before, l, 64)));
         }
-        before += uniform(__shfl(upto, 63, 64));
-        units_before += uniform(__shfl(units_upto, 63, 64));
+        want -= all;
     }
-    return t;
+    return Tile{};
+}
+
+// A share's units of all, [from, to), and the tile that it begins in.
+struct Share {
+    int64_t each, over;  // shares below `over` have one unit more than the others
+    int64_t from, to;
+    Tile tile;
+    __device__ __forceinline__ int64_t first_of(int64_t w) const { return w * each + min(w, over); }
+    // The share that has unit u.
+    __device__ __forceinline__ int32_t of(int64_t u) const {
+        const int64_t more = over * (each + 1);
+        if (u < more) return (int32_t)(u / (each + 1));
+        return (int32_t)(over + (u - more) / each);
+    }
+};
+
+// W: what holds the number of all units.
+template <typename W> __device__ __forceinline__ Share find_share(const AttendArgs &x, int32_t number) {
+    const int lane = threadIdx.x & 63;
+    const int32_t batch = (int32_t)x.a.batch;
+    Sequences r = sequences_from(x, lane);
+    W all, before = sum_before((W)((W)r.tiles * r.units), &all);
+    for (int32_t s0 = 64; s0 < batch; s0 += 64) {
+        const Sequences more = sequences_from(x, s0 + lane);
+        W sum;
+        sum_before((W)((W)more.tiles * more.units), &sum);
+        all += sum;
+    }
+    Share p;
+    p.each = sizeof(W) == 4 ? (int64_t)quotient(x.by_shares, (uint32_t)all) : (int64_t)(all / x.plan.shares);
+    p.over = all - p.each * x.plan.shares;
+    p.from = p.first_of(number);
+    p.to = p.first_of(number + 1);
+    p.tile = Tile{};
+    W start = 0;
+    for (int32_t s0 = 0; p.from < p.to && s0 < batch; s0 += 64) {
+        if (s0) {
+            r = sequences_from(x, s0 + lane);
+            W sum;
+            before = sum_before((W)((W)r.tiles * r.units), &sum) + start;
+            start += sum;
+        } else {
+            start = uniform(__shfl((W)(before + (W)r.tiles * r.units), 63, 64));
+        }
+        const W want = (W)p.from;
+        const uint64_t here = __ballot(want >= before && want < before + (W)r.tiles * r.units);
+        if (here) {
+            const int l = __ffsll((unsigned long long)here) - 1;
+            const int64_t first = uniform(__shfl(before, l, 64));
+            p.tile = tile_in<false>(r, l, s0, first, p.from - first);
+            return p;
+        }
+    }
+    p.to = p.from;
+    return p;
+}
+__device__ __forceinline__ Tile uniform(const Tile &t) {
+    return Tile{t.found,
+                uniform(t.seq),
+                uniform(t.tile),
+                uniform(t.units),
+                uniform(t.first),
+                Sequence{uniform(t.q.first), uniform(t.q.count), uniform(t.q.length), uniform(t.q.end)}};
+}
+__device__ __forceinline__ Share find_share(const AttendArgs &x, int32_t number) {
+    Share p = x.few_units ? find_share<int32_t>(x, number) : find_share<int64_t>(x, number);
+    p.each = uniform(p.each);
+    p.over = uniform(p.over);
+    p.from = uniform(p.from);
+    p.to = uniform(p.to);
+    p.tile = uniform(p.tile);
+    return p;
+}
+
+// What a share leaves for the join of the tile that it began and did not end.
+struct Begun {
+    int32_t last_share;  // the tile's; -1: there is no such tile
+    int32_t first, count, tile;
+};
+__device__ __forceinline__ void leave_begun(const AttendArgs &x, int32_t number, const Share &p,
+                                            const Tile &t) {
+    // t: the share's last tile, p.to its end
+    const bool begun = t.found && t.first >= p.from && t.first + t.units > p.to;
+    if (threadIdx.x == 0)
+        x.begun[number] = begun ? int4{p.of(t.first + t.units - 1), t.q.first, t.q.count, t.tile}
+                                : int4{-1, 0, 0, 0};
 }
 
 // The tile after t; not found behind the last.

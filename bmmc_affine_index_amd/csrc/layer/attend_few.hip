@@ -16,6 +16,8 @@
 // rows of a tile.  Four waves of a workgroup take tiles of 32 keys in turn, each
 // with a maximum of its own, and are joined through LDS at the end; a tile's
 // keys are on their way while the one before is in the products.
+#include <algorithm>
+
 #include "attend.h"
 
 namespace bmmc {
@@ -93,16 +95,16 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
     }
     const int64_t number = block / heads;
     const int head = (int)(block - number * heads);
+    Share share{};
     Tile tile;
     int64_t unit, stop;  // of all: this workgroup's
     if (x.plan.shares) {
-        const int64_t all = all_units(x);
-        unit = first_of(x, all, number);
-        stop = first_of(x, all, number + 1);
-        if (unit >= stop) return;
-        tile = find_tile<false>(x, unit);
+        share = find_share(x, (int32_t)number);
+        unit = share.from;
+        stop = share.to;
+        tile = share.tile;
     } else {
-        tile = find_tile<true>(x, number);
+        tile = uniform(find_tile(x, number));
         unit = tile.first;
         stop = tile.first + tile.units;
     }
@@ -457,8 +459,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                         for (int i = 0; i < x.a.v_dim - d; ++i) out[d + i] = (T)y[i];
                     }
                 } else {
-                    float *to = x.partial + slot * x.a.v_dim + d;
-                    for (int i = 0; i < min(4, x.a.v_dim - d); ++i) to[i] = y[i];
+                    *reinterpret_cast<f4 *>(x.partial + slot * x.pitch + d) = y;
                 }
             }
         }
@@ -466,77 +467,102 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
         if (unit < stop) next_tile(x, tile);
         __syncthreads();  // LDS is used again
     }
+    if (x.plan.shares && head == 0) leave_begun(x, (int32_t)number, share, tile);
 }
 
-// The parts of a tile joined: a wave for each row.
-template <typename T>
+// The parts of a tile joined, by the share that began it; a wave takes a row at a
+// time, LANES lanes a part with 4 C elements each.
+template <typename T, int LANES, int C>
 __global__ void __launch_bounds__(256) bmmc_attend_join_kernel(const AttendArgs x, int64_t block0) {
+    constexpr int kParts = 64 / LANES;       // that a wave loads at once
+    constexpr int kAhead = C == 1 ? 8 : 4;   // such loads on their way
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t block = block0 + blockIdx.x, heads = x.a.heads;
-    const int64_t at = block / heads;
-    const int head = (int)(block - at * heads);
-    const Tile tile = find_tile<true>(x, at);
-    if (!tile.found) return;
-    const int r = blockIdx.y * 4 + wave;
-    const int64_t row = (int64_t)tile.tile * x.plan.rows + r;
-    if (row >= (int64_t)tile.q.count * x.group) return;
-    const int64_t all = all_units(x);
-    const int32_t share0 = share_of(x, all, tile.first);
-    const int32_t share1 = share_of(x, all, tile.first + tile.units - 1);
-    if (share0 == share1) return;  // the tile was one workgroup's
-    // A lane for each share; those without a unit have made nothing, and the first
-    // holds the tile's begin.
-    const auto slot_of = [&](int32_t share) {
-        return (((int64_t)share * 2 + (share == share0)) * heads + head) * x.plan.rows + r;
-    };
-    const auto state_of = [&](int32_t share) {
-        const bool made = share <= share1 && first_of(x, all, share) < first_of(x, all, share + 1);
-        return made ? x.state[slot_of(share)] : make_float2(kNothing, 0.0f);
-    };
-    float2 state = state_of(share0 + lane);
-    float top = state.x;
-    for (int32_t s = share0 + 64; s <= share1; s += 64) top = fmaxf(top, state_of(s + lane).x);
-#pragma unroll
-    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-    const int dim = x.a.v_dim;
-    float sum = 0.0f, y[8] = {};
-    for (int32_t s = share0; s <= share1; s += 64) {
-        if (s > share0) state = state_of(s + lane);
-        const float by = exp2_of(state.x - settled(top));
-        sum += state.y * by;
-        uint64_t left = __ballot(by != 0.0f);
-        while (left) {
-            // four parts at a time are on their way
-            constexpr int kAhead = 4;
-            float in[kAhead][8], weight[kAhead];
-            int count = 0;
+    const int32_t share0 = (int32_t)(block / heads);
+    const int head = (int)(block - share0 * heads);
+    const int4 begun = x.begun[share0];
+    const int32_t share1 = uniform(begun.x);
+    if (share1 < 0) return;
+    const int64_t row0 = (int64_t)uniform(begun.w) * x.plan.rows;
+    const int rows = (int)min((int64_t)uniform(begun.z) * x.group - row0, (int64_t)x.plan.rows);
+    const int32_t count = share1 - share0 + 1;
+    const int dim = x.a.v_dim, pitch = x.pitch, at = lane % LANES * 4, mine = lane / LANES;
+    for (int r = blockIdx.y * 4 + wave; r < rows; r += gridDim.y * 4) {
+        // the first share holds the tile's begin
+        const auto slot_of = [&](int32_t p) {
+            return (((int64_t)(share0 + p) * 2 + (p == 0)) * heads + head) * x.plan.rows + r;
+        };
+        const auto state_of = [&](int32_t p) {
+            return p < count ? x.state[slot_of(p)] : make_float2(kNothing, 0.0f);
+        };
+        float2 state = state_of(lane);
+        f4 in[kAhead][C];
+        const auto fetch_parts = [&](int32_t p0) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const int l = left ? __ffsll((unsigned long long)left) - 1 : 0;
-                weight[k] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, by), l));
-                if (!left) break;
-                left &= left - 1;
-                ++count;
-                const float *from = x.partial + slot_of(s + l) * dim;
+                const float *from = x.partial + slot_of(min(p0 + k * kParts + mine, count - 1)) * pitch;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j * 64 + lane < dim) in[k][j] = from[j * 64 + lane];
+                for (int j = 0; j < C; ++j)
+                    in[k][j] = *reinterpret_cast<const f4 *>(from + min(at + j * LANES * 4, pitch - 4));
             }
+        };
+        // the first parts are fetched before their weights are known
+        fetch_parts(0);
+        float top = state.x;
+        for (int32_t p = 64; p < count; p += 64) top = fmaxf(top, state_of(p + lane).x);
+        top = max_over_32(max_over_16(top));
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (k < count)
+        for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        float sum = 0.0f;
+        f4 y[C];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j * 64 + lane < dim) y[j] += weight[k] * in[k][j];
+        for (int j = 0; j < C; ++j) y[j] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int32_t p0 = 0; p0 < count; p0 += 64) {
+            if (p0) state = state_of(p0 + lane);
+            const float by = exp2_of(state.x - settled(top));
+            sum += state.y * by;
+            for (int32_t p = p0; p < min(p0 + 64, count); p += kAhead * kParts) {
+                f4 now[kAhead][C];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+                    for (int j = 0; j < C; ++j) now[k][j] = in[k][j];
+                if (p + kAhead * kParts < count) fetch_parts(p + kAhead * kParts);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int part = p + k * kParts + mine;
+                    const float weight = __shfl(by, (part - p0) & 63, 64);
+                    if (part < count)
+#pragma unroll
+                        for (int j = 0; j < C; ++j) y[j] += weight * now[k][j];
+                }
+            }
+        }
+        sum = wave_sum(sum);
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int d = LANES; d < 64; d <<= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[j][i] += __shfl_xor(y[j][i], d, 64);
+        const int32_t token = (int32_t)quotient(x.by_group, (uint32_t)(row0 + r));
+        T *out = static_cast<T *>(x.a.out) + (begun.y + (int64_t)token) * x.a.out_token +
+                 ((int64_t)head * x.group + (row0 + r - (int64_t)token * x.group)) * x.a.out_head;
+        if (mine) continue;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int to = at + j * LANES * 4;
+            const f4 z = sum == 0.0f ? f4{0.0f, 0.0f, 0.0f, 0.0f} : y[j] / sum;
+            if (to + 4 <= dim) {
+                Floats<4> w = z;
+                store<T, 4, false>(out + to, narrow<T, 4>(w));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (to + i < dim) out[to + i] = (T)z[i];
+            }
         }
     }
-    sum = wave_sum(sum);
-    const int32_t token = (int32_t)quotient(x.by_group, (uint32_t)row);
-    T *out = static_cast<T *>(x.a.out) + (tile.q.first + (int64_t)token) * x.a.out_token +
-             ((int64_t)head * x.group + (row - (int64_t)token * x.group)) * x.a.out_head;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j * 64 + lane < dim) out[j * 64 + lane] = (T)(sum == 0.0f ? 0.0f : y[j] / sum);
 }
 
 template <typename T, typename E, int DP, int KB, bool AHEAD>
@@ -563,11 +589,22 @@ template <typename T> int few_by_cache(const AttendArgs &x, hipStream_t s) {
     return x.k.type == BMMC_E4M3 ? few_by_size<T, uint8_t>(x, s) : few_by_size<T, T>(x, s);
 }
 
-template <typename T> int join(const AttendArgs &x, hipStream_t s) {
-    const uint32_t groups = (uint32_t)x.plan.rows / 4;
-    return in_launches(x.plan.tiles * x.a.heads, 256 * groups, [&](uint32_t nb, int64_t b0) {
-        hipLaunchKernelGGL(bmmc_attend_join_kernel<T>, dim3(nb, groups), dim3(256), 0, s, x, b0);
+template <typename T, int LANES, int C> int join(const AttendArgs &x, hipStream_t s) {
+    // a wave for each row that a tile has on average; 4096 workgroups that find
+    // nothing to do take 4 us
+    const int64_t filled = std::max<int64_t>(std::min(x.a.batch, x.a.tokens), 1);
+    const int64_t rows = std::min<int64_t>((x.a.tokens * x.group + filled - 1) / filled, x.plan.rows);
+    const int64_t blocks = x.plan.shares * x.a.heads;
+    const uint32_t groups = (uint32_t)std::max<int64_t>(std::min((rows + 3) / 4, 4096 / blocks), 1);
+    return in_launches(blocks, 256 * groups, [&](uint32_t nb, int64_t b0) {
+        hipLaunchKernelGGL((bmmc_attend_join_kernel<T, LANES, C>), dim3(nb, groups), dim3(256), 0, s, x, b0);
     });
+}
+
+template <typename T> int join_by_size(const AttendArgs &x, hipStream_t s) {
+    if (x.pitch <= 64) return join<T, 16, 1>(x, s);
+    if (x.pitch <= 128) return join<T, 32, 1>(x, s);
+    return x.pitch <= 256 ? join<T, 64, 1>(x, s) : join<T, 64, 2>(x, s);
 }
 
 }  // namespace
@@ -582,9 +619,9 @@ int launch_attend_few(const AttendArgs &x, hipStream_t s) {
 
 int launch_attend_join(const AttendArgs &x, hipStream_t s) {
     switch (x.a.type) {
-    case BMMC_F32: return join<float>(x, s);
-    case BMMC_F16: return join<f16_t>(x, s);
-    default: return join<bf16_t>(x, s);
+    case BMMC_F32: return join_by_size<float>(x, s);
+    case BMMC_F16: return join_by_size<f16_t>(x, s);
+    default: return join_by_size<bf16_t>(x, s);
     }
 }
 

@@ -111,17 +111,17 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
     }
     const int64_t number = block / heads;
     const int head = (int)(block - number * heads);
+    Share share{};
     Tile tile;
     int64_t unit, stop;  // of all: this workgroup's
     if (x.plan.shares) {
-        const int64_t all = all_units(x);
-        unit = first_of(x, all, number);
-        stop = first_of(x, all, number + 1);
-        if (unit >= stop) return;
-        tile = find_tile<false>(x, unit);
+        share = find_share(x, (int32_t)number);
+        unit = share.from;
+        stop = share.to;
+        tile = share.tile;
     } else {
         // a sequence's last tiles see most: they come first
-        tile = find_tile<true>(x, x.plan.tiles - 1 - number);
+        tile = uniform(find_tile(x, x.plan.tiles - 1 - number));
         unit = tile.first;
         stop = tile.first + tile.units;
     }
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                 ((number * 2 + (unit0 == 0)) * heads + head) * kManyRows + wave * 32 + n;
             if (!whole && half == 0) x.state[slot] = make_float2(m, l);
             T *out = static_cast<T *>(x.a.out) + q_row * x.a.out_token + q_head * x.a.out_head;
-            float *part = x.partial + slot * x.a.v_dim;
+            float *part = x.partial + slot * x.pitch;
             const int dim = kept(x.a.v_dim), from = kept_lane(4 * half);
 #pragma unroll
             for (int d = 0; d < DB; ++d)
@@ -463,14 +463,14 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                                 if (at + j < dim) out[at + j] = (T)y[j];
                         }
                     } else {
-                        for (int j = 0; j < 4; ++j)
-                            if (at + j < dim) part[at + j] = y[j] * by_value;
+                        if (at < dim) *reinterpret_cast<f4 *>(part + at) = y * by_value;
                     }
                 }
         }
         unit = tile.first + unit1;
         if (unit < stop) next_tile(x, tile);
     }
+    if (x.plan.shares && head == 0) leave_begun(x, (int32_t)number, share, tile);
 }
 
 template <typename T, typename E, int DP, bool DIRECT> int many(const AttendArgs &x, hipStream_t s) {

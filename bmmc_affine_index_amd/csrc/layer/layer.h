@@ -31,14 +31,17 @@ struct AttendArgs {
     bmmc_attention a;
     bmmc_scaled_cache k, v;
     AttendPlan plan;
-    FastDiv by_group, by_page;
+    FastDiv by_group, by_page, by_shares;
     int32_t group;
     int32_t rows_scaled;  // scales by place, not by head alone
+    int32_t few_units;    // their number is below 2^31
     int64_t reach;        // places the table has
+    int32_t pitch;        // v_dim in whole vectors of 4
     // Of each share: a tile's end that it begins with, and one's begin that it ends
-    // with; [shares, 2, heads, rows, v_dim] and [shares, 2, heads, rows]
+    // with; [shares, 2, heads, rows, pitch] and [shares, 2, heads, rows]
     float *partial;
     float2 *state;  // maximum and sum
+    int4 *begun;    // shares: the tile that each begins and does not end
 };
 
 constexpr int kClearBlocks = 32;  // workgroups that clear rows of no sequence

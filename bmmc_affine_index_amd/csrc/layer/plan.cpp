@@ -18,7 +18,7 @@ AttendPlan attend_plan(const bmmc_attention &a) {
     const bool wide = a.type == BMMC_F32;
     const int dim = std::max(a.k_dim, a.v_dim);
     AttendPlan p{};
-    const bool many = !wide && dim <= 256 && a.tokens * group > 32 * filled;
+    const bool many = !wide && dim <= 256 && a.tokens * group > 48 * filled;
     p.rows = many ? 128 : 16;
     // four waves, of 16 keys each where long rows of 32 bits leave no registers for 32
     p.unit = many || (wide && dim > 64) ? 64 : 128;
