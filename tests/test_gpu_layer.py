@@ -386,6 +386,78 @@ def test_the_results_are_the_same_each_time():
         assert all(torch.equal(first, bm.cache_attention(*args, **named)) for _ in range(3))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("new", [3, 130])
+def test_scales_of_values_in_the_hundreds(new, dtype):
+    """A weight times its value's scale fits the type while scores rise along the keys."""
+    c = Case([new], [400], 16, 4, 1, 64, 64, dtype, "row")
+    c.v = (c.v.float() / 64).to(F8)
+    c.scales = c.scales[0], 400.0 + 2000 * (c.scales[1] - 0.01)
+    at = torch.arange(400)
+    rise = torch.zeros_like(c.scales[0])
+    rise[c.table[0, at // 16].long(), at % 16] = (at / 400.0)[:, None]
+    c.scales = c.scales[0] * rise, c.scales[1]
+    assert 450 < float(c.scales[1].max()) < 500
+    got = c.check()
+    assert bool(got.isfinite().all())
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_more_sequences_than_lanes(tokens):
+    """150 sequences, some of them empty, without new tokens or shorter than their new tokens."""
+    g = _gen(11)
+    lengths = (torch.rand(150, generator=g) ** 4 * 700).long().tolist()
+    new = [0 if i % 13 == 5 else min(tokens, i + 1) for i in range(150)]
+    Case(new, lengths, 16, 4, 2, 64, 64, torch.bfloat16).check()
+    Case(new[:70], lengths[:70], 16, 4, 2, 64, 64, torch.float32).check()
+
+
+def test_tables_of_more_places_than_31_bits_count():
+    """A wide table of few pages in use: the number of parts that it could make needs 64 bits."""
+    page, width, batch = 1 << 16, 1 << 15, 300
+    c = Case([1] * batch, [5 + i % 7 for i in range(batch)], 16, 2, 1, 64, 64, torch.bfloat16)
+    (q, k, v, table, _), named = c.args()
+    lengths = torch.tensor([5 + i % 2 for i in range(batch)], dtype=torch.int32, device=DEV)
+    two = torch.arange(batch, device=DEV) % 2
+    wide = torch.full((batch, width), -1, dtype=torch.int32, device=DEV)
+    wide[:, 0] = two
+    pools = []
+    for x in (k, v):
+        pools.append(torch.zeros(2, page, 1, 64, dtype=torch.bfloat16, device=DEV))
+        pools[-1][:, :16] = x[table[:2, 0].long()]
+    table[:, 0] = table[two, 0]
+    want = bm.cache_attention(q, k, v, table, lengths, **named)
+    got = bm.cache_attention(q, *pools, wide, lengths, **named)
+    assert torch.equal(got, want) and bool(got.isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("case", [
+    ([1, 2], [500, 90], 16, 64, 1, 64, 64, 0), ([40], [170], 16, 4, 1, 36, 44, 0),
+    ([90, 2], [500, 3], 16, 4, 2, 100, 84, 77), ([80], [400], 128, 6, 2, 200, 256, 0),
+    ([65, 65], [65, 1000], 1, 2, 2, 8, 17, 0), ([5], [5], 16, 3, 1, 128, 128, 2)], ids=str)
+def test_attention_of_other_shapes(case, dtype):
+    """Rows of no multiple of 16 bytes in tiles of many rows, groups past a tile, pages of one place."""
+    new, lengths, page, q_heads, heads, dim, v_dim, window = case
+    for narrow in ("no", "row"):
+        Case(new, lengths, page, q_heads, heads, dim, v_dim, dtype, narrow, window=window, before=2,
+             behind=3).check()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with a workspace of its own."""
+    cases = [Case([1] * 6, [1, 900, 33, 2000, 5, 64], 16, 8, 2, 128, 128, torch.bfloat16),
+             Case([50, 3], [700, 64], 16, 8, 2, 128, 128, torch.bfloat16, seed=1)]
+    work = [c.args() for c in cases]
+    want = [bm.cache_attention(*a, **named) for a, named in work]
+    streams = [torch.cuda.Stream() for _ in work]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [bm.cache_attention(*a, **named, stream=s) for (a, named), s in zip(work, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 # --------------------------------------------------------------------------
 # The cache in 8 bits
 # --------------------------------------------------------------------------
