@@ -293,7 +293,7 @@ int64_t bmmc_expert_balance_workspace(int64_t tokens, int num_experts) {
     if (tokens < 0 || tokens > kMaxIndex || num_experts < 1 || num_experts > BMMC_MAX_EXPERTS)
         return -1;
     // sums and counts of each workgroup, then how many have ended and their losses
-    const int64_t ends = 1 + (num_experts + 63) / 64;
+    const int64_t ends = 1 + (num_experts + kBalanceColumns - 1) / kBalanceColumns;
     return ((int64_t)balance_blocks(tokens, num_experts) * (2 * (int64_t)num_experts + 1) + ends) * 4;
 }
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "../tokens/device.h"
+#include "lanes.h"
 #include "layer.h"
 
 namespace bmmc {
@@ -467,18 +468,6 @@ __device__ __forceinline__ int32_t entry_of(const AttendArgs &x, const int32_t *
 __device__ __forceinline__ int32_t page_of(const AttendArgs &x, int32_t entry, int32_t place,
                                            int32_t end) {
     return place < end && entry >= 0 && entry < x.a.pages ? entry : -1;
-}
-
-// The largest of a lane's number and those of the lanes 16 (32) away.
-__device__ __forceinline__ float max_over_16(float v) {
-    const uint32_t w = __builtin_bit_cast(uint32_t, v);
-    const auto both = __builtin_amdgcn_permlane16_swap(w, w, false, false);
-    return fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
-}
-__device__ __forceinline__ float max_over_32(float v) {
-    const uint32_t w = __builtin_bit_cast(uint32_t, v);
-    const auto both = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-    return fmaxf(__builtin_bit_cast(float, (uint32_t)both[0]), __builtin_bit_cast(float, (uint32_t)both[1]));
 }
 
 }  // namespace dev

@@ -121,29 +121,6 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
         const bool on = row < (int64_t)tile.q.count * x.group;
         const int32_t token = (int32_t)quotient(x.by_group, (uint32_t)row);
         const int32_t place = tile.q.length - tile.q.count + token;
-        vec_t q[F::kQueriesInLds ? 1 : NK];
-        {
-            const int64_t h = (int64_t)head * x.group + (row - (int64_t)token * x.group);
-            const uint8_t *in = reinterpret_cast<const uint8_t *>(kZeros);
-            if (on)
-                in = reinterpret_cast<const uint8_t *>(
-                    static_cast<const T *>(x.a.q) +
-                    (tile.q.first + (int64_t)token) * x.a.q_token + h * x.a.q_head);
-            const int dim = kept(x.a.k_dim);
-#pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                if (F::kQueriesInLds && (k & (kFewWaves - 1)) != wave) continue;
-                Raw<T, CE> r = fetch<T, CE>(in, (k * 4 + g) * CE, dim);
-                if (dim & (CE - 1)) settle(r, (k * 4 + g) * CE, dim);
-                if constexpr (F::kQueriesInLds)
-                    *reinterpret_cast<u4 *>(&main_lds.q[(k * 64 + lane) * 4]) =
-                        u4{r.w[0], r.w[1], r.w[2], r.w[3]};
-                else
-                    q[k] = product_vec<T>(r);
-            }
-            if constexpr (F::kQueriesInLds) __syncthreads();
-        }
-
         // lanes 0 to 31 look after the keys, 32 to 63 after the values of a tile
         const int kl = lane & 31, half = lane >> 5;
         const uint8_t *base = static_cast<const uint8_t *>(half ? x.v.data : x.k.data);
@@ -216,12 +193,35 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
         const int32_t step = kFewWaves * KT;
         int32_t t = span.from + wave * KT;
         int which = 0;
+        const int32_t first = t < span.to ? look(t) : -1;  // on its way while the queries are
+        vec_t q[F::kQueriesInLds ? 1 : NK];
+        {
+            const int64_t h = (int64_t)head * x.group + (row - (int64_t)token * x.group);
+            const uint8_t *in = reinterpret_cast<const uint8_t *>(kZeros);
+            if (on)
+                in = reinterpret_cast<const uint8_t *>(
+                    static_cast<const T *>(x.a.q) +
+                    (tile.q.first + (int64_t)token) * x.a.q_token + h * x.a.q_head);
+            const int dim = kept(x.a.k_dim);
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+                if (F::kQueriesInLds && (k & (kFewWaves - 1)) != wave) continue;
+                Raw<T, CE> r = fetch<T, CE>(in, (k * 4 + g) * CE, dim);
+                if (dim & (CE - 1)) settle(r, (k * 4 + g) * CE, dim);
+                if constexpr (F::kQueriesInLds)
+                    *reinterpret_cast<u4 *>(&main_lds.q[(k * 64 + lane) * 4]) =
+                        u4{r.w[0], r.w[1], r.w[2], r.w[3]};
+                else
+                    q[k] = product_vec<T>(r);
+            }
+            if constexpr (F::kQueriesInLds) __syncthreads();
+        }
         // What is on its way, in this order: the table's entries for the tile after the
         // next, the next tile's keys, its values.  A wait for the first leaves the others.
         int32_t entry = -1;
         uint32_t seen = 0;
         if (t < span.to) {
-            seen = put(look(t), t, 0);
+            seen = put(first, t, 0);
             entry = look(t + step);
             __builtin_amdgcn_sched_barrier(0);
             if (AHEAD) load_all_keys(0);
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
             for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, s[b][i]);
-            top = max_over_32(max_over_16(top));
+            top = over_32(over_16(top, Largest()), Largest());
             const float m_new = fmaxf(m, top);
             if (__any(m_new != m)) {
                 const float down = exp2_of(m - settled(m_new));
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(256) bmmc_attend_join_kernel(const AttendArgs 
         fetch_parts(0);
         float top = state.x;
         for (int32_t p = 64; p < count; p += 64) top = fmaxf(top, state_of(p + lane).x);
-        top = max_over_32(max_over_16(top));
+        top = over_32(over_16(top, Largest()), Largest());
 #pragma unroll
         for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
         float sum = 0.0f;

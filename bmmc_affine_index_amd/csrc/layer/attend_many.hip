@@ -340,10 +340,12 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-                top = max_over_32(top) * c;
+                top = over_32(top, Largest()) * c;
                 // Weights may grow to 2^8 before the sums are brought down to a new
-                // maximum, which both types hold
-                if (__any(top > m + 8.0f)) {
+                // maximum, which both types hold; not where 16 bits of 5 exponent bits
+                // hold a weight times its value's scale, so that scales up to 500 fit
+                const float room = scaled && __is_same(T, f16_t) ? 0.0f : 8.0f;
+                if (__any(top > m + room)) {
                     const float m_new = fmaxf(m, top);
                     const float down = exp2_of(m - settled(m_new));
                     l *= down;

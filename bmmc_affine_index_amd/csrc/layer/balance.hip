@@ -13,16 +13,17 @@
 #include <algorithm>
 
 #include "../tokens/device.h"
+#include "lanes.h"
 #include "layer.h"
 
 namespace bmmc {
 
 namespace {
 
-constexpr int kBalanceThreads = 512;
-constexpr int kBalanceWaves = kBalanceThreads / 64;
+// Waves of a workgroup that sums rows: as many as have registers for a lane's vectors.
+template <typename T, int C> constexpr int kBalanceWaves = C * dev::Lanes<T>::N > 16 ? 8 : 16;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kColumns = 64;  // experts of a workgroup that sums
+constexpr int kColumns = kBalanceColumns;
 
 // C vectors of a row in each of 1 << shift lanes; past its end what weighs nothing.
 template <typename T, int C>
@@ -42,15 +43,6 @@ __device__ __forceinline__ void load_row(const T *row, int lane, int shift, int 
     }
 }
 
-__device__ __forceinline__ float over_lanes_max(float v, int shift) {
-    for (int d = 1; d < 1 << shift; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-    return v;
-}
-__device__ __forceinline__ float over_lanes_sum(float v, int shift) {
-    for (int d = 1; d < 1 << shift; d <<= 1) v += __shfl_xor(v, d, 64);
-    return v;
-}
-
 // p = softmax of a row.  A maximum that is no number leaves NaN in all of it.
 template <typename T, int C>
 __device__ __forceinline__ void softmax_row(const dev::Vec<T, dev::Lanes<T>::N> (&raw)[C], int shift,
@@ -66,27 +58,43 @@ __device__ __forceinline__ void softmax_row(const dev::Vec<T, dev::Lanes<T>::N> 
             top = fmaxf(top, x[i]);
         }
     }
-    top = over_lanes_max(top, shift);
+    top = dev::over_lanes(top, shift, dev::Largest());
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < C * N; ++i) {
         p[i] = __builtin_amdgcn_exp2f((p[i] - top) * kLog2e);
         sum += p[i];
     }
-    sum = over_lanes_sum(sum, shift);
+    sum = dev::over_lanes(sum, shift, dev::Sum());
     const float by = 1.0f / sum;
 #pragma unroll
     for (int i = 0; i < C * N; ++i) p[i] *= by;
 }
 
 template <typename T, int C>
-__global__ void __launch_bounds__(kBalanceThreads)
+__global__ void __launch_bounds__((64 * kBalanceWaves<T, C>))
     bmmc_balance_rows_kernel(const BalanceArgs a, int shift) {
-    constexpr int N = dev::Lanes<T>::N;
-    extern __shared__ float part[];  // kBalanceWaves, num_experts; first the counts
+    constexpr int N = dev::Lanes<T>::N, WAVES = kBalanceWaves<T, C>;
+    extern __shared__ float part[];  // WAVES, num_experts; first the counts
     int32_t *hits = reinterpret_cast<int32_t *>(part);
     const int E = a.num_experts, tid = threadIdx.x;
     const int64_t from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.tokens);
+    const int lane = tid & 63, in_row = lane & ((1 << shift) - 1), wave = tid >> 6;
+    const int rows = 64 >> shift;
+    float sums[C * N] = {};
+    dev::Vec<T, N> next[C];
+    const int64_t step = (int64_t)rows * WAVES;
+    const T *logits = static_cast<const T *>(a.logits);
+    bool on = false;
+    // a row that is not counted is read all the same, not to wait for its mask first
+    const auto fetch = [&](int64_t t) {
+        on = t < to;
+        if (!on) return;
+        if (a.mask) on = a.mask[t] != 0;
+        load_row<T, C>(logits + t * a.stride, in_row, shift, E, next);
+    };
+    int64_t t = from + (int64_t)wave * rows + (lane >> shift);
+    fetch(t);  // on its way while the choices are counted
     for (int e = tid; e <= E; e += blockDim.x) hits[e] = 0;
     if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<uint32_t *>(a.hits + (int64_t)a.blocks * (E + 1)) = 0;
     __syncthreads();
@@ -104,28 +112,14 @@ __global__ void __launch_bounds__(kBalanceThreads)
     for (int e = tid; e <= E; e += blockDim.x) hist[e] = hits[e];
     __syncthreads();
 
-    const int lane = tid & 63, in_row = lane & ((1 << shift) - 1), wave = tid >> 6;
-    const int rows = 64 >> shift;
-    float sums[C * N] = {};
-    dev::Vec<T, N> next[C];
-    const int64_t step = (int64_t)rows * kBalanceWaves;
-    const T *logits = static_cast<const T *>(a.logits);
-    const auto counted = [&](int64_t t) { return t < to && (!a.mask || a.mask[t]); };
-    int64_t t = from + (int64_t)wave * rows + (lane >> shift);
-    bool on = counted(t);
-    if (on) load_row<T, C>(logits + t * a.stride, in_row, shift, E, next);
     // every lane of a wave goes round as often as any: rows of a wave are in step
     for (int64_t t0 = from + (int64_t)wave * rows; t0 < to; t0 += step, t += step) {
         dev::Vec<T, N> raw[C];
         const bool now = on;
 #pragma unroll
         for (int c = 0; c < C; ++c) raw[c] = next[c];
-        on = counted(t + step);
-        if (on) load_row<T, C>(logits + (t + step) * a.stride, in_row, shift, E, next);
+        fetch(t + step);
         float p[C * N];
-        if (!now)
-#pragma unroll
-            for (int c = 0; c < C; ++c) raw[c] = dev::Vec<T, N>{};
         softmax_row<T, C>(raw, shift, p);
 #pragma unroll
         for (int i = 0; i < C * N; ++i) sums[i] += now ? p[i] : 0.0f;
@@ -145,58 +139,61 @@ __global__ void __launch_bounds__(kBalanceThreads)
     for (int e = tid; e < E; e += blockDim.x) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kBalanceWaves; ++w) s += part[w * E + e];
+        for (int w = 0; w < WAVES; ++w) s += part[w * E + e];
         a.sums[(int64_t)blockIdx.x * E + e] = s;
     }
 }
 
-// The workgroups' sums joined, kColumns experts a workgroup; the last one to end
-// sums the loss, in the experts' order.
+// The workgroups' sums joined, kColumns experts a workgroup, in an order that is
+// always the same; the last one to end sums the loss, in the experts' order.
 __global__ void __launch_bounds__(1024) bmmc_balance_join_kernel(const BalanceArgs a) {
-    __shared__ double sums[16][kColumns];
-    __shared__ int32_t hits[16][kColumns];
-    __shared__ int32_t tokens, last;
-    const int E = a.num_experts, col = threadIdx.x & 63, row = threadIdx.x >> 6;
+    constexpr int R = 1024 / kColumns;  // threads of an expert
+    __shared__ double sums[R][kColumns];
+    __shared__ int32_t hits[R][kColumns];
+    __shared__ int32_t tokens;
+    const int E = a.num_experts, col = threadIdx.x % kColumns, row = threadIdx.x / kColumns;
     const int e = blockIdx.x * kColumns + col;
     if (threadIdx.x == 0) tokens = 0;
     __syncthreads();
     int32_t n = 0;
     for (int b = threadIdx.x; b < a.blocks; b += blockDim.x) n += a.hits[(int64_t)b * (E + 1) + E];
-    if (n) atomicAdd(&tokens, n);
     double s = 0.0;
     int32_t h = 0;
     if (e < E)
-        for (int b = row; b < a.blocks; b += 16) {
+#pragma unroll 4
+        for (int b = row; b < a.blocks; b += R) {
             s += (double)a.sums[(int64_t)b * E + e];
             h += a.hits[(int64_t)b * (E + 1) + e];
         }
+    if (n) atomicAdd(&tokens, n);
     sums[row][col] = s;
     hits[row][col] = h;
-    __syncthreads();
+    for (int half = R / 2; half; half >>= 1) {
+        __syncthreads();
+        if (row < half) {
+            sums[row][col] += sums[row + half][col];
+            hits[row][col] += hits[row + half][col];
+        }
+    }
     uint32_t *done = reinterpret_cast<uint32_t *>(a.hits + (int64_t)a.blocks * (E + 1));
     float *losses = reinterpret_cast<float *>(done + 1);
     if (row == 0) {
-        for (int r = 1; r < 16; ++r) {
-            s += sums[r][col];
-            h += hits[r][col];
-        }
         double term = 0.0;
         if (e < E) {
             const double counted = (double)tokens;
             const float slope =
-                tokens ? (float)((double)h * E / (counted * counted * a.choices)) : 0.0f;
-            a.counts[e] = h;
+                tokens ? (float)((double)hits[0][col] * E / (counted * counted * a.choices)) : 0.0f;
+            a.counts[e] = hits[0][col];
             a.slopes[e] = slope;
-            term = (double)slope * s;
+            term = (double)slope * sums[0][col];
         }
 #pragma unroll
-        for (int d = 32; d; d >>= 1) term += __shfl_xor(term, d, 64);
+        for (int d = kColumns / 2; d; d >>= 1) term += __shfl_xor(term, d, kColumns);
         if (col == 0) {
             __hip_atomic_store(&losses[blockIdx.x], (float)term, __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);
-            last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-                   gridDim.x - 1;
-            if (last) {
+            if (__hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                gridDim.x - 1) {
                 double all = 0.0;
                 for (uint32_t b = 0; b < gridDim.x; ++b)
                     all += (double)__hip_atomic_load(&losses[b], __ATOMIC_RELAXED,
@@ -225,26 +222,28 @@ __global__ void __launch_bounds__(256) bmmc_balance_backward_kernel(const Balanc
     const float g = *a.grad;
     const T *logits = static_cast<const T *>(a.logits);
     dev::Vec<T, N> next[C];
-    const auto counted = [&](int64_t t) { return t < a.tokens && (!a.mask || a.mask[t]); };
+    bool on = false;
+    const auto fetch = [&](int64_t t) {
+        on = t < a.tokens;
+        if (!on) return;
+        if (a.mask) on = a.mask[t] != 0;
+        load_row<T, C>(logits + t * a.stride, in_row, shift, E, next);
+    };
     int64_t t = first + (lane >> shift);
-    bool on = counted(t);
-    if (on) load_row<T, C>(logits + t * a.stride, in_row, shift, E, next);
+    fetch(t);
     for (int64_t k = 0; k < a.chunk && first + k * rows < a.tokens; ++k, t += rows) {
         dev::Vec<T, N> raw[C];
         const bool now = on;
 #pragma unroll
         for (int c = 0; c < C; ++c) raw[c] = next[c];
-        on = k + 1 < a.chunk && counted(t + rows);
-        if (on) load_row<T, C>(logits + (t + rows) * a.stride, in_row, shift, E, next);
-        if (!now)
-#pragma unroll
-            for (int c = 0; c < C; ++c) raw[c] = dev::Vec<T, N>{};
+        on = false;
+        if (k + 1 < a.chunk) fetch(t + rows);
         float p[C * N];
         softmax_row<T, C>(raw, shift, p);
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < C * N; ++i) dot += slope[i] * p[i];
-        dot = over_lanes_sum(dot, shift);
+        dot = dev::over_lanes(dot, shift, dev::Sum());
         if (t >= a.tokens) continue;
         T *out = static_cast<T *>(a.grad_logits) + t * a.grad_stride;
 #pragma unroll
@@ -266,7 +265,8 @@ __global__ void __launch_bounds__(256) bmmc_balance_backward_kernel(const Balanc
     }
 }
 
-// Lanes and vectors a lane of a row.
+// Lanes and vectors a lane of a row: 16 lanes, which exchange at the least cost and
+// leave a wave several rows to work on, and more of them beyond four vectors each.
 struct Cut {
     int shift, vectors;
 };
@@ -274,7 +274,9 @@ template <typename T> Cut cut_of(int experts) {
     constexpr int N = dev::Lanes<T>::N;
     const int all = (experts + N - 1) / N;
     Cut c{0, 1};
-    while (c.shift < 6 && 1 << c.shift < all) ++c.shift;
+    while (c.shift < 4 && 1 << c.shift < all) ++c.shift;
+    while (c.vectors < 4 && c.vectors << c.shift < all) c.vectors *= 2;
+    while (c.shift < 6 && c.vectors << c.shift < all) ++c.shift;
     while (c.vectors << c.shift < all) c.vectors *= 2;
     return c;
 }
@@ -282,9 +284,10 @@ template <typename T> Cut cut_of(int experts) {
 template <typename T, int C> int forward(const BalanceArgs &x, int shift, hipStream_t s) {
     BalanceArgs a = x;
     a.chunk = (a.tokens + a.blocks - 1) / a.blocks;
-    const size_t lds = std::max((size_t)kBalanceWaves * a.num_experts, (size_t)a.num_experts + 1) * 4;
-    hipLaunchKernelGGL((bmmc_balance_rows_kernel<T, C>), dim3(a.blocks), dim3(kBalanceThreads), lds, s,
-                       a, shift);
+    const int waves = kBalanceWaves<T, C>;
+    const size_t lds = std::max((size_t)waves * a.num_experts, (size_t)a.num_experts + 1) * 4;
+    hipLaunchKernelGGL((bmmc_balance_rows_kernel<T, C>), dim3(a.blocks), dim3(64 * waves), lds, s, a,
+                       shift);
     hipLaunchKernelGGL(bmmc_balance_join_kernel, dim3((a.num_experts + kColumns - 1) / kColumns),
                        dim3(1024), 0, s, a);
     return hipGetLastError() == hipSuccess ? BMMC_OK : BMMC_ERR_HIP;

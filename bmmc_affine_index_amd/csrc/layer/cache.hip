@@ -10,6 +10,7 @@
 // Bound by memory: each element is read once and written once, in 1 byte.
 // Turns are made once a token, in LDS, as for rotary positions.
 #include "../tokens/turns.h"
+#include "lanes.h"
 #include "layer.h"
 
 namespace bmmc {
@@ -22,13 +23,13 @@ constexpr int kPer = 8;  // elements of a row in a lane
 struct RowCut {
     int32_t shift;  // log2 of lanes
     __device__ int row() const { return (threadIdx.x & 63) >> shift; }
-    __device__ int at() const { return (threadIdx.x & ((1 << shift) - 1)) * kPer; }
+    __device__ int lane() const { return threadIdx.x & ((1 << shift) - 1); }
     __host__ __device__ int rows_a_wave() const { return 64 >> shift; }
 };
 
-RowCut row_cut(int dim) {
+RowCut row_cut(int dim, int each) {
     RowCut c{0};
-    while (kPer << c.shift < dim) ++c.shift;
+    while (each << c.shift < dim) ++c.shift;
     return c;
 }
 
@@ -82,43 +83,39 @@ struct Quantize {
     int32_t q_tasks, k_tasks;  // waves' tasks a token for q and for k
 };
 
-// Elements at .. at + 7 of a row of `dim`, turned.  The row's other lanes hold the
-// rest of it; where pairs are not whole vectors, a pair's other half is read
-// from the row.
+// value / scale in 8 bits, clamped, NaN kept, rounded to nearest, ties to even.  The
+// quotient is the product with by = 1 / scale, put right by what it leaves of x.
+__device__ __forceinline__ float quotient_of(float x, float scale, float by) {
+    constexpr float kMax = 448.0f;
+    // an infinity's product leaves infinity again, not the difference of two
+    const float q = __builtin_amdgcn_fmed3f(x * by, -2.0f * kMax, 2.0f * kMax);
+    const float y = fmaf(fmaf(-q, scale, x), by, q);
+    return y > kMax ? kMax : y < -kMax ? -kMax : y;
+}
+
+// A part of a row: its elements, in 32 bits, and where in the row they are.
+struct Part {
+    float x[kPer];
+    int at;
+};
+
+// Turned elements of a part whose pairs are its neighbours, or whose other halves are
+// read from the row.
 template <typename T, bool PAIRED>
-__device__ __forceinline__ void turn_part(const dev::Vec<T, kPer> &raw, const T *row, bool on, int at,
-                                          int pairs, const float2 *cs, float (&x)[kPer]) {
-    if constexpr (PAIRED) {
+__device__ __forceinline__ void turn_part(Part &p, const T *row, bool on, int pairs, const float2 *cs) {
 #pragma unroll
-        for (int i = 0; i < kPer; i += 2) {
-            if (at + i >= 2 * pairs) continue;
-            const float2 u = cs[(at + i) / 2];
-            const float a = x[i], b = x[i + 1];
-            x[i] = a * u.x - b * u.y;
-            x[i + 1] = b * u.x + a * u.y;
-        }
-    } else {
-        float other[kPer];
-        if ((pairs & (kPer - 1)) == 0) {
-            const int lanes = pairs / kPer;
-            const int from = ((int)threadIdx.x & 63) + (at < pairs ? lanes : -lanes);
-            const float w[kPer] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
-            // lanes past the pairs take what they get and do not use it
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) other[i] = __shfl(w[i], from & 63, 64);
+    for (int i = 0; i < kPer; i += PAIRED ? 2 : 1) {
+        const int e = p.at + i;
+        if (e >= 2 * pairs) continue;
+        if constexpr (PAIRED) {
+            const float2 u = cs[e / 2];
+            const float a = p.x[i], b = p.x[i + 1];
+            p.x[i] = a * u.x - b * u.y;
+            p.x[i + 1] = b * u.x + a * u.y;
         } else {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int e = at + i;
-                other[i] = on && e < 2 * pairs ? (float)row[e < pairs ? e + pairs : e - pairs] : 0.0f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = at + i;
-            if (e >= 2 * pairs) continue;
             const float2 u = cs[e < pairs ? e : e - pairs];
-            x[i] = x[i] * u.x + (e < pairs ? -other[i] : other[i]) * u.y;
+            const float other = on ? (float)row[e < pairs ? e + pairs : e - pairs] : 0.0f;
+            p.x[i] = p.x[i] * u.x + (e < pairs ? -other : other) * u.y;
         }
     }
 }
@@ -133,29 +130,37 @@ __global__ void __launch_bounds__(kTurnThreads)
     const int per = (int)a.by_tasks.d, tasks = tokens * per, waves = blockDim.x >> 6;
     const int first = (int)(blockIdx.y * waves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
     const int step = (int)gridDim.y * waves;
-    const int at = a.cut.at(), lane_row = a.cut.row(), rows = a.cut.rows_a_wave();
+    const int lane = a.cut.lane(), lane_row = a.cut.row(), rows = a.cut.rows_a_wave();
 
+    // A lane has two vectors of its row: both halves of the same pairs, where those are
+    // whole vectors, and two neighbours of the rest.
+    const int halves = !PAIRED && (r.pairs & (kPer - 1)) == 0 ? r.pairs / kPer : 0;
     struct Row {
         const T *in;
         int t, kind, head;  // kind: 0 q, 1 k, 2 v
         bool on;
+    } row{};
+    dev::Vec<T, kPer> next[2];
+    const auto at_of = [&](int kind, int half) {
+        const int turned = kind == 2 ? 0 : halves;
+        return lane < turned ? (lane + half * turned) * kPer : (2 * lane + half) * kPer;
     };
-    const auto locate = [&](int task) {
+    const auto fetch = [&](int task) {
         const int t = (int)quotient(a.by_tasks, (uint32_t)task);
         int number = task - t * per;
         const int kind = number < a.q_tasks ? 0 : number < a.q_tasks + a.k_tasks ? 1 : 2;
         number -= kind == 0 ? 0 : kind == 1 ? a.q_tasks : a.q_tasks + a.k_tasks;
         const Rows &x = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
         const int head = number * rows + lane_row;
-        return Row{static_cast<const T *>(x.in) + (token0 + t) * x.token + head * x.head, t, kind,
-                   head, head < (kind == 0 ? a.q_heads : a.heads)};
-    };
-    dev::Vec<T, kPer> next{};
-    const auto fetch = [&](int task) {
-        const Row w = locate(task);
-        const int dim = w.kind == 2 ? a.v_dim : a.k_dim;
-        next = dev::Vec<T, kPer>{};
-        if (w.on && at < dim) next = load_part<T>(w.in, at, dim);
+        row = Row{static_cast<const T *>(x.in) + (token0 + t) * x.token + head * x.head, t, kind,
+                  head, head < (kind == 0 ? a.q_heads : a.heads)};
+        const int dim = kind == 2 ? a.v_dim : a.k_dim;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = at_of(kind, h);
+            next[h] = dev::Vec<T, kPer>{};
+            if (row.on && at < dim) next[h] = load_part<T>(row.in, at, dim);
+        }
     };
     const int looker = (int)threadIdx.x - ((int)blockDim.x - 64);
     if (looker >= 0 && looker < tokens) places[looker] = page_place(a.where, token0 + looker);
@@ -164,50 +169,79 @@ __global__ void __launch_bounds__(kTurnThreads)
     });
     __syncthreads();
     for (int task = first; task < tasks; task += step) {
-        const Row w = locate(task);
-        const dev::Vec<T, kPer> raw = next;
+        const Row w = row;
+        Part p[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const dev::Floats<kPer> wide = dev::widen<T, kPer>(next[h]);
+            p[h].at = at_of(w.kind, h);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) p[h].x[i] = wide[i];
+        }
         if (task + step < tasks) fetch(task + step);
         const int dim = w.kind == 2 ? a.v_dim : a.k_dim;
-        float x[kPer];
-        const dev::Floats<kPer> wide = dev::widen<T, kPer>(raw);
+        if (w.kind != 2 && r.pairs) {
+            const float2 *turns = cs + w.t * r.pairs;
+            if (!PAIRED && halves) {
+                if (lane < halves)
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = wide[i];
-        if (w.kind != 2 && r.pairs)
-            turn_part<T, PAIRED>(raw, w.in, w.on, at, r.pairs, cs + w.t * r.pairs, x);
+                    for (int i = 0; i < kPer; ++i) {
+                        const float2 u = turns[p[0].at + i];
+                        const float x = p[0].x[i], y = p[1].x[i];
+                        p[0].x[i] = x * u.x + -y * u.y;
+                        p[1].x[i] = y * u.x + x * u.y;
+                    }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) turn_part<T, PAIRED>(p[h], w.in, w.on, r.pairs, turns);
+            }
+        }
         if (w.kind == 0) {
-            if (!w.on || at >= dim) continue;
-            dev::Floats<kPer> y;
+            if (!w.on) continue;
+            T *out = static_cast<T *>(a.q_out) + (token0 + w.t) * a.q_out_token + w.head * a.q_out_head;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) y[i] = x[i];
-            store_part<T>(static_cast<T *>(a.q_out) + (token0 + w.t) * a.q_out_token +
-                              w.head * a.q_out_head,
-                          at, dim, dev::narrow<T, kPer>(y));
+            for (int h = 0; h < 2; ++h) {
+                if (p[h].at >= dim) continue;
+                dev::Floats<kPer> y;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) y[i] = p[h].x[i];
+                store_part<T>(out, p[h].at, dim, dev::narrow<T, kPer>(y));
+            }
             continue;
         }
         float most = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float m = fabsf(x[i]);
-            if (m < __builtin_inff()) most = fmaxf(most, m);  // neither infinities nor NaN
-        }
-        for (int d = 1; d < 1 << a.cut.shift; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const float m = fabsf(p[h].x[i]);
+                if (m < __builtin_inff()) most = fmaxf(most, m);  // neither infinities nor NaN
+            }
+        most = dev::over_lanes(most, a.cut.shift, dev::Largest());
         const float scale = most == 0.0f ? 1.0f : fmaxf(most / 448.0f, 0x1p-126f);
+        const float by = 1.0f / scale;
         const PagePlace home = places[w.t];
-        if (home.page < 0 || !w.on || at >= dim) continue;
+        if (home.page < 0 || !w.on) continue;
         const Scaled &c = w.kind == 1 ? a.k_cache : a.v_cache;
         uint8_t *out = c.data + home.page * c.page + home.place * c.place + w.head * c.head;
-        if (at == 0)
+        if (lane == 0)
             c.scale[home.page * c.scale_page + home.place * c.scale_place + w.head * c.scale_head] =
                 scale;
-        if (at + kPer <= dim) {
-            dev::Floats<kPer> y;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) y[i] = x[i];
-            store_e4m3<kPer>(out + at, y, scale);
-        } else {
+        for (int h = 0; h < 2; ++h) {
+            if (p[h].at >= dim) continue;
+            uint32_t word[2];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (at + i < dim) store_e4m3<1>(out + at + i, dev::Floats<1>{x[i]}, scale);
+            for (int k = 0; k < 2; ++k) {
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = quotient_of(p[h].x[4 * k + i], scale, by);
+                const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+                word[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+            }
+            dev::Vec<uint8_t, kPer> bytes;
+            __builtin_memcpy(&bytes.v, word, kPer);
+            store_part<uint8_t>(out, p[h].at, dim, bytes);
         }
     }
 }
@@ -225,7 +259,7 @@ template <typename T, bool PAIRED> int quantize(const QuantizeArgs &h, hipStream
     a.v_cache = scaled_of(h.v_cache);
     a.where = h.where;
     a.tokens = h.tokens;
-    a.cut = row_cut(std::max(h.k_dim, h.v_dim));
+    a.cut = row_cut(std::max(h.k_dim, h.v_dim), 2 * kPer);
     a.q_heads = (int32_t)h.q.heads;
     a.heads = (int32_t)h.k.heads;
     a.k_dim = h.k_dim;
@@ -249,8 +283,14 @@ template <typename T> int quantize_t(const QuantizeArgs &h, hipStream_t s) {
 
 // ---- rows read back ------------------------------------------------------------------
 
-constexpr int kReadTokens = 8;  // of a workgroup, where there are many
-constexpr int kReadAhead = 4;   // rows a lane has on their way
+constexpr int kReadTokens = 64;  // most of a workgroup
+constexpr int kReadBlocks = 2048;
+constexpr int kReadAhead = 4;    // rows a lane has on their way
+
+// Where a token's rows and their scales begin, in elements; k is below 0 if nowhere.
+struct ReadPlace {
+    int64_t k, v, k_scale, v_scale;
+};
 
 struct Read {
     void *k_out, *v_out;
@@ -285,55 +325,60 @@ template <typename E> __device__ __forceinline__ dev::Floats<kPer> widened(const
 
 template <typename T, typename E>
 __global__ void __launch_bounds__(256) bmmc_cache_read_kernel(const Read a, int64_t block0) {
-    __shared__ PagePlace places[kReadTokens];
+    __shared__ ReadPlace places[kReadTokens];
     const int64_t token0 = (block0 + blockIdx.x) * a.tokens_a_block;
     const int tokens = (int)min((int64_t)a.tokens_a_block, a.tokens - token0);
-    if ((int)threadIdx.x < tokens) places[threadIdx.x] = page_place(a.where, token0 + threadIdx.x);
+    if ((int)threadIdx.x < tokens) {
+        const PagePlace p = page_place(a.where, token0 + threadIdx.x);
+        ReadPlace &to = places[threadIdx.x];
+        to.k = p.page < 0 ? -1 : p.page * a.k_cache.page + p.place * a.k_cache.place;
+        to.v = p.page * a.v_cache.page + p.place * a.v_cache.place;
+        to.k_scale = p.page * a.k_cache.scale_page + p.place * a.k_cache.scale_place;
+        to.v_scale = p.page * a.v_cache.scale_page + p.place * a.v_cache.scale_place;
+    }
     __syncthreads();
-    const int at = a.cut.at(), each = a.cut.rows_a_wave() * 4;  // rows of a workgroup at once
+    const int at = a.cut.lane() * kPer, each = a.cut.rows_a_wave() * 4;  // rows of a workgroup at once
     const int mine = (int)(threadIdx.x >> 6) * a.cut.rows_a_wave() + a.cut.row();
     const int rows = tokens * 2 * a.heads;
     for (int base = (int)blockIdx.y * each * kReadAhead; base < rows;
          base += (int)gridDim.y * each * kReadAhead) {
         dev::Vec<E, kPer> x[kReadAhead];
         float scale[kReadAhead];
+        T *out[kReadAhead];
+        int dim[kReadAhead];  // 0 where the lane has nothing to write
 #pragma unroll
         for (int j = 0; j < kReadAhead; ++j) {
             const int row = base + j * each + mine;
             x[j] = dev::Vec<E, kPer>{};
             scale[j] = 1.0f;
+            dim[j] = 0;
             if (row >= rows) continue;
             const int t = (int)quotient(a.by_rows, (uint32_t)row);
             int head = row - t * 2 * a.heads;
             const bool key = head < a.heads;
             head -= key ? 0 : a.heads;
-            const int dim = key ? a.k_dim : a.v_dim;
-            const PagePlace home = places[t];
-            if (home.page < 0 || at >= dim) continue;
-            const Scaled &c = key ? a.k_cache : a.v_cache;
-            x[j] = load_part<E>(reinterpret_cast<const E *>(c.data) + home.page * c.page +
-                                    home.place * c.place + head * c.head,
-                                at, dim);
+            const int size = key ? a.k_dim : a.v_dim;
+            if (at >= size) continue;
+            dim[j] = size;
+            out[j] = static_cast<T *>(key ? a.k_out : a.v_out) +
+                     (token0 + t) * (key ? a.k_token : a.v_token) + head * (key ? a.k_head : a.v_head);
+            const ReadPlace &home = places[t];
+            if (home.k < 0) continue;
+            const Scaled &k = a.k_cache, &v = a.v_cache;
+            x[j] = load_part<E>(reinterpret_cast<const E *>(key ? k.data : v.data) +
+                                    (key ? home.k : home.v) + head * (key ? k.head : v.head),
+                                at, size);
             if (sizeof(E) == 1)
-                scale[j] = c.scale[home.page * c.scale_page + home.place * c.scale_place +
-                                   head * c.scale_head];
+                scale[j] = (key ? k.scale : v.scale)[(key ? home.k_scale : home.v_scale) +
+                                                     head * (key ? k.scale_head : v.scale_head)];
         }
 #pragma unroll
         for (int j = 0; j < kReadAhead; ++j) {
-            const int row = base + j * each + mine;
-            if (row >= rows) continue;
-            const int t = (int)quotient(a.by_rows, (uint32_t)row);
-            int head = row - t * 2 * a.heads;
-            const bool key = head < a.heads;
-            head -= key ? 0 : a.heads;
-            const int dim = key ? a.k_dim : a.v_dim;
-            if (at >= dim) continue;
-            T *out = key ? static_cast<T *>(a.k_out) + (token0 + t) * a.k_token + head * a.k_head
-                         : static_cast<T *>(a.v_out) + (token0 + t) * a.v_token + head * a.v_head;
+            if (!dim[j]) continue;
             if constexpr (sizeof(E) == 1)
-                store_part<T>(out, at, dim, dev::narrow<T, kPer>(widened<E>(x[j]) * scale[j]));
+                store_part<T>(out[j], at, dim[j], dev::narrow<T, kPer>(widened<E>(x[j]) * scale[j]));
             else
-                store_part<T>(out, at, dim, x[j]);
+                store_part<T>(out[j], at, dim[j], x[j]);
         }
     }
 }
@@ -350,17 +395,18 @@ template <typename T, typename E> int read(const ReadArgs &h, hipStream_t s) {
     a.v_cache = scaled_of(h.v_cache);
     a.where = h.where;
     a.tokens = h.tokens;
-    a.cut = row_cut(std::max(h.k_dim, h.v_dim));
+    a.cut = row_cut(std::max(h.k_dim, h.v_dim), kPer);
     a.heads = (int32_t)h.k.heads;
     a.k_dim = h.k_dim;
     a.v_dim = h.v_dim;
     a.by_rows = fast_div((uint32_t)(2 * h.k.heads));
-    a.tokens_a_block = h.tokens >= 2048 * kReadTokens ? kReadTokens : 1;
+    a.tokens_a_block =
+        (int32_t)std::min<int64_t>(kReadTokens, (h.tokens + kReadBlocks - 1) / kReadBlocks);
     const int64_t blocks = (a.tokens + a.tokens_a_block - 1) / a.tokens_a_block;
     // a token's rows are shared by workgroups where there are few tokens
     const int64_t passes = (a.tokens_a_block * 2 * h.k.heads - 1) /
                                (a.cut.rows_a_wave() * 4 * kReadAhead) + 1;
-    const uint32_t shares = (uint32_t)std::max<int64_t>(1, std::min(passes, 2048 / blocks));
+    const uint32_t shares = (uint32_t)std::max<int64_t>(1, std::min(passes, kReadBlocks / blocks));
     return in_launches(blocks, 256 * shares, [&](uint32_t nb, int64_t b0) {
         hipLaunchKernelGGL((bmmc_cache_read_kernel<T, E>), dim3(nb, shares), dim3(256), 0, s, a, b0);
     });

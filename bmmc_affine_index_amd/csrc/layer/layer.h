@@ -44,6 +44,7 @@ struct AttendArgs {
     int4 *begun;    // shares: the tile that each begins and does not end
 };
 
+constexpr int kBalanceColumns = 16;  // experts of a workgroup that joins their sums
 constexpr int kClearBlocks = 32;  // workgroups that clear rows of no sequence
 
 // How a call is cut; sizes alone tell.
