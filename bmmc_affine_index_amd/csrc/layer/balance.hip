@@ -71,13 +71,24 @@ __device__ __forceinline__ void softmax_row(const dev::Vec<T, dev::Lanes<T>::N> 
     for (int i = 0; i < C * N; ++i) p[i] *= by;
 }
 
+// An expert's count and slope, and its part of the loss.
+__device__ __forceinline__ double end_expert(const BalanceArgs &a, int e, int32_t count,
+                                             int32_t tokens, double sum) {
+    const double counted = (double)tokens;
+    const float slope =
+        tokens ? (float)((double)count * a.num_experts / (counted * counted * a.choices)) : 0.0f;
+    a.counts[e] = count;
+    a.slopes[e] = slope;
+    return (double)slope * sum;
+}
+
 template <typename T, int C>
 __global__ void __launch_bounds__((64 * kBalanceWaves<T, C>))
     bmmc_balance_rows_kernel(const BalanceArgs a, int shift) {
     constexpr int N = dev::Lanes<T>::N, WAVES = kBalanceWaves<T, C>;
-    extern __shared__ float part[];  // WAVES, num_experts; first the counts
-    int32_t *hits = reinterpret_cast<int32_t *>(part);
+    extern __shared__ float part[];  // WAVES, num_experts; then the counts and the tokens'
     const int E = a.num_experts, tid = threadIdx.x;
+    int32_t *hits = reinterpret_cast<int32_t *>(part + WAVES * E);
     const int64_t from = blockIdx.x * a.chunk, to = min(from + a.chunk, a.tokens);
     const int lane = tid & 63, in_row = lane & ((1 << shift) - 1), wave = tid >> 6;
     const int rows = 64 >> shift;
@@ -107,11 +118,6 @@ __global__ void __launch_bounds__((64 * kBalanceWaves<T, C>))
         if (e >= 0 && e < E) atomicAdd(&hits[e], 1);
         if (i == t * a.choices) atomicAdd(&hits[E], 1);
     }
-    __syncthreads();
-    int32_t *hist = a.hits + (int64_t)blockIdx.x * (E + 1);
-    for (int e = tid; e <= E; e += blockDim.x) hist[e] = hits[e];
-    __syncthreads();
-
     // every lane of a wave goes round as often as any: rows of a wave are in step
     for (int64_t t0 = from + (int64_t)wave * rows; t0 < to; t0 += step, t += step) {
         dev::Vec<T, N> raw[C];
@@ -136,11 +142,31 @@ __global__ void __launch_bounds__((64 * kBalanceWaves<T, C>))
                 if (e < E) part[wave * E + e] = sums[c * N + i];
             }
     __syncthreads();
+    double all = 0.0;
     for (int e = tid; e < E; e += blockDim.x) {
         float s = 0.0f;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) s += part[w * E + e];
-        a.sums[(int64_t)blockIdx.x * E + e] = s;
+        if (gridDim.x > 1) {
+            a.sums[(int64_t)blockIdx.x * E + e] = s;
+            a.hits[(int64_t)blockIdx.x * (E + 1) + e] = hits[e];
+        } else {
+            all += end_expert(a, e, hits[e], hits[E], (double)s);
+        }
+    }
+    if (gridDim.x > 1) {
+        if (tid == 0) a.hits[(int64_t)blockIdx.x * (E + 1) + E] = hits[E];
+        return;
+    }
+    // alone: the loss is the sum of its terms
+#pragma unroll
+    for (int d = 32; d; d >>= 1) all += __shfl_xor(all, d, 64);
+    __shared__ double ends[WAVES];
+    if (lane == 0) ends[wave] = all;
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < WAVES; ++w) all += ends[w];
+        *a.loss = (float)all;
     }
 }
 
@@ -179,27 +205,23 @@ __global__ void __launch_bounds__(1024) bmmc_balance_join_kernel(const BalanceAr
     float *losses = reinterpret_cast<float *>(done + 1);
     if (row == 0) {
         double term = 0.0;
-        if (e < E) {
-            const double counted = (double)tokens;
-            const float slope =
-                tokens ? (float)((double)hits[0][col] * E / (counted * counted * a.choices)) : 0.0f;
-            a.counts[e] = hits[0][col];
-            a.slopes[e] = slope;
-            term = (double)slope * sums[0][col];
-        }
+        if (e < E) term = end_expert(a, e, hits[0][col], tokens, sums[0][col]);
 #pragma unroll
         for (int d = kColumns / 2; d; d >>= 1) term += __shfl_xor(term, d, kColumns);
+        int32_t last = 0;
         if (col == 0) {
             __hip_atomic_store(&losses[blockIdx.x], (float)term, __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);
-            if (__hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-                gridDim.x - 1) {
-                double all = 0.0;
-                for (uint32_t b = 0; b < gridDim.x; ++b)
-                    all += (double)__hip_atomic_load(&losses[b], __ATOMIC_RELAXED,
-                                                     __HIP_MEMORY_SCOPE_AGENT);
-                *a.loss = (float)all;
-            }
+            last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                   gridDim.x - 1;
+        }
+        if (__shfl(last, 0, kColumns)) {
+            double all = 0.0;
+            for (uint32_t b = col; b < gridDim.x; b += kColumns)
+                all += (double)__hip_atomic_load(&losses[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (int d = kColumns / 2; d; d >>= 1) all += __shfl_xor(all, d, kColumns);
+            if (col == 0) *a.loss = (float)all;
         }
     }
 }
@@ -285,11 +307,12 @@ template <typename T, int C> int forward(const BalanceArgs &x, int shift, hipStr
     BalanceArgs a = x;
     a.chunk = (a.tokens + a.blocks - 1) / a.blocks;
     const int waves = kBalanceWaves<T, C>;
-    const size_t lds = std::max((size_t)waves * a.num_experts, (size_t)a.num_experts + 1) * 4;
+    const size_t lds = ((size_t)(waves + 1) * a.num_experts + 1) * 4;
     hipLaunchKernelGGL((bmmc_balance_rows_kernel<T, C>), dim3(a.blocks), dim3(64 * waves), lds, s, a,
                        shift);
-    hipLaunchKernelGGL(bmmc_balance_join_kernel, dim3((a.num_experts + kColumns - 1) / kColumns),
-                       dim3(1024), 0, s, a);
+    if (a.blocks > 1)
+        hipLaunchKernelGGL(bmmc_balance_join_kernel, dim3((a.num_experts + kColumns - 1) / kColumns),
+                           dim3(1024), 0, s, a);
     return hipGetLastError() == hipSuccess ? BMMC_OK : BMMC_ERR_HIP;
 }
 

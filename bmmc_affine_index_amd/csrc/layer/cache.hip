@@ -33,19 +33,19 @@ RowCut row_cut(int dim, int each) {
     return c;
 }
 
-template <typename T>
+template <typename T, bool NT = false>
 __device__ __forceinline__ dev::Vec<T, kPer> load_part(const T *row, int at, int dim) {
-    if (at + kPer <= dim) return dev::load<T, kPer, false>(row + at);
+    if (at + kPer <= dim) return dev::load<T, kPer, NT>(row + at);
     dev::Vec<T, kPer> r;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) r.v[i] = at + i < dim ? row[at + i] : (T)0;
     return r;
 }
 
-template <typename T>
+template <typename T, bool NT = false>
 __device__ __forceinline__ void store_part(T *row, int at, int dim, const dev::Vec<T, kPer> &x) {
     if (at + kPer <= dim) {
-        dev::store<T, kPer, false>(row + at, x);
+        dev::store<T, kPer, NT>(row + at, x);
         return;
     }
 #pragma unroll
@@ -83,14 +83,25 @@ struct Quantize {
     int32_t q_tasks, k_tasks;  // waves' tasks a token for q and for k
 };
 
-// value / scale in 8 bits, clamped, NaN kept, rounded to nearest, ties to even.  The
-// quotient is the product with by = 1 / scale, put right by what it leaves of x.
-__device__ __forceinline__ float quotient_of(float x, float scale, float by) {
-    constexpr float kMax = 448.0f;
-    // an infinity's product leaves infinity again, not the difference of two
-    const float q = __builtin_amdgcn_fmed3f(x * by, -2.0f * kMax, 2.0f * kMax);
-    const float y = fmaf(fmaf(-q, scale, x), by, q);
-    return y > kMax ? kMax : y < -kMax ? -kMax : y;
+// 8 bits of value / scale.  The quotient is the product with by = 1 / scale, put right
+// by what it leaves of x; it passes 448 by its rounding at most, which 8 bits round off.
+__device__ __forceinline__ dev::Vec<uint8_t, kPer> quotients_of(const float (&x)[kPer], float scale,
+                                                                float by) {
+    uint32_t word[kPer / 4];
+#pragma unroll
+    for (int k = 0; k < kPer / 4; ++k) {
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float q = x[4 * k + i] * by;
+            y[i] = fmaf(fmaf(-q, scale, x[4 * k + i]), by, q);
+        }
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+        word[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+    }
+    dev::Vec<uint8_t, kPer> r;
+    __builtin_memcpy(&r.v, word, kPer);
+    return r;
 }
 
 // A part of a row: its elements, in 32 bits, and where in the row they are.
@@ -120,7 +131,8 @@ __device__ __forceinline__ void turn_part(Part &p, const T *row, bool on, int pa
     }
 }
 
-template <typename T, bool PAIRED>
+// WHOLE: rows, and halves of pairs, are whole vectors of a lane.
+template <typename T, bool PAIRED, bool WHOLE>
 __global__ void __launch_bounds__(kTurnThreads)
     bmmc_cache_quantize_kernel(const Quantize a, const Turn r, int64_t block0) {
     __shared__ float2 cs[kTurnPairs];
@@ -133,8 +145,9 @@ __global__ void __launch_bounds__(kTurnThreads)
     const int lane = a.cut.lane(), lane_row = a.cut.row(), rows = a.cut.rows_a_wave();
 
     // A lane has two vectors of its row: both halves of the same pairs, where those are
-    // whole vectors, and two neighbours of the rest.
-    const int halves = !PAIRED && (r.pairs & (kPer - 1)) == 0 ? r.pairs / kPer : 0;
+    // whole vectors, and of the rest one of each half, so that lanes side by side load and
+    // store side by side.
+    const int halves = !PAIRED && WHOLE ? r.pairs / kPer : 0;
     struct Row {
         const T *in;
         int t, kind, head;  // kind: 0 q, 1 k, 2 v
@@ -143,7 +156,10 @@ __global__ void __launch_bounds__(kTurnThreads)
     dev::Vec<T, kPer> next[2];
     const auto at_of = [&](int kind, int half) {
         const int turned = kind == 2 ? 0 : halves;
-        return lane < turned ? (lane + half * turned) * kPer : (2 * lane + half) * kPer;
+        const int all = ((kind == 2 ? a.v_dim : a.k_dim) + kPer - 1) / kPer;
+        const int rest = (all + 1) / 2 - turned;  // lanes of the rest
+        const int by = lane < turned ? half * turned : lane < turned + rest ? turned + half * rest : all;
+        return (lane + by) * kPer;
     };
     const auto fetch = [&](int task) {
         const int t = (int)quotient(a.by_tasks, (uint32_t)task);
@@ -159,7 +175,7 @@ __global__ void __launch_bounds__(kTurnThreads)
         for (int h = 0; h < 2; ++h) {
             const int at = at_of(kind, h);
             next[h] = dev::Vec<T, kPer>{};
-            if (row.on && at < dim) next[h] = load_part<T>(row.in, at, dim);
+            if (row.on && at < dim) next[h] = load_part<T>(row.in + at, 0, WHOLE ? kPer : dim - at);
         }
     };
     const int looker = (int)threadIdx.x - ((int)blockDim.x - 64);
@@ -182,7 +198,7 @@ __global__ void __launch_bounds__(kTurnThreads)
         const int dim = w.kind == 2 ? a.v_dim : a.k_dim;
         if (w.kind != 2 && r.pairs) {
             const float2 *turns = cs + w.t * r.pairs;
-            if (!PAIRED && halves) {
+            if constexpr (!PAIRED && WHOLE) {
                 if (lane < halves)
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) {
@@ -205,22 +221,43 @@ __global__ void __launch_bounds__(kTurnThreads)
                 dev::Floats<kPer> y;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) y[i] = p[h].x[i];
-                store_part<T>(out, p[h].at, dim, dev::narrow<T, kPer>(y));
+                store_part<T>(out + p[h].at, 0, WHOLE ? kPer : dim - p[h].at, dev::narrow<T, kPer>(y));
             }
             continue;
         }
-        float most = 0.0f;
+        // magnitudes are in the order of their bits, infinities and NaN behind the others
+        uint32_t bits = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const float m = fabsf(p[h].x[i]);
-                if (m < __builtin_inff()) most = fmaxf(most, m);  // neither infinities nor NaN
-            }
+            for (int i = 0; i < kPer; ++i)
+                bits = max(bits, __builtin_bit_cast(uint32_t, p[h].x[i]) & 0x7fffffffu);
+        const bool odd = __any(bits >= 0x7f800000u);
+        float most = __builtin_bit_cast(float, bits);
+        if (odd) {
+            most = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const float m = fabsf(p[h].x[i]);
+                    if (m < __builtin_inff()) most = fmaxf(most, m);
+                }
+        }
         most = dev::over_lanes(most, a.cut.shift, dev::Largest());
         const float scale = most == 0.0f ? 1.0f : fmaxf(most / 448.0f, 0x1p-126f);
         const float by = 1.0f / scale;
-        const PagePlace home = places[w.t];
+        if (odd) {  // infinities become what is stored as the type's largest; NaN stays
+            const float largest = fminf(448.0f * scale, 0x1.fffffep127f);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (fabsf(p[h].x[i]) == __builtin_inff())
+                        p[h].x[i] = __builtin_copysignf(largest, p[h].x[i]);
+        }
+        const PagePlace home{__builtin_amdgcn_readfirstlane(places[w.t].page),
+                             __builtin_amdgcn_readfirstlane(places[w.t].place)};
         if (home.page < 0 || !w.on) continue;
         const Scaled &c = w.kind == 1 ? a.k_cache : a.v_cache;
         uint8_t *out = c.data + home.page * c.page + home.place * c.place + w.head * c.head;
@@ -230,18 +267,8 @@ __global__ void __launch_bounds__(kTurnThreads)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (p[h].at >= dim) continue;
-            uint32_t word[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = quotient_of(p[h].x[4 * k + i], scale, by);
-                const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-                word[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
-            }
-            dev::Vec<uint8_t, kPer> bytes;
-            __builtin_memcpy(&bytes.v, word, kPer);
-            store_part<uint8_t>(out, p[h].at, dim, bytes);
+            store_part<uint8_t>(out + p[h].at, 0, WHOLE ? kPer : dim - p[h].at,
+                                quotients_of(p[h].x, scale, by));
         }
     }
 }
@@ -269,11 +296,15 @@ template <typename T, bool PAIRED> int quantize(const QuantizeArgs &h, hipStream
     a.k_tasks = (a.heads + rows - 1) / rows;
     const int64_t tasks = a.q_tasks + 2 * a.k_tasks;
     a.by_tasks = fast_div((uint32_t)tasks);
-    const TurnCut cut = turn_cut(a.tokens, r.pairs, tasks);
+    TurnCut cut = turn_cut(a.tokens, r.pairs, tasks);
+    const int n = std::min(kTurnTokens, r.pairs ? kTurnPairs / r.pairs : kTurnTokens);
+    if (a.tokens / n >= kTurnBlocks) cut = TurnCut{n, kTurnWaves, (a.tokens + n - 1) / n, 1};
     a.tokens_a_block = cut.tokens_a_block;
+    const bool whole = h.k_dim % kPer == 0 && h.v_dim % kPer == 0 && (PAIRED || r.pairs % kPer == 0);
+    const auto kernel = whole ? bmmc_cache_quantize_kernel<T, PAIRED, true>
+                              : bmmc_cache_quantize_kernel<T, PAIRED, false>;
     return in_launches(cut.blocks, kTurnThreads, [&](uint32_t nb, int64_t b0) {
-        hipLaunchKernelGGL((bmmc_cache_quantize_kernel<T, PAIRED>), dim3(nb, cut.shares),
-                           dim3(64 * cut.waves), 0, s, a, r, b0);
+        hipLaunchKernelGGL(kernel, dim3(nb, cut.shares), dim3(64 * cut.waves), 0, s, a, r, b0);
     });
 }
 
@@ -287,20 +318,26 @@ constexpr int kReadTokens = 64;  // most of a workgroup
 constexpr int kReadBlocks = 2048;
 constexpr int kReadAhead = 4;    // rows a lane has on their way
 
-// Where a token's rows and their scales begin, in elements; k is below 0 if nowhere.
-struct ReadPlace {
-    int64_t k, v, k_scale, v_scale;
+// Keys or values: one grid's half each, so that all of it is the same in a workgroup.
+struct ReadHalf {
+    void *out;
+    int64_t out_token, out_head;
+    Scaled cache;
+    int32_t dim;
 };
 
 struct Read {
-    void *k_out, *v_out;
-    int64_t k_token, k_head, v_token, v_head;
-    Scaled k_cache, v_cache;
+    ReadHalf half[2];
     PageTable where;
-    FastDiv by_rows;
+    FastDiv by_heads;
     int64_t tokens;
     RowCut cut;
-    int32_t heads, k_dim, v_dim, tokens_a_block;
+    int32_t heads, tokens_a_block;
+};
+
+// Where a token's rows and their scales begin, in elements; `in` is below 0 if nowhere.
+struct ReadPlace {
+    int64_t in, scale;
 };
 
 template <typename E> __device__ __forceinline__ dev::Floats<kPer> widened(const dev::Vec<E, kPer> &x) {
@@ -323,92 +360,80 @@ template <typename E> __device__ __forceinline__ dev::Floats<kPer> widened(const
     }
 }
 
-template <typename T, typename E>
+// WHOLE: rows are whole vectors of a lane.
+template <typename T, typename E, bool WHOLE, bool NT>
 __global__ void __launch_bounds__(256) bmmc_cache_read_kernel(const Read a, int64_t block0) {
     __shared__ ReadPlace places[kReadTokens];
+    const ReadHalf &x = a.half[blockIdx.z];
     const int64_t token0 = (block0 + blockIdx.x) * a.tokens_a_block;
     const int tokens = (int)min((int64_t)a.tokens_a_block, a.tokens - token0);
     if ((int)threadIdx.x < tokens) {
         const PagePlace p = page_place(a.where, token0 + threadIdx.x);
-        ReadPlace &to = places[threadIdx.x];
-        to.k = p.page < 0 ? -1 : p.page * a.k_cache.page + p.place * a.k_cache.place;
-        to.v = p.page * a.v_cache.page + p.place * a.v_cache.place;
-        to.k_scale = p.page * a.k_cache.scale_page + p.place * a.k_cache.scale_place;
-        to.v_scale = p.page * a.v_cache.scale_page + p.place * a.v_cache.scale_place;
+        places[threadIdx.x] =
+            ReadPlace{p.page < 0 ? -1 : p.page * x.cache.page + p.place * x.cache.place,
+                      p.page * x.cache.scale_page + p.place * x.cache.scale_place};
     }
     __syncthreads();
     const int at = a.cut.lane() * kPer, each = a.cut.rows_a_wave() * 4;  // rows of a workgroup at once
+    if (at >= x.dim) return;
     const int mine = (int)(threadIdx.x >> 6) * a.cut.rows_a_wave() + a.cut.row();
-    const int rows = tokens * 2 * a.heads;
+    const int rows = tokens * a.heads;
+    const E *const in = reinterpret_cast<const E *>(x.cache.data) + at;
+    T *const out = static_cast<T *>(x.out) + token0 * x.out_token + at;
+    const int size = WHOLE ? kPer : x.dim - at;
     for (int base = (int)blockIdx.y * each * kReadAhead; base < rows;
          base += (int)gridDim.y * each * kReadAhead) {
-        dev::Vec<E, kPer> x[kReadAhead];
+        dev::Vec<E, kPer> raw[kReadAhead];
         float scale[kReadAhead];
-        T *out[kReadAhead];
-        int dim[kReadAhead];  // 0 where the lane has nothing to write
+        int64_t to[kReadAhead];
 #pragma unroll
         for (int j = 0; j < kReadAhead; ++j) {
-            const int row = base + j * each + mine;
-            x[j] = dev::Vec<E, kPer>{};
+            // rows behind the last are read as the last, and not written
+            const uint32_t row = (uint32_t)min(base + j * each + mine, rows - 1);
+            const uint32_t t = quotient(a.by_heads, row), head = row - t * (uint32_t)a.heads;
+            to[j] = t * x.out_token + head * x.out_head;
+            raw[j] = dev::Vec<E, kPer>{};
             scale[j] = 1.0f;
-            dim[j] = 0;
-            if (row >= rows) continue;
-            const int t = (int)quotient(a.by_rows, (uint32_t)row);
-            int head = row - t * 2 * a.heads;
-            const bool key = head < a.heads;
-            head -= key ? 0 : a.heads;
-            const int size = key ? a.k_dim : a.v_dim;
-            if (at >= size) continue;
-            dim[j] = size;
-            out[j] = static_cast<T *>(key ? a.k_out : a.v_out) +
-                     (token0 + t) * (key ? a.k_token : a.v_token) + head * (key ? a.k_head : a.v_head);
-            const ReadPlace &home = places[t];
-            if (home.k < 0) continue;
-            const Scaled &k = a.k_cache, &v = a.v_cache;
-            x[j] = load_part<E>(reinterpret_cast<const E *>(key ? k.data : v.data) +
-                                    (key ? home.k : home.v) + head * (key ? k.head : v.head),
-                                at, size);
-            if (sizeof(E) == 1)
-                scale[j] = (key ? k.scale : v.scale)[(key ? home.k_scale : home.v_scale) +
-                                                     head * (key ? k.scale_head : v.scale_head)];
+            const ReadPlace home = places[t];
+            if (home.in < 0) continue;
+            raw[j] = load_part<E, NT>(in + home.in + head * x.cache.head, 0, size);
+            if (sizeof(E) == 1) scale[j] = x.cache.scale[home.scale + head * x.cache.scale_head];
         }
 #pragma unroll
         for (int j = 0; j < kReadAhead; ++j) {
-            if (!dim[j]) continue;
+            if (base + j * each + mine >= rows) continue;
             if constexpr (sizeof(E) == 1)
-                store_part<T>(out[j], at, dim[j], dev::narrow<T, kPer>(widened<E>(x[j]) * scale[j]));
+                store_part<T, NT>(out + to[j], 0, size, dev::narrow<T, kPer>(widened<E>(raw[j]) * scale[j]));
             else
-                store_part<T>(out[j], at, dim[j], x[j]);
+                store_part<T, NT>(out + to[j], 0, size, raw[j]);
         }
     }
 }
 
 template <typename T, typename E> int read(const ReadArgs &h, hipStream_t s) {
     Read a{};
-    a.k_out = h.k.out;
-    a.v_out = h.v.out;
-    a.k_token = h.k.out_token;
-    a.k_head = h.k.out_head;
-    a.v_token = h.v.out_token;
-    a.v_head = h.v.out_head;
-    a.k_cache = scaled_of(h.k_cache);
-    a.v_cache = scaled_of(h.v_cache);
+    a.half[0] = ReadHalf{h.k.out, h.k.out_token, h.k.out_head, scaled_of(h.k_cache), h.k_dim};
+    a.half[1] = ReadHalf{h.v.out, h.v.out_token, h.v.out_head, scaled_of(h.v_cache), h.v_dim};
     a.where = h.where;
     a.tokens = h.tokens;
     a.cut = row_cut(std::max(h.k_dim, h.v_dim), kPer);
     a.heads = (int32_t)h.k.heads;
-    a.k_dim = h.k_dim;
-    a.v_dim = h.v_dim;
-    a.by_rows = fast_div((uint32_t)(2 * h.k.heads));
+    a.by_heads = fast_div((uint32_t)h.k.heads);
     a.tokens_a_block =
-        (int32_t)std::min<int64_t>(kReadTokens, (h.tokens + kReadBlocks - 1) / kReadBlocks);
+        (int32_t)std::min<int64_t>(kReadTokens, (2 * h.tokens + kReadBlocks - 1) / kReadBlocks);
     const int64_t blocks = (a.tokens + a.tokens_a_block - 1) / a.tokens_a_block;
     // a token's rows are shared by workgroups where there are few tokens
-    const int64_t passes = (a.tokens_a_block * 2 * h.k.heads - 1) /
-                               (a.cut.rows_a_wave() * 4 * kReadAhead) + 1;
-    const uint32_t shares = (uint32_t)std::max<int64_t>(1, std::min(passes, kReadBlocks / blocks));
-    return in_launches(blocks, 256 * shares, [&](uint32_t nb, int64_t b0) {
-        hipLaunchKernelGGL((bmmc_cache_read_kernel<T, E>), dim3(nb, shares), dim3(256), 0, s, a, b0);
+    const int64_t passes =
+        (a.tokens_a_block * h.k.heads - 1) / (a.cut.rows_a_wave() * 4 * kReadAhead) + 1;
+    const uint32_t shares =
+        (uint32_t)std::max<int64_t>(1, std::min(passes, kReadBlocks / (2 * blocks)));
+    const bool whole = h.k_dim % kPer == 0 && h.v_dim % kPer == 0;
+    const bool streamed = whole && streams(a.tokens * a.heads * (h.k_dim + h.v_dim), sizeof(T));
+    const auto kernel = streamed ? bmmc_cache_read_kernel<T, E, true, true>
+                        : whole  ? bmmc_cache_read_kernel<T, E, true, false>
+                                 : bmmc_cache_read_kernel<T, E, false, false>;
+    return in_launches(blocks, 512 * shares, [&](uint32_t nb, int64_t b0) {
+        hipLaunchKernelGGL(kernel, dim3(nb, shares, 2), dim3(256), 0, s, a, b0);
     });
 }
 

@@ -35,6 +35,7 @@ AttendPlan attend_plan(const bmmc_attention &a) {
 // Workgroups that sum the tokens' probabilities: of 16 tokens at least, and no
 // more than leave the second launch little to sum.
 int32_t balance_blocks(int64_t tokens, int num_experts) {
+    if (tokens * num_experts <= 32768) return 1;
     const int64_t most = std::max<int64_t>(64, std::min<int64_t>(256, 65536 / num_experts));
     return (int32_t)std::max<int64_t>(1, std::min(most, (tokens + 15) / 16));
 }
