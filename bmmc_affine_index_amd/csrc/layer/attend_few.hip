@@ -49,14 +49,15 @@ template <typename E> __device__ __forceinline__ bool has_nonfinite(uint32_t w) 
 template <typename T, typename E, int DP, int KB, bool AHEAD> struct Few {
     static constexpr int CE = Product<T>::N;      // elements of a vector along a head
     static constexpr int NK = DP / (4 * CE);      // of them a lane has of a key
-    static constexpr int VE = sizeof(T) == 2 && DP == 64 ? 4 : CE;  // values of a key in a vector
-    static constexpr int VG = DP / (16 * VE);     // vectors of a key's values in a lane
+    // values of a key in a vector, and such vectors in a lane
+    static constexpr int VE = sizeof(T) == 2 ? (DP == 64 ? 4 : CE) : DP == 96 ? 2 : CE;
+    static constexpr int VG = (DP + 16 * VE - 1) / (16 * VE);
     static constexpr int KT = 16 * KB;            // keys of a tile
     static constexpr int VK = 4 * KB;             // keys in a lane
     static constexpr int KG = AHEAD ? NK : 8;     // vectors of a key fetched at a time
     static constexpr bool kQueriesInLds = DP == 512;
-    // DP + 4: the 16 rows of a joined tile start in different banks
-    static constexpr int kPitch = DP + 4;
+    // + 4: the 16 rows of a joined tile start in different banks
+    static constexpr int kPitch = VG * 16 * VE + 4;
 
     struct PerWave {
         const uint8_t *at[2][2][KT];  // of this tile and the next: keys' and values' rows
@@ -421,9 +422,14 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int e = 0; e < VE; e += 4)
-                    *reinterpret_cast<f4 *>(&joined.o[wave][n][(v * 16 + 4 * g + i) * VE + e]) =
-                        f4{o[v][e][i], o[v][e + 1][i], o[v][e + 2][i], o[v][e + 3][i]};
+                for (int e = 0; e < VE; e += VE < 4 ? VE : 4) {
+                    float *to = &joined.o[wave][n][(v * 16 + 4 * g + i) * VE + e];
+                    if constexpr (VE == 2)
+                        *reinterpret_cast<float2 *>(to) = make_float2(o[v][0][i], o[v][1][i]);
+                    else
+                        *reinterpret_cast<f4 *>(to) =
+                            f4{o[v][e][i], o[v][e + 1][i], o[v][e + 2][i], o[v][e + 3][i]};
+                }
         __syncthreads();
         const int r = threadIdx.x >> 4, col = threadIdx.x & 15;
         const int64_t out_row = (int64_t)tile.tile * 16 + r;
@@ -580,6 +586,7 @@ template <typename T, typename E> int few_by_size(const AttendArgs &x, hipStream
     constexpr bool kWide = sizeof(T) == 4;
     const int dim = x.a.k_dim > x.a.v_dim ? x.a.k_dim : x.a.v_dim;
     if (dim <= 64) return few<T, E, 64, 2, true>(x, s);
+    if (dim <= 96) return few<T, E, 96, 2, true>(x, s);
     if (dim <= 128) return few<T, E, 128, kWide ? 1 : 2, true>(x, s);
     if (dim <= 256) return few<T, E, 256, kWide ? 1 : 2, true>(x, s);
     return few<T, E, 512, kWide ? 1 : 2, false>(x, s);

@@ -21,7 +21,7 @@ AttendPlan attend_plan(const bmmc_attention &a) {
     const bool many = !wide && dim <= 256 && a.tokens * group > 48 * filled;
     p.rows = many ? 128 : 16;
     // four waves, of 16 keys each where long rows of 32 bits leave no registers for 32
-    p.unit = many || (wide && dim > 64) ? 64 : 128;
+    p.unit = many || (wide && dim > 96) ? 64 : 128;
     p.tiles = a.starts ? a.tokens * group / p.rows + filled
                        : a.tokens * ((group + p.rows - 1) / p.rows);
     // workgroups of a compute unit, by the registers that a head's elements take
