@@ -887,3 +887,24 @@ def test_in_place_results_count_for_autograd():
         call(t)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             loss.backward()
+
+
+# --------------------------------------------------------------------------
+# The example
+# --------------------------------------------------------------------------
+
+def test_the_example_from_8_bits():
+    """A layer served from a cache in 8 bits: finite, and the router's balance gradient among those
+    that the training step compares (it raises where shapes or gradients are missing)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(__file__), "..", "examples", "sparse_layer.py")
+    spec = importlib.util.spec_from_file_location("sparse_layer", path)
+    layer = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(layer)
+    device = torch.device(DEV)
+    with torch.no_grad():
+        most, middle = layer.serve(device, torch.bfloat16, 70, 3, narrow=True)
+    assert math.isfinite(most) and middle <= most
+    # as in the serving test: sums of at most 512 terms, each off by one rounding in 32 bits
+    assert layer.train(device, 33) <= 512 * U32
