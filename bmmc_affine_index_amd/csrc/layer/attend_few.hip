@@ -49,8 +49,9 @@ template <typename E> __device__ __forceinline__ bool has_nonfinite(uint32_t w) 
 template <typename T, typename E, int DP, int KB, bool AHEAD> struct Few {
     static constexpr int CE = Product<T>::N;      // elements of a vector along a head
     static constexpr int NK = DP / (4 * CE);      // of them a lane has of a key
-    // values of a key in a vector, and such vectors in a lane
-    static constexpr int VE = sizeof(T) == 2 ? (DP == 64 ? 4 : CE) : DP == 96 ? 2 : CE;
+    // values of a key in a vector, of whole words, and such vectors in a lane
+    static constexpr int VE = sizeof(T) == 2 ? (DP == 64 ? 4 : CE) : DP == 96 && sizeof(E) == 4 ? 2 : CE;
+    static_assert(VE * sizeof(E) % 4 == 0);
     static constexpr int VG = (DP + 16 * VE - 1) / (16 * VE);
     static constexpr int KT = 16 * KB;            // keys of a tile
     static constexpr int VK = 4 * KB;             // keys in a lane

@@ -444,6 +444,26 @@ def test_attention_of_other_shapes(case, dtype):
              behind=3).check()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("narrow", ["no", "head", "row"])
+@pytest.mark.parametrize("dim,v_dim", [(64, 60), (80, 96), (96, 65), (72, 128), (128, 112), (130, 256), (260, 512)])
+def test_attention_of_each_padded_size(dim, v_dim, narrow, dtype):
+    """Heads that are padded to each of the sizes, in shares of few rows and of many."""
+    for new, lengths in (([1, 3], [70, 333]), ([40, 1], [150, 9])):
+        Case(new, lengths, 16, 6, 2, dim, v_dim, dtype, narrow).check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,v_dim,narrow", [(96, 96, "no"), (80, 96, "row"), (128, 70, "head"), (250, 256, "no")])
+def test_attention_of_whole_tiles(dim, v_dim, narrow, dtype):
+    """As many rows as make a workgroup a tile: of 16 rows in 32 bits, of 128 in 16."""
+    if dtype == torch.float32:
+        Case([130, 1, 200], [180, 40, 200], 16, 128, 32, dim, v_dim, dtype, narrow).check()
+    else:
+        Case([20] * 63 + [50], [20 + 3 * i for i in range(63)] + [300], 16, 128, 32, dim, v_dim, dtype,
+             narrow).check()
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with a workspace of its own."""
     cases = [Case([1] * 6, [1, 900, 33, 2000, 5, 64], 16, 8, 2, 128, 128, torch.bfloat16),
