@@ -2,14 +2,16 @@
 //
 // The loss sums p = softmax(logits) over the tokens for each expert, the
 // gradient needs each token's p again: one pass over the logits each, in which
-// a token's row lies in as many lanes of a wave as it has vectors, and its
-// maximum and sums go through exchanges among them.  A lane holds the same
+// a token's row lies in 16 lanes of a wave or, if long, more, and its maximum and
+// sums go through moves among them.  A lane holds the same
 // experts of all its rows, so that the sums over tokens stay in registers until
 // the end; they leave the workgroup once and are summed by a second launch, in
 // a fixed order.  Choices are counted in LDS by whole numbers, whose order
 // does not matter.
 //
 // Bound by memory: the logits are read once for the loss, once for the gradient.
+// 65536 tokens of 256 experts in fp32: 17 us and 7 for the join (36 and 10 with a row in
+// 64 lanes and 8 waves a workgroup), the gradient 22.5, 6.0 TB/s.
 #include <algorithm>
 
 #include "../tokens/device.h"

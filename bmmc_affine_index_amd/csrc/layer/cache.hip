@@ -3,12 +3,17 @@
 //
 // A head of a token is a row with a scale of its own: its largest finite
 // magnitude / 448.  The largest is known only when all of the row has been
-// turned, so a row lies in one wave, 8 elements a lane, and never leaves its
-// registers: loaded, turned (a pair's other half comes from another lane), its
-// largest magnitude found by exchanges among the row's lanes, divided and stored.
+// turned, so a row lies in one wave, 16 elements a lane, and never leaves its
+// registers: loaded, turned (both halves of a pair are in one lane), its largest
+// magnitude found by moves among the row's lanes, divided and stored.
 //
-// Bound by memory: each element is read once and written once, in 1 byte.
-// Turns are made once a token, in LDS, as for rotary positions.
+// Bound by memory: each element is read once and written once, keys and values in 1
+// byte.  Turns are made once a token, in LDS, as for rotary positions.
+//
+// Measured: 16384 tokens of 24 + 8 heads of 128 and 8 of 96 in bf16, 291 MB: 64 us, 4.6
+// TB/s (96 with 8 elements a lane, halves exchanged and true divisions); 64 tokens 4 us
+// on the device.  Read back: 40001 tokens of 8 + 8 heads of 128, 8 bits to bf16, 249 MB:
+// 51.5 us, 4.8 TB/s.
 #include "../tokens/turns.h"
 #include "lanes.h"
 #include "layer.h"
@@ -296,6 +301,9 @@ template <typename T, bool PAIRED> int quantize(const QuantizeArgs &h, hipStream
     a.k_tasks = (a.heads + rows - 1) / rows;
     const int64_t tasks = a.q_tasks + 2 * a.k_tasks;
     a.by_tasks = fast_div((uint32_t)tasks);
+    // Many tokens go four to a workgroup, whose waves then have as many tasks each
+    // (16384 tokens of 5 tasks: 1 token 75 us, 2 65.2, 3 64.1, 4 65.0, 6 68.7, 8 71.0).
+    // Streamed loads and stores: 70, rows being written in parts of lines.
     TurnCut cut = turn_cut(a.tokens, r.pairs, tasks);
     const int n = std::min(kTurnTokens, r.pairs ? kTurnPairs / r.pairs : kTurnTokens);
     if (a.tokens / n >= kTurnBlocks) cut = TurnCut{n, kTurnWaves, (a.tokens + n - 1) / n, 1};
@@ -428,6 +436,7 @@ template <typename T, typename E> int read(const ReadArgs &h, hipStream_t s) {
     const uint32_t shares =
         (uint32_t)std::max<int64_t>(1, std::min(passes, kReadBlocks / (2 * blocks)));
     const bool whole = h.k_dim % kPer == 0 && h.v_dim % kPer == 0;
+    // 164 MB of results: 51.5 us streamed, 56 through the caches
     const bool streamed = whole && streams(a.tokens * a.heads * (h.k_dim + h.v_dim), sizeof(T));
     const auto kernel = streamed ? bmmc_cache_read_kernel<T, E, true, true>
                         : whole  ? bmmc_cache_read_kernel<T, E, true, false>

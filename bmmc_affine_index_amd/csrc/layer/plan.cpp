@@ -18,6 +18,8 @@ AttendPlan attend_plan(const bmmc_attention &a) {
     const bool wide = a.type == BMMC_F32;
     const int dim = std::max(a.k_dim, a.v_dim);
     AttendPlan p{};
+    // tiles of 128 rows where a sequence has more than 48 (64 rows over 32768 keys: 50 us,
+    // 66 by tiles of 16; up to 48 rows as many tiles of 16 read no more than one of 128)
     const bool many = !wide && dim <= 256 && a.tokens * group > 48 * filled;
     p.rows = many ? 128 : 16;
     // four waves, of 16 keys each where long rows of 32 bits leave no registers for 32
@@ -32,10 +34,12 @@ AttendPlan attend_plan(const bmmc_attention &a) {
     return p;
 }
 
-// Workgroups that sum the tokens' probabilities: of 16 tokens at least, and no
-// more than leave the second launch little to sum.
+// Workgroups that sum the tokens' probabilities: one, without a second launch, for a
+// few rounds of rows (32 tokens of 1024 experts 7.4 us, 11.0 with two launches; 128 of
+// 256 9.4 and 10.5; 512 of 64 9.8 and 8.7), otherwise of 16 tokens at least, and no more
+// than leave the second launch little to sum.
 int32_t balance_blocks(int64_t tokens, int num_experts) {
-    if (tokens * num_experts <= 32768) return 1;
+    if (tokens <= 1024 && tokens * num_experts <= 32768) return 1;
     const int64_t most = std::max<int64_t>(64, std::min<int64_t>(256, 65536 / num_experts));
     return (int32_t)std::max<int64_t>(1, std::min(most, (tokens + 15) / 16));
 }

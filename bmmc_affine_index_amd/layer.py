@@ -117,7 +117,9 @@ def cache_quantize(k, v, k_cache, v_cache, k_scale, v_scale, page_table, positio
     The caches are float8_e4m3fn, k_scale and v_scale float32 [pages, places,
     H] with any strides; both are written in place.  What is stored is value /
     scale to the nearest; infinities become the type's largest value, NaN stays
-    NaN.  Everything else is as in ``cache_append``."""
+    NaN.  Tokens of one call go to places of their own: where two go to the
+    same, its scale may be one's and its values the other's.  Everything else
+    is as in ``cache_append``."""
     return _run(_calls().quantize,
                 (k, v, k_cache, v_cache, k_scale, v_scale, page_table, positions, sequences, freqs,
                  axes, turns, interleaved, scale, q, q_out), stream)

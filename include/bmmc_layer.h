@@ -98,7 +98,9 @@ int bmmc_cache_attention(const bmmc_attention *a, const bmmc_scaled_cache *k_cac
  * rounded to nearest; infinities become the type's largest value, NaN stays
  * NaN.  Magnitudes are those of the turned keys in 32 bits.  The other
  * arguments are bmmc_cache_append's.  No two scales of a cache share an
- * address, and none lies in a cache or in what is read. */
+ * address, and none lies in a cache or in what is read.  Tokens of one call go
+ * to places of their own: where two go to the same, its scale may be one's and
+ * its values the other's. */
 int bmmc_cache_quantize(const bmmc_heads *q, const bmmc_heads *k, const bmmc_heads *v,
                         const bmmc_scaled_cache *k_cache, const bmmc_scaled_cache *v_cache,
                         int64_t pages, int64_t page_size, const int32_t *table, int64_t batch,

@@ -444,6 +444,23 @@ def test_attention_of_other_shapes(case, dtype):
              behind=3).check()
 
 
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("tokens", [2, 100])
+def test_attention_over_a_cache_without_pages(tokens, page):
+    """Every entry of the table is out of range, and there may be no scales at all."""
+    q = torch.randn(tokens, 4, 64, device=DEV)
+    table = torch.zeros(1, 3, dtype=torch.int32, device=DEV)
+    where = dict(starts=torch.tensor([0, tokens], dtype=torch.int32, device=DEV))
+    lengths = torch.tensor([3 * page], dtype=torch.int32, device=DEV)
+    for dtype in TYPES:
+        for kind in (dtype, F8):
+            pools = [torch.zeros(0, page, 2, 64, dtype=kind, device=DEV) for _ in range(2)]
+            scales = dict(zip(("k_scale", "v_scale"), (torch.zeros(0, page, 2, device=DEV) for _ in range(2)))) \
+                if kind == F8 else {}
+            got = bm.cache_attention(q.to(dtype), *pools, table, lengths, **where, **scales)
+            assert got.shape == (tokens, 4, 64) and not bool(got.any())
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("narrow", ["no", "head", "row"])
 @pytest.mark.parametrize("dim,v_dim", [(64, 60), (80, 96), (96, 65), (72, 128), (128, 112), (130, 256), (260, 512)])
@@ -752,7 +769,8 @@ def _balance(logits, chosen, mask, grad=1.0):
 BALANCE = [  # tokens, choices, experts, masked
     (1, 1, 1, 0.0), (1, 2, 3, 0.0), (5, 1, 7, 0.5), (33, 4, 8, 0.0), (257, 4, 60, 0.1), (100, 8, 64, 0.0), (63, 2, 65, 0.2),
     (300, 10, 256, 0.3), (77, 3, 257, 0.0), (50, 6, 1000, 0.1), (40, 8, 2048, 0.0), (19, 1024, 13, 0.0),
-    (20000, 8, 128, 0.05), (9000, 2, 5, 0.0), (4097, 4, 513, 1.0), (3000, 7, 2041, 0.4)]
+    (20000, 8, 128, 0.05), (9000, 2, 5, 0.0), (4097, 4, 513, 1.0), (3000, 7, 2041, 0.4),
+    (1024, 3, 32, 0.1), (1025, 3, 31, 0.0), (16, 5, 2048, 0.0), (17, 5, 2048, 0.2), (1023, 1, 2, 0.3)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
