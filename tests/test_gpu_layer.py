@@ -444,6 +444,32 @@ def test_attention_of_other_shapes(case, dtype):
              behind=3).check()
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("narrow", ["no", "row"])
+@pytest.mark.parametrize("width", [3, 1 << 13])
+def test_attention_in_shares_of_many_rows(width, narrow, dtype):
+    """Tiles of 128 rows whose keys are cut into shares, as by tables that are wide, and not."""
+    for new, lengths in (([60, 33, 1, 0], [700, 40, 64, 5]), ([70], [900]), ([5] * 70, list(range(5, 215, 3)))):
+        c = Case(new, lengths, 16, 8, 2, 128, 96, dtype, narrow, behind=1)
+        args, named = c.args()
+        table = torch.full((len(new), c.table.shape[1] + width), -1, dtype=torch.int32, device=DEV)
+        table[:, :c.table.shape[1]] = c.table
+        want, slack = c.want(128 ** -0.5)
+        _within(bm.cache_attention(*args[:3], table, args[4], **named), want, slack, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new,width", [(1, 0), (6, 0), (6, 300)])
+def test_attention_of_hundreds_of_short_sequences(new, width, dtype):
+    """More sequences than tiles are looked for in, shorter than a tile of keys; of a wide table too."""
+    c = Case([new] * 600, [new + i % 97 for i in range(600)], 16, 6, 2, 64, 64, dtype)
+    args, named = c.args()
+    table = torch.full((600, c.table.shape[1] + width), -1, dtype=torch.int32, device=DEV)
+    table[:, :c.table.shape[1]] = c.table
+    want, slack = c.want(64 ** -0.5)
+    _within(bm.cache_attention(*args[:3], table, args[4], **named), want, slack, dtype)
+
+
 @pytest.mark.parametrize("page", [1, 16])
 @pytest.mark.parametrize("tokens", [2, 100])
 def test_attention_over_a_cache_without_pages(tokens, page):
@@ -466,7 +492,7 @@ def test_attention_over_a_cache_without_pages(tokens, page):
 @pytest.mark.parametrize("dim,v_dim", [(64, 60), (80, 96), (96, 65), (72, 128), (128, 112), (130, 256), (260, 512)])
 def test_attention_of_each_padded_size(dim, v_dim, narrow, dtype):
     """Heads that are padded to each of the sizes, in shares of few rows and of many."""
-    for new, lengths in (([1, 3], [70, 333]), ([40, 1], [150, 9])):
+    for new, lengths in (([1, 3], [70, 333]), ([40, 1], [150, 9]), ([90], [290])):
         Case(new, lengths, 16, 6, 2, dim, v_dim, dtype, narrow).check()
 
 
