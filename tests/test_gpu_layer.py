@@ -458,6 +458,20 @@ def test_attention_in_shares_of_many_rows(width, narrow, dtype):
         _within(bm.cache_attention(*args[:3], table, args[4], **named), want, slack, dtype)
 
 
+@pytest.mark.parametrize("sequences", [3, 600])
+def test_attention_with_a_table_of_no_pages(sequences):
+    """No sequence has a place that could be seen: zeros, and rows of nobody left as they are."""
+    table = torch.zeros(sequences, 0, dtype=torch.int32, device=DEV)
+    lengths = torch.full((sequences,), 40, dtype=torch.int32, device=DEV)
+    starts = 2 + 3 * torch.arange(sequences + 1, dtype=torch.int32, device=DEV)
+    for dtype in TYPES:
+        q = torch.randn(3 * sequences + 4, 40, 64, device=DEV).to(dtype)
+        pools = [torch.full((2, 16, 2, 64), NAN, device=DEV).to(dtype) for _ in range(2)]
+        out = torch.full((3 * sequences + 4, 40, 64), 7.0, device=DEV).to(dtype)
+        bm.cache_attention(q, *pools, table, lengths, starts=starts, out=out)
+        assert bool((out[:2] == 7).all()) and bool((out[-2:] == 7).all()) and not bool(out[2:-2].any())
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("new,width", [(1, 0), (6, 0), (6, 300)])
 def test_attention_of_hundreds_of_short_sequences(new, width, dtype):
@@ -930,6 +944,39 @@ def test_in_a_graph():
         torch.cuda.synchronize()
         assert _same(outs[0], want), seed
         assert _same(outs[1], wanted), seed
+
+
+@pytest.mark.parametrize("tokens", [40, 3000])
+def test_a_balance_step_in_a_graph(tokens):
+    """Loss and gradient captured together, in one workgroup and in two launches, replayed on other
+    inputs with eager steps in between; no eager graph of the leaves is alive while it is captured."""
+    def inputs(seed):
+        logits, chosen, mask = _balance_case(tokens, 4, 64, torch.bfloat16, 0.2, seed)
+        return [logits.to(DEV).requires_grad_(), chosen.to(DEV), mask.to(DEV)]
+
+    def step(x, chosen, mask):
+        got = bm.expert_balance(x, chosen, mask=mask)
+        return [got.loss, got.counts, got.slopes, *torch.autograd.grad(got.loss * 0.5, x)]
+    a = inputs(1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step(*a)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*a)
+    for seed in (2, 3, 4):
+        b = inputs(seed)
+        want = [t.detach().clone() for t in step(*b)]
+        with torch.no_grad():
+            for t, u in zip(a, b):
+                t.copy_(u)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want)), seed
 
 
 def test_in_place_results_count_for_autograd():
