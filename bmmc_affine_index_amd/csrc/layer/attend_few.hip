@@ -333,6 +333,11 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                     p[b * 4 + i] = scaled ? w * by[i] : w;
                 }
             }
+            // a weight of 0 times a scale that is no number would reach rows that do not see its key
+            if (scaled && parted)
+#pragma unroll
+                for (int j = 0; j < VK; ++j)
+                    if (!(see >> 4 * g & 1u << (j / 4 * 16 + j % 4))) p[j] = 0.0f;
             // a value that is no number must not reach rows that do not see its key
             bool odd = false;
             if (parted) {

@@ -330,15 +330,16 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                 const uint64_t there = uniform(lds.seen[which]);
                 const bool parted = t + kKeys - 1 > wave_first ||
                                     (x.a.window && t <= wave_last - x.a.window);
-                if (parted || ~there) {
-                    const uint64_t see = seen_of(place - t, x.a.window) & there;
-                    const uint64_t mine = see >> 4 * half;
+                // this lane's scores of keys that its row does not see
+                const auto hide = [&](float as) {
+                    const uint64_t mine = (seen_of(place - t, x.a.window) & there) >> 4 * half;
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (!((uint32_t)(mine >> b * 32) & 1u << (8 * (i / 4) + i % 4))) s[b][i] = kNothing;
-                }
+                            if (!((uint32_t)(mine >> b * 32) & 1u << (8 * (i / 4) + i % 4))) s[b][i] = as;
+                };
+                if (parted || ~there) hide(kNothing);
                 float top = kNothing;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
@@ -377,6 +378,8 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) s[b][i + j] *= by[j];
                         }
+                    // a weight of 0 times a scale that is no number is no number
+                    if (parted) hide(0.0f);
                 }
                 // this lane reads 4 elements of value row 4 half + (l % 16) / 4 of 8
                 const int v_row = 4 * half + (lane >> 2 & 3);

@@ -1,0 +1,82 @@
+"""GPU tests of the scales of caches in 8 bits that attention reads: those of places that are not
+seen, of no and of other signs than the usual one, and of all magnitudes.
+
+Tolerances are those of test_gpu_layer: a rounding to a type is off by at most half a step, a chain
+of n 32-bit operations by n 2^-24 times the sum of the terms' magnitudes."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import bmmc_affine_index_amd as bm  # noqa: E402
+from test_gpu_layer import DEV, F8, NAN, TYPES, U32, Case, _gen, _least, _u, _within  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def _seen(c):
+    """The places that some token sees, as [pages, places]."""
+    seen = torch.zeros(c.k.shape[:2], dtype=torch.bool)
+    for s, n in enumerate(c.new):
+        first = max(0, c.lengths[s] - n - c.window + 1) if c.window else 0
+        at = torch.arange(first, c.lengths[s]) if n else torch.arange(0)
+        seen[c.table[s, at // c.page].long(), at % c.page] = True
+    return seen
+
+
+def _attend(c, k_scale, v_scale, k=None, v=None, scale=None):
+    args, named = c.args()
+    named.update(k_scale=c.on(k_scale), v_scale=c.on(v_scale))
+    return bm.cache_attention(args[0], args[1] if k is None else c.on(k), args[2] if v is None else c.on(v),
+                              *args[3:], scale=scale, **named)
+
+
+# new, lengths, window: few rows in shares, many rows a sequence, and both with a window's begin
+# inside a tile of keys
+ROWS = [([1, 1], [300, 17], 100), ([3, 1], [200, 90], 33), ([30, 1], [150, 300], 0), ([130, 70], [400, 75], 77),
+        ([130], [290], 0)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("what", [NAN, math.inf, -math.inf])
+@pytest.mark.parametrize("case", ROWS, ids=str)
+def test_scales_of_places_that_nobody_sees(case, what, dtype):
+    """Pages of nobody, places behind a sequence's end and in front of a window: their scales, as
+    their keys and values, may be anything."""
+    new, lengths, window = case
+    c = Case(new, lengths, 16, 6, 2, 64, 80, dtype, "row", window=window)
+    want, slack = c.want(64 ** -0.5)
+    seen = _seen(c)[..., None]
+    scales = [torch.where(seen, s, what) for s in c.scales]
+    _within(_attend(c, *scales), want, slack, dtype)
+    k, v = (torch.where(seen[..., None], x.float(), NAN).to(F8) for x in (c.k, c.v))
+    _within(_attend(c, *scales, k=k, v=v), want, slack, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", [(4, 2, 64, 64, 3), (8, 2, 96, 72, 30), (4, 2, 128, 104, 150), (4, 2, 256, 200, 80)], ids=str)
+def test_a_scale_that_is_none_reaches_only_those_that_see_it(shape, dtype):
+    """A NaN or an infinity for a scale in the middle of a chunk shows in the rows that see its place
+    and in no other, also where another value is a NaN."""
+    q_heads, heads, dim, v_dim, n = shape
+    group, length, page = q_heads // heads, 2 * n + 50, 16
+    for window in (0, n // 2 + 1):
+        c = Case([n], [length], page, q_heads, heads, dim, v_dim, dtype, "row", window=window, seed=3)
+        want, slack = c.want(dim ** -0.5)
+        place = torch.arange(length - n, length)
+        for back, what, which in ((0, NAN, 1), (n // 2, math.inf, 1), (n + 3, -math.inf, 1), (n - 1, NAN, 0)):
+            for odd_value in (False, True):
+                at = length - 1 - back
+                home = int(c.table[0, at // page]), at % page
+                sees = (place >= at) & ((place < at + window) if window else True)
+                none = torch.zeros_like(want, dtype=torch.bool)
+                none[sees, :group] = True
+                scales, v = [s.clone() for s in c.scales], c.v.float()
+                scales[which][home][0] = what
+                if odd_value:  # of the last token's place, which only that token sees
+                    v[int(c.table[0, (length - 1) // page]), (length - 1) % page, 1, 5] = NAN
+                    none[n - 1, group:, 5] = True
+                got = _attend(c, *scales, v=v.to(F8)).cpu()
+                assert torch.equal(~got.isfinite(), none)
+                _within(torch.where(none, 0, got), torch.where(none, 0, want), slack, dtype)
