@@ -130,10 +130,16 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
         stop = tile.first + tile.units;
     }
     const bool scaled = kNarrow && x.rows_scaled;
-    float c = x.a.scale * 1.4426950408889634f, by_value = 1.0f;
+    // A head's scale of the keys goes into c, by which scores are multiplied behind the
+    // mask and the maximum, where that leaves c above 0 and finite; other scales (0,
+    // below 0, lost in 32 bits) are multiplied to the scores before those.
+    float c = x.a.scale * 1.4426950408889634f, by_key = 1.0f, by_value = 1.0f;
+    bool key_apart = false;
     if (kNarrow && !scaled && x.a.pages) {  // without pages there may be no scales
-        c *= x.k.scale[head * x.k.scale_head];
+        by_key = x.k.scale[head * x.k.scale_head];
         by_value = x.v.scale[head * x.v.scale_head];
+        key_apart = !(c * by_key > 0.0f && c * by_key < __builtin_inff());
+        if (!key_apart) c *= by_key;
     }
     // threads 0 to 63 look after the rows of a tile's keys, 64 to 127 of its values
     const int of_values = tid >> 6 & 1, key_row = tid & 63;
@@ -327,6 +333,11 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                             for (int j = 0; j < 4; ++j) s[b][i + j] *= by[j];
                         }
                 }
+                if (kNarrow && key_apart)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) s[b][i] *= by_key;
                 const uint64_t there = uniform(lds.seen[which]);
                 const bool parted = t + kKeys - 1 > wave_first ||
                                     (x.a.window && t <= wave_last - x.a.window);

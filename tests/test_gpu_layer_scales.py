@@ -80,3 +80,31 @@ def test_a_scale_that_is_none_reaches_only_those_that_see_it(shape, dtype):
                 got = _attend(c, *scales, v=v.to(F8)).cpu()
                 assert torch.equal(~got.isfinite(), none)
                 _within(torch.where(none, 0, got), torch.where(none, 0, want), slack, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("narrow", ["one", "head", "row"])
+@pytest.mark.parametrize("case", ROWS, ids=str)
+def test_scales_of_no_and_of_both_signs(case, narrow, dtype):
+    """Scales of 0 and below are scales as others are, for one token and for many."""
+    new, lengths, window = case
+    for signs in ([0.0, 1.0, -1.0], [-1.0, 0.0, 0.0], [0.0, 0.0, 0.0]):
+        c = Case(new, lengths, 16, 6, 3, 64, 80, dtype, narrow, window=window)
+        k, v = c.scales
+        by = torch.tensor(signs if narrow == "head" else signs[0])
+        if narrow == "row":
+            by = torch.tensor(signs)[torch.randint(0, 3, k.shape, generator=_gen(1))]
+        c.scales = k * by, v * by.flip(-1) if by.dim() else v * by
+        c.check()
+        c.scales = k * by, v
+        c.check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("case", ROWS, ids=str)
+def test_keys_scales_whose_product_with_the_scale_is_none(case, dtype):
+    """A head's scale that is lost in 32 bits when multiplied by the scores' scale."""
+    new, lengths, window = case
+    c = Case(new, lengths, 16, 6, 2, 64, 80, dtype, "head", window=window)
+    c.scales = torch.tensor([2.0 ** -120, 0.02]), c.scales[1]
+    c.check(scale=2.0 ** -40)
