@@ -358,12 +358,12 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int key = b * 16 + g * 4 + i;
-                        mine.p[key][n] = see >> key & 1u ? p[b * 4 + i] : -1.0f;
+                        mine.p[key][n] = p[b * 4 + i];
                     }
                 wave_fence();
                 for (int key = 0; key < KT; ++key) {
+                    if (!(see >> key & 1u)) continue;  // this lane's row, as the weights'
                     const float w = mine.p[key][n];
-                    if (w == -1.0f) continue;
                     const int dim = kept(x.a.v_dim);
                     const E *in = reinterpret_cast<const E *>(mine.at[which][1][key]);
 #pragma unroll

@@ -108,3 +108,22 @@ def test_keys_scales_whose_product_with_the_scale_is_none(case, dtype):
     c = Case(new, lengths, 16, 6, 2, 64, 80, dtype, "head", window=window)
     c.scales = torch.tensor([2.0 ** -120, 0.02]), c.scales[1]
     c.check(scale=2.0 ** -40)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [-1.0, -2.0 ** -7, 1.0])
+def test_weights_that_a_scale_makes_minus_one(dtype, scale):
+    """Equal weights times a scale below 0, beside a value that is no number and that only the last
+    token sees: no key is left out."""
+    n, length, page = 3, 60, 16
+    c = Case([n], [length], page, 2, 1, 64, 64, dtype, "row")
+    c.k = torch.where(c.k.float().isnan(), c.k.float(), 0.0).to(F8)
+    c.scales = c.scales[0], torch.full_like(c.scales[1], scale)
+    want, slack = c.want(0.125)
+    v = c.v.float()
+    v[int(c.table[0, (length - 1) // page]), (length - 1) % page, 0, 7] = NAN
+    got = _attend(c, *c.scales, v=v.to(F8)).cpu()
+    none = torch.zeros_like(want, dtype=torch.bool)
+    none[n - 1, :, 7] = True
+    assert torch.equal(~got.isfinite(), none)
+    _within(torch.where(none, 0, got), torch.where(none, 0, want), slack, dtype)
