@@ -444,9 +444,27 @@ __device__ __forceinline__ f4 mfma16(Product<float>::vec a, Product<float>::vec 
 // was read before it was written; this waits for all of them.
 __device__ __forceinline__ void wait_for(f4 &x) { asm volatile("s_nop 15" : "+v"(x)); }
 
-// Weights are made as 2^(score - maximum + kLift).  In 16 bits of 5 exponent bits
-// small ones would be lost below 2^-25 of the largest; lifted, below 2^-32.
-template <typename T> constexpr float kLift = __is_same(T, f16_t) ? 7.0f : 0.0f;
+// What weights and values are in their product: the inputs' type, but bfloat16 for
+// float16 inputs whose values have a scale for each row (ROWS).  There a weight is
+// multiplied by its value's scale, and 5 exponent bits do not hold both: a row of zeros
+// has the scale 1, one of small values 2^-20, and either may weigh 2^-14 of the other.
+// So that no bits are lost for the exponent's, the weight goes into two products, as its
+// rounding and as the rounding of what that leaves out, which is 2^-16 of it at most
+// (float16: 2^-11).  e4m3's values are all values of both types.  One product and two:
+// 4096 tokens over 4 x 2048 places, 16 over 4 heads of 128, 154 us (bfloat16) and 181;
+// one token of 128 sequences of up to 4096, 24 over 4 heads of 96, 67.0 us and 67.7.
+template <typename T, bool ROWS> struct Weighed {
+    typedef T type;
+    static constexpr bool kTwo = false;
+};
+template <> struct Weighed<f16_t, true> {
+    typedef bf16_t type;
+    static constexpr bool kTwo = true;
+};
+
+// Weights of type W are made as 2^(score - maximum + kLift).  In 16 bits of 5 exponent
+// bits small ones would be lost below 2^-25 of the largest; lifted, below 2^-32.
+template <typename W> constexpr float kLift = __is_same(W, f16_t) ? 7.0f : 0.0f;
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 

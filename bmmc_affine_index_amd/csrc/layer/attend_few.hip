@@ -82,13 +82,17 @@ template <typename T, typename E, int DP, int KB, bool AHEAD> struct Few {
     static constexpr size_t kLds = sizeof(Main) > sizeof(Joined) ? sizeof(Main) : sizeof(Joined);
 };
 
-template <typename T, typename E, int DP, int KB, bool AHEAD>
+// ROWS: 8-bit values have a scale for each row.
+template <typename T, typename E, int DP, int KB, bool AHEAD, bool ROWS>
 __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
     bmmc_attend_few_kernel(const AttendArgs x, int64_t block0) {
     using F = Few<T, E, DP, KB, AHEAD>;
     constexpr int CE = F::CE, NK = F::NK, VE = F::VE, VG = F::VG, KT = F::KT, VK = F::VK, KG = F::KG;
     constexpr bool kNarrow = sizeof(E) == 1;
     typedef typename Product<T>::vec vec_t;
+    typedef typename Weighed<T, ROWS>::type W;
+    typedef typename Product<W>::vec weights_t;
+    constexpr bool kTwo = Weighed<T, ROWS>::kTwo;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     typename F::Main &main_lds = *reinterpret_cast<typename F::Main *>(lds);
     typename F::Joined &joined = *reinterpret_cast<typename F::Joined *>(lds);
@@ -135,8 +139,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
         const int64_t by_page = half ? x.v.page_stride : x.k.page_stride;
         const int64_t by_place = half ? x.v.place_stride : x.k.place_stride;
         const int64_t by_head = (half ? x.v.head_stride : x.k.head_stride) * head;
-        const bool scaled = kNarrow && x.rows_scaled;
-        const auto look = [&](int32_t t) { return entry_of(x, table, t + kl, span.to); };
+            const auto look = [&](int32_t t) { return entry_of(x, table, t + kl, span.to); };
         float scale_next = 0.0f;
         // Rows of the tile at t into LDS; bits of the keys that are there
         const auto put = [&](int32_t entry, int32_t t, int which) {
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                 mine.at[which][half][kl] =
                     page < 0 ? reinterpret_cast<const uint8_t *>(kZeros)
                              : base + (page * by_page + in * by_place + by_head) * (int64_t)sizeof(E);
-            if (scaled) {
+            if (ROWS) {
                 const bmmc_scaled_cache &c = half ? x.v : x.k;
                 scale_next = page < 0 ? 0.0f
                                       : c.scale[page * c.scale_page + in * c.scale_place + head * c.scale_head];
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
         };
 
         float c = x.a.scale * 1.4426950408889634f, by_value = 1.0f;
-        if (kNarrow && !scaled && x.a.pages) {  // without pages there may be no scales
+        if (kNarrow && !ROWS && x.a.pages) {  // without pages there may be no scales
             c *= x.k.scale[head * x.k.scale_head];
             by_value = x.v.scale[head * x.v.scale_head];
         }
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                 }
                 wait_for(s[b]);
             }
-            if (scaled) {
+            if (ROWS) {
                 if (kl < KT) mine.scale[half][kl] = scale_next;
                 wave_fence();
             }
@@ -288,7 +291,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 f4 by{c, c, c, c};
-                if (scaled) by *= *reinterpret_cast<const f4 *>(&mine.scale[0][b * 16 + g * 4]);
+                if (ROWS) by *= *reinterpret_cast<const f4 *>(&mine.scale[0][b * 16 + g * 4]);
                 s[b] *= by;
             }
             // the tile has keys that are not there, or that some rows do not see
@@ -320,21 +323,21 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                     for (int e = 0; e < VE; ++e) o[v][e] *= down;
                 m = m_new;
             }
-            const float base = settled(m) - kLift<T>;
+            const float base = settled(m) - kLift<W>;
             float p[VK];
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 f4 by{1.0f, 1.0f, 1.0f, 1.0f};
-                if (scaled) by = *reinterpret_cast<const f4 *>(&mine.scale[1][b * 16 + g * 4]);
+                if (ROWS) by = *reinterpret_cast<const f4 *>(&mine.scale[1][b * 16 + g * 4]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float w = exp2_of(s[b][i] - base);
                     l += w;
-                    p[b * 4 + i] = scaled ? w * by[i] : w;
+                    p[b * 4 + i] = ROWS ? w * by[i] : w;
                 }
             }
             // a weight of 0 times a scale that is no number would reach rows that do not see its key
-            if (scaled && parted)
+            if (ROWS && parted)
 #pragma unroll
                 for (int j = 0; j < VK; ++j)
                     if (!(see >> 4 * g & 1u << (j / 4 * 16 + j % 4))) p[j] = 0.0f;
@@ -378,10 +381,13 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                 }
                 wave_fence();
             } else {
-                vec_t pv;
+                weights_t pv, rest;  // rounded once here, and what that leaves out
                 if constexpr (sizeof(T) == 2)
 #pragma unroll
-                    for (int j = 0; j < VK; ++j) pv[j] = (T)p[j];
+                    for (int j = 0; j < VK; ++j) pv[j] = (W)p[j];
+                if constexpr (kTwo)
+#pragma unroll
+                    for (int j = 0; j < VK; ++j) rest[j] = (W)(p[j] - (float)pv[j]);
 #pragma unroll
                 for (int v = 0; v < VG; ++v) {
                     constexpr int kWords = VE * (int)sizeof(T) / 4;
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                     }
                     uint32_t w[VK][kWords];
 #pragma unroll
-                    for (int j = 0; j < VK; ++j) expand<T>(vr[j][at], w[j]);
+                    for (int j = 0; j < VK; ++j) expand<W>(vr[j][at], w[j]);
 #pragma unroll
                     for (int e = 0; e < VE; ++e) {
                         if constexpr (sizeof(T) == 4) {
@@ -410,9 +416,10 @@ __global__ void __launch_bounds__(64 * kFewWaves, (DP <= 128 ? 2 : 1))
                             for (int j = 0; j < 4; ++j)
                                 keys[j] = __builtin_amdgcn_perm(w[2 * j + 1][e / 2], w[2 * j][e / 2],
                                                                 e & 1 ? 0x07060302u : 0x05040100u);
-                            vec_t a;
+                            weights_t a;
                             __builtin_memcpy(&a, keys, 16);
                             o[v][e] = mfma16(a, pv, o[v][e]);
+                            if constexpr (kTwo) o[v][e] = mfma16(a, rest, o[v][e]);
                         }
                     }
                 }
@@ -586,7 +593,9 @@ __global__ void __launch_bounds__(256) bmmc_attend_join_kernel(const AttendArgs 
 template <typename T, typename E, int DP, int KB, bool AHEAD>
 int few(const AttendArgs &x, hipStream_t s) {
     using F = Few<T, E, DP, KB, AHEAD>;
-    const auto kernel = bmmc_attend_few_kernel<T, E, DP, KB, AHEAD>;
+    const bool rows = sizeof(E) == 1 && x.rows_scaled;
+    const auto kernel = rows ? bmmc_attend_few_kernel<T, E, DP, KB, AHEAD, sizeof(E) == 1>
+                             : bmmc_attend_few_kernel<T, E, DP, KB, AHEAD, false>;
     const int64_t blocks = (x.plan.shares ? x.plan.shares : x.plan.tiles) * x.a.heads +
                            (x.a.clear_rest && x.a.starts ? kClearBlocks : 0);
     return in_launches(blocks, 64 * kFewWaves, [&](uint32_t nb, int64_t b0) {

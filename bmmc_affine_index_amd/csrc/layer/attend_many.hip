@@ -38,17 +38,17 @@ __device__ __forceinline__ f16x mfma32(Product<bf16_t>::vec a, Product<bf16_t>::
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// The order of a block's N products and EACH reads from LDS for each of them: reads
-// for AHEAD products come first, so that no product waits for its own.
-template <int N, int EACH, int AHEAD> __device__ __forceinline__ void reads_ahead() {
+// The order of a block's N times PRODUCTS products and EACH reads from LDS for each of
+// the N: reads for AHEAD of them come first, so that no product waits for its own.
+template <int N, int EACH, int AHEAD, int PRODUCTS = 1> __device__ __forceinline__ void reads_ahead() {
     constexpr int kProduct = 0x8, kRead = 0x100;
     __builtin_amdgcn_sched_group_barrier(kRead, EACH * AHEAD, 0);
 #pragma unroll
     for (int i = 0; i < N - AHEAD; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kProduct, PRODUCTS, 0);
         __builtin_amdgcn_sched_group_barrier(kRead, EACH, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(kProduct, AHEAD, 0);
+    __builtin_amdgcn_sched_group_barrier(kProduct, PRODUCTS * AHEAD, 0);
 }
 
 // DP: the heads' elements, padded.
@@ -94,13 +94,17 @@ __device__ __forceinline__ void wait_for_copies() {
     __builtin_amdgcn_s_waitcnt(0x0f70);  // every load of this wave, no other wait
 }
 
-template <typename T, typename E, int DP, bool DIRECT>
+// ROWS: 8-bit values have a scale for each row.
+template <typename T, typename E, int DP, bool DIRECT, bool ROWS>
 __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
     bmmc_attend_many_kernel(const AttendArgs x, int64_t block0) {
     using M = Many<T, DP>;
     constexpr int CR = M::CR, NC = M::NC, KS = DP / 16, DB = DP / 32;
     constexpr bool kNarrow = sizeof(E) == 1;
     typedef typename Product<T>::vec vec_t;
+    typedef typename Weighed<T, ROWS>::type W;
+    typedef typename Product<W>::vec weights_t;
+    constexpr bool kTwo = Weighed<T, ROWS>::kTwo;
     extern __shared__ __attribute__((aligned(256))) uint8_t lds_bytes[];
     typename M::Lds &lds = *reinterpret_cast<typename M::Lds *>(lds_bytes);
 
@@ -129,21 +133,20 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
         unit = tile.first;
         stop = tile.first + tile.units;
     }
-    const bool scaled = kNarrow && x.rows_scaled;
     // A head's scale of the keys goes into c, by which scores are multiplied behind the
     // mask and the maximum, where that leaves c above 0 and finite; other scales (0,
     // below 0, lost in 32 bits) are multiplied to the scores before those.
     float c = x.a.scale * 1.4426950408889634f, by_key = 1.0f, by_value = 1.0f;
     bool key_apart = false;
-    if (kNarrow && !scaled && x.a.pages) {  // without pages there may be no scales
+    if (kNarrow && !ROWS && x.a.pages) {  // without pages there may be no scales
         by_key = x.k.scale[head * x.k.scale_head];
         by_value = x.v.scale[head * x.v.scale_head];
         key_apart = !(c * by_key > 0.0f && c * by_key < __builtin_inff());
         if (!key_apart) c *= by_key;
     }
     // threads 0 to 63 look after the rows of a tile's keys, 64 to 127 of its values
-    const int of_values = tid >> 6 & 1, key_row = tid & 63;
-    const bool looks = tid < 128;
+    const int of_values = wave & 1, key_row = lane;  // the same in a wave: their strides are scalars
+    const bool looks = wave < 2;
     const uint8_t *base = static_cast<const uint8_t *>(of_values ? x.v.data : x.k.data);
     const int64_t by_page = of_values ? x.v.page_stride : x.k.page_stride;
     const int64_t by_place = of_values ? x.v.place_stride : x.k.place_stride;
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                 lds.seen[which] = seen;
                 lds.odd[which] = 0;
             }
-            if (scaled) {
+            if (ROWS) {
                 const bmmc_scaled_cache &cache = of_values ? x.v : x.k;
                 scale_next = page < 0 ? 0.0f
                                       : cache.scale[page * cache.scale_page + in * cache.scale_place +
@@ -238,11 +241,11 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
         };
         const auto store = [&](int32_t t, int which) {
             const bool parted = parted_at(t);
-            if (scaled && looks) lds.scale[which][of_values][key_row] = scale_next;
+            if (ROWS && looks) lds.scale[which][of_values][key_row] = scale_next;
             const auto put_aside = [&](int r, uint32_t (&w)[4]) {
                 bool odd = false;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) odd |= drop_nonfinite<T>(w[j]);
+                for (int j = 0; j < 4; ++j) odd |= drop_nonfinite<W>(w[j]);
                 if (odd) atomicOr(reinterpret_cast<unsigned long long *>(&lds.odd[which]), 1ull << r);
                 return odd;
             };
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                     if (v_dim & 7) settle(vr[i], my_c * 8, v_dim);
                     uint32_t kw[4], vw[4];
                     expand<T>(kr[i], kw);
-                    expand<T>(vr[i], vw);
+                    expand<W>(vr[i], vw);
                     if (parted) put_aside(r, vw);
                     *reinterpret_cast<u4 *>(lds.k[which] + r * M::kRowBytes + M::key_at(r, my_c) * 16) =
                         u4{kw[0], kw[1], kw[2], kw[3]};
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                 reads_ahead<2 * KS, 1, 6>();
 #pragma unroll
                 for (int b = 0; b < 2; ++b) asm volatile("s_nop 15" : "+v"(s[b]));
-                if (scaled) {
+                if (ROWS) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                             for (int j = 0; j < 4; ++j) s[b][i + j] *= by[j];
                         }
                 }
-                if (kNarrow && key_apart)
+                if (kNarrow && !ROWS && key_apart)
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -357,11 +360,9 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
                 top = over_32(top, Largest()) * c;
-                // Weights may grow to 2^8 before the sums are brought down to a new
-                // maximum, which both types hold; not where 16 bits of 5 exponent bits
-                // hold a weight times its value's scale, so that scales up to 500 fit
-                const float room = scaled && __is_same(T, f16_t) ? 0.0f : 8.0f;
-                if (__any(top > m + room)) {
+                // weights may grow to 2^8 before the sums are brought down to a new
+                // maximum, which both types hold
+                if (__any(top > m + 8.0f)) {
                     const float m_new = fmaxf(m, top);
                     const float down = exp2_of(m - settled(m_new));
                     l *= down;
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                     for (int d = 0; d < DB; ++d) o[d] *= down;
                     m = m_new;
                 }
-                const float minus = kLift<T> - settled(m);
+                const float minus = kLift<W> - settled(m);
                 float sum[4] = {};
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                         sum[i & 3] += s[b][i];
                     }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                if (scaled) {
+                if (ROWS) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -395,11 +396,15 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                 // this lane reads 4 elements of value row 4 half + (l % 16) / 4 of 8
                 const int v_row = 4 * half + (lane >> 2 & 3);
                 const uint8_t *values = lds.v[which] + v_row * M::kRowBytes + (lane & 1) * 8;
-                vec_t p[4];  // of 16 keys each
+                weights_t p[4], rest[kTwo ? 4 : 1];  // of 16 keys each
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) p[k][j] = (T)s[k / 2][k % 2 * 8 + j];
+                    for (int j = 0; j < 8; ++j) {
+                        const float w = s[k / 2][k % 2 * 8 + j];
+                        p[k][j] = (W)w;
+                        if constexpr (kTwo) rest[k][j] = (W)(w - (float)p[k][j]);
+                    }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -413,11 +418,12 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
                         s4 v4[2];
                         v4[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)at);
                         v4[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(at + 8 * M::kRowBytes));
-                        vec_t a;
+                        weights_t a;
                         __builtin_memcpy(&a, v4, 16);
                         o[d] = mfma32(a, p[k], o[d]);
+                        if constexpr (kTwo) o[d] = mfma32(a, rest[k], o[d]);
                     }
-                reads_ahead<4 * DB, 2, 4>();
+                reads_ahead<4 * DB, 2, 4, kTwo ? 2 : 1>();
                 // values put aside for any wave, to the rows that see them
                 uint64_t odd = parted_at(t) ? uniform(lds.odd[which]) : 0;
                 while (odd) {
@@ -496,9 +502,12 @@ __global__ void __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1)
 template <typename T, typename E, int DP, bool DIRECT> int many(const AttendArgs &x, hipStream_t s) {
     const int64_t blocks = (x.plan.shares ? x.plan.shares : x.plan.tiles) * x.a.heads +
                            (x.a.clear_rest && x.a.starts ? kClearBlocks : 0);
+    const bool rows = sizeof(E) == 1 && x.rows_scaled;
+    const auto kernel = rows ? bmmc_attend_many_kernel<T, E, DP, DIRECT, sizeof(E) == 1>
+                             : bmmc_attend_many_kernel<T, E, DP, DIRECT, false>;
     return in_launches(blocks, kManyThreads, [&](uint32_t nb, int64_t b0) {
-        hipLaunchKernelGGL((bmmc_attend_many_kernel<T, E, DP, DIRECT>), dim3(nb), dim3(kManyThreads),
-                           sizeof(typename Many<T, DP>::Lds), s, x, b0);
+        hipLaunchKernelGGL(kernel, dim3(nb), dim3(kManyThreads), sizeof(typename Many<T, DP>::Lds), s, x,
+                           b0);
     });
 }
 

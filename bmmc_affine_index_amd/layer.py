@@ -100,11 +100,12 @@ def cache_attention(q, k_cache, v_cache, page_table, lengths, starts=None, k_sca
 
     float8_e4m3fn caches have k_scale and v_scale, float32: one value, one for
     each head, or [pages, places, H], one for each row, as cache_quantize
-    makes.  With float16 and scales for each row, a weight times v_scale
-    past 500 is an infinity.  Rows of q that belong to no sequence give zeros in
-    a new tensor and leave a given `out` as it is.  Scores and sums are in 32
-    bits; weights are rounded to q's type before they meet the values.  There
-    is no gradient."""
+    makes.  Scales may be any numbers; what a row does not see has none.  Rows
+    of q that belong to no sequence give zeros in a new tensor and leave a given
+    `out` as it is.  Scores and sums are in 32 bits; weights, times v_scale
+    where that is one for each row, are rounded to q's type before they meet the
+    values, and so that 2^-16 of one is left out at most where q is float16 and
+    v_scale is one for each row.  There is no gradient."""
     return _run(_calls().attention, (q, k_cache, v_cache, page_table, lengths, starts, k_scale,
                                      v_scale, scale, window, out), stream)[0]
 

@@ -60,7 +60,9 @@ typedef struct bmmc_scaled_cache {
  * whatever its weight: an infinity or a NaN in its value shows.
  *
  * Scores, sums and the running maximum are in 32 bits; the weights of one
- * product with values are rounded to `type`.  Rows of no sequence are left as
+ * product with values, times their scales where those differ by place, are
+ * rounded to `type`, or where that is BMMC_F16 and scales differ by place so that
+ * 2^-16 of one is left out at most.  Rows of no sequence are left as
  * they are or, with clear_rest, those before the first and behind the last
  * sequence set to zeros.  starts must not fall; where it does, rows of some
  * sequences are not written. */

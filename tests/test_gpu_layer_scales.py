@@ -127,3 +127,64 @@ def test_weights_that_a_scale_makes_minus_one(dtype, scale):
     none[n - 1, :, 7] = True
     assert torch.equal(~got.isfinite(), none)
     _within(torch.where(none, 0, got), torch.where(none, 0, want), slack, dtype)
+
+
+def _without_loss(c, scale):
+    """c.want, its slack without what weights of 5 exponent bits may lose: the weights' half step, twice
+    the scores' worst, and both sums."""
+    want, _ = c.want(scale)
+    slack = torch.zeros_like(want)
+    for s, n in enumerate(c.new):
+        (k, there), (v, _) = c.rows(s, 0), c.rows(s, 1)
+        length = c.lengths[s]
+        see = (torch.arange(length) <= length - n + torch.arange(n)[:, None]) & there
+        rows = slice(int(c.starts[s]), int(c.starts[s + 1]))
+        x = c.q[rows].double()
+        for h in range(x.shape[1]):
+            kh, vh = k[:, h // c.group], v[:, h // c.group]
+            a = (scale * (x[:, h] @ kh.t())).masked_fill(~see, -math.inf)
+            off = scale * (x.shape[2] + 16) * U32 * (x[:, h].abs() @ kh.abs().t()) + 4 * U32
+            worst = off.masked_fill(~see, 0.0).amax(1, keepdim=True)
+            slack[rows, h] = torch.softmax(a, dim=1) @ vh.abs() * (
+                _u(c.dtype) + 2 * worst + 2 * (length + 16) * U32) * 1.01
+    return want, slack
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new,length", [(1, 700), (3, 300), (130, 400)])
+@pytest.mark.parametrize("low,high", [(-24, 10), (-24, -20), (5, 10), (-60, -30)])
+def test_scales_of_values_of_all_magnitudes(low, high, new, length, dtype):
+    """Row scales between two powers of two: what a weight times its scale is does not matter."""
+    c = Case([new], [length], 16, 4, 2, 64, 72, dtype, "row")
+    c.v = (c.v.float() / 64).to(F8)
+    g = _gen(high)
+    by = 2.0 ** (low + (high - low) * torch.rand(c.scales[1].shape, generator=g))
+    c.scales = c.scales[0], by.float()
+    want, slack = _without_loss(c, 0.125)
+    _within(_attend(c, *c.scales), want, slack, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new", [1, 130])
+@pytest.mark.parametrize("most,first", [(1e-3, 1.0), (1e-3, 1e-3 / 448), (1e-2, 1.0), (1e-1, 1e-4)])
+def test_small_values_behind_a_row_of_zeros(most, first, new, dtype):
+    """One key of weight 1 whose values are zeros, with the scale 1 as a row of zeros is stored or
+    another, and thousands of 2^-14 of its weight, of small values."""
+    length, page = 8192, 64
+    c = Case([new], [length], page, 4, 1, 64, 64, dtype, "row", seed=2)
+    at = torch.arange(length)
+    page_of, place = c.table[0, at // page].long(), at % page
+    k, v = torch.zeros(*c.k.shape), torch.zeros(*c.v.shape)
+    k[page_of, place, 0, 0] = -448.0
+    k[page_of[0], place[0], 0, 0] = 0.0
+    v[page_of, place, 0] = 448.0 * (0.5 + 0.5 * torch.rand(length, 64, generator=_gen(1)))
+    v[page_of[0], place[0]] = 0.0
+    c.k, c.v = k.to(F8), v.to(F8)
+    c.q = torch.zeros_like(c.q)
+    c.q[..., 0] = 1.0
+    scales = torch.full_like(c.scales[1], most / 448)
+    scales[page_of[0], place[0]] = first
+    c.scales = torch.full_like(scales, 14 * math.log(2.0) / 448), scales
+    want, slack = _without_loss(c, 1.0)
+    assert float(want[-1].abs().max()) > 0.1 * most
+    _within(_attend(c, *c.scales, scale=1.0), want, slack, dtype)
