@@ -77,6 +77,27 @@ int check_places(int64_t tokens, const int32_t *sequences, const void *positions
     return BMMC_OK;
 }
 
+// Numbers that a call reads besides rows: `rows` times `bytes` bytes, `stride` bytes apart.
+struct Numbers {
+    const void *at;
+    int64_t bytes, rows, stride;
+};
+
+Numbers flat(const void *p, int64_t bytes) { return Numbers{p, p ? bytes : 0, 1, 0}; }
+
+Numbers table_of(const int32_t *table, int64_t batch, int64_t width, int64_t stride) {
+    return Numbers{table, 4 * width, batch, 4 * stride};
+}
+
+// Whether a written array, of extent e, has a byte of what is read.
+bool overwrites(const void *p, const Extent &e, const Steps &steps, int element, const Numbers &r) {
+    if (r.bytes <= 0 || !meet(e, extent(r.at, 1, r.bytes, &r.rows, &r.stride, 1))) return false;
+    Steps in_bytes = steps;
+    in_bytes.inner *= element;
+    for (int i = 0; i < steps.dims; ++i) in_bytes.strides[i] *= element;
+    return share(p, in_bytes, r.at, Steps(r.bytes, &r.rows, &r.stride, 1), 1);
+}
+
 bool dim_ok(int dim, int least) { return dim >= least && dim <= BMMC_MAX_HEAD_DIM; }
 
 // Sizes of an attention alone, without what its pointers point to.
@@ -141,6 +162,11 @@ int bmmc_cache_attention(const bmmc_attention *a, const bmmc_scaled_cache *k_cac
     if (meet(out, work)) return BMMC_ERR_ALIAS;
     for (const Extent &e : {q, ke.data, ke.scale, ve.data, ve.scale})
         if (meet(out, e) || meet(work, e)) return BMMC_ERR_ALIAS;
+    for (const Numbers &r : {table_of(a->table, a->batch, a->table_width, a->table_stride),
+                             flat(a->lengths, 4 * a->batch), flat(a->starts, 4 * (a->batch + 1))})
+        if (overwrites(a->out, out, Steps(a->v_dim, sizes, os, 2), bytes, r) ||
+            overwrites(workspace, work, Steps(need, nullptr, nullptr, 0), 1, r))
+            return BMMC_ERR_ALIAS;
     AttendArgs x{};
     x.a = *a;
     x.k = *k_cache;

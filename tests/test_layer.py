@@ -174,6 +174,31 @@ def test_attention_refuses_caches(host, k, v, status):
     assert host.bmmc_cache_attention(a, _cache(**k), _cache(**v), 1 << 40, need, None) == status
 
 
+def test_attention_does_not_write_its_indexes(host):
+    """The result and the workspace share no byte with the table, the lengths or the starts, which may
+    lie between the result's heads."""
+    a = _attention()
+    need = host.bmmc_cache_attention_workspace(a)
+    k, v = _cache(D), _cache(E)
+    end = B + 10 * 8 * 64 * 2
+    for name, size in (("table", 3 * 20 * 4), ("lengths", 3 * 4), ("starts", 4 * 4)):
+        for at, status in ((B, ALIAS), (B - size + 4, ALIAS), (B - size, ACCEPTED), (end - 4, ALIAS), (end, ACCEPTED)):
+            assert host.bmmc_cache_attention(_attention(**{name: at}), k, v, 1 << 40, need, None) == status, (name, at)
+        for at, status in (((1 << 40) - size, ACCEPTED), ((1 << 40) - size + 4, ALIAS), ((1 << 40) + need - 4, ALIAS),
+                           ((1 << 40) + need, ACCEPTED)):
+            assert host.bmmc_cache_attention(_attention(**{name: at}), k, v, 1 << 40, need, None) == status, (name, at)
+    # 16 bytes of lengths and starts in the 64 that follow each head, and a table's rows
+    for name, inside in (("lengths", 12), ("starts", 16)):
+        between = dict(out_head=64 + 32, out_token=8 * 96, **{name: B + 96 * 2 * 5 + 128})
+        assert host.bmmc_cache_attention(_attention(**between), k, v, 1 << 40, need, None) == ACCEPTED
+        between[name] += 64 - inside + 4
+        assert host.bmmc_cache_attention(_attention(**between), k, v, 1 << 40, need, None) == ALIAS
+    rows = dict(out_head=64 + 40, out_token=8 * 104, table_stride=104 // 2, table=B + 128)
+    assert host.bmmc_cache_attention(_attention(**rows), k, v, 1 << 40, need, None) == ACCEPTED
+    rows["table_width"] = 21
+    assert host.bmmc_cache_attention(_attention(**rows), k, v, 1 << 40, 1 << 30, None) == ALIAS
+
+
 def test_attention_workspace(host):
     a = _attention()
     need = host.bmmc_cache_attention_workspace(a)
