@@ -243,6 +243,24 @@ int bmmc_cache_quantize(const bmmc_heads *q, const bmmc_heads *k, const bmmc_hea
             share(q->out, out, v->in, steps_in(*v, 1, tokens, v_dim), bytes))
             return BMMC_ERR_ALIAS;
     }
+    const int64_t each = position_type == BMMC_I64 ? 8 : 4;
+    Numbers numbers[6] = {table_of(table, batch, table_width, table_stride), flat(sequences, 4 * tokens),
+                          flat(positions, each * tokens)};
+    if (rotation) {
+        const int64_t turn = rotation->position_type == BMMC_I64 ? 8 : 4;
+        numbers[3] = flat(rotation->freqs, rotation->pairs * (rotation->freqs_are_64 ? 8 : 4));
+        numbers[4] = flat(rotation->axis_of_pair, rotation->pairs * 4);
+        if (rotation->positions)
+            numbers[5] = Numbers{rotation->positions, turn * tokens, rotation->axes,
+                                 turn * rotation->axis_stride};
+    }
+    for (const Numbers &r : numbers)
+        if (overwrites(k_cache->data, kc.data, data_steps(*k_cache, pages, page_size, k->heads, k_dim), 1, r) ||
+            overwrites(v_cache->data, vc.data, data_steps(*v_cache, pages, page_size, k->heads, v_dim), 1, r) ||
+            overwrites(k_cache->scale, kc.scale, scale_steps(*k_cache, pages, page_size, k->heads), 4, r) ||
+            overwrites(v_cache->scale, vc.scale, scale_steps(*v_cache, pages, page_size, k->heads), 4, r) ||
+            (q && overwrites(q->out, qe.out, steps_out(*q, 1, tokens, k_dim), element_bytes(type), r)))
+            return BMMC_ERR_ALIAS;
     QuantizeArgs a{};
     if (q) a.q = *q;
     a.k = *k;

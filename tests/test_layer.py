@@ -274,6 +274,31 @@ def test_quantize_refusals(host):
     assert _quantize(host, rotation=many) == BAD  # two axes need positions of their own
 
 
+def test_quantize_does_not_write_its_numbers(host):
+    """The caches, their scales and the turned queries share no byte with the indexes, positions and
+    frequencies, which may lie between a cache's rows."""
+    p = 0x1000000
+    data, scales, rows = 100 * 16 * 2 * 64, 100 * 16 * 2 * 4, 10 * 512 * 2
+    written = {"k_cache": (C, data), "v_cache": (C + p, data), "k_scale": (D, scales), "v_scale": (D + p, scales),
+               "q": (A + p, rows)}
+    q = _heads(A, token=512, heads=8, out=A + p)
+
+    def turn(positions=None, freqs=A + 4 * p, axes=None):
+        return tk.bmmc_rotation(positions, freqs, axes, 10, tk.I64, 1, 2 if positions else 1, 32, 0, 0, 1.0)
+    reads = [("table", 240, lambda at: dict(table=at)), ("sequences", 40, lambda at: dict(sequences=at)),
+             ("positions", 80, lambda at: dict(positions=at)), ("turns", 160, lambda at: dict(rotation=turn(positions=at))),
+             ("freqs", 256, lambda at: dict(rotation=turn(freqs=at))), ("axes", 128, lambda at: dict(rotation=turn(axes=at)))]
+    for where, (start, size) in written.items():
+        for name, n, how in reads:
+            for at, status in ((start - n, ACCEPTED), (start - n + 8, ALIAS), (start + size // 2, ALIAS), (start + size - 8, ALIAS),
+                               (start + size, ACCEPTED)):
+                assert _quantize(host, **{"q": q, "rotation": turn(), **how(at)}) == status, (where, name, hex(at))
+    # pages of keys with 64 bytes behind each
+    kc = _narrow(C, D, page_stride=16 * 2 * 64 + 64)
+    assert _quantize(host, kc=kc, sequences=C + 2048) == ACCEPTED
+    assert _quantize(host, kc=kc, sequences=C + 2048 + 28) == ALIAS
+
+
 def _read(host, k=None, v=None, kc=None, vc=None, **changes):
     p = 0x1000000
     a = dict(k=k or _heads(None, out=B), v=v or _heads(None, out=B + p), k_cache=kc or _cache(C),
