@@ -319,6 +319,11 @@ int bmmc_cache_read(const bmmc_heads *k, const bmmc_heads *v, const bmmc_scaled_
         return BMMC_ERR_ALIAS;
     for (const Extent &c : {kc.data, kc.scale, vc.data, vc.scale})
         if (meet(c, ke.out) || meet(c, ve.out)) return BMMC_ERR_ALIAS;
+    for (const Numbers &r : {table_of(table, batch, table_width, table_stride), flat(sequences, 4 * tokens),
+                             flat(positions, (position_type == BMMC_I64 ? 8 : 4) * tokens)})
+        if (overwrites(k->out, ke.out, steps_out(*k, 1, tokens, k_dim), element_bytes(type), r) ||
+            overwrites(v->out, ve.out, steps_out(*v, 1, tokens, v_dim), element_bytes(type), r))
+            return BMMC_ERR_ALIAS;
     ReadArgs a{};
     a.k = *k;
     a.v = *v;

@@ -321,6 +321,18 @@ def test_read_refusals(host):
         assert _read(host, **how) == status, how
 
 
+def test_read_does_not_write_its_indexes(host):
+    """The two results share no byte with the table, the sequences or the positions, which may lie
+    between their heads."""
+    p = 0x1000000
+    size = 9 * 6 * 64 * 2 + 2 * 64 * 2
+    for start in (B, B + p):
+        for name, n in (("table", 240), ("sequences", 40), ("positions", 80)):
+            for at, status in ((start - n, ACCEPTED), (start - n + 8, ALIAS), (start, ALIAS), (start + size - 8, ALIAS),
+                               (start + size, ACCEPTED), (start + 256, ACCEPTED), (start + 248, ALIAS)):
+                assert _read(host, **{name: at}) == status, (name, hex(at))
+
+
 def test_balance_refusals(host):
     p = 0x1000000
     base = dict(logits=A, stride=64, type=tk.F32, e=64, experts=B, kind=tk.I64, tokens=100, choices=4, mask=C, loss=D,
