@@ -58,14 +58,21 @@ bool by_place(const bmmc_scaled_cache &c, int64_t pages, int64_t page_size) {
            ((pages > 1 && c.scale_page) || (page_size > 1 && c.scale_place));
 }
 
-// What the calls on a paged cache have in common.
+// What the calls on a paged cache have in common: sizes, and the table itself.
+bool page_sizes_ok(int64_t pages, int64_t page_size, int64_t batch, int64_t table_width,
+                   int64_t table_stride) {
+    return pages >= 0 && pages <= kMaxIndex && page_size >= 1 && page_size <= kMaxIndex && batch >= 0 &&
+           batch <= kMaxIndex && table_width >= 0 && table_width <= kMaxIndex && stride_ok(table_stride);
+}
+bool table_ok(const int32_t *table, int64_t batch, int64_t table_width) {
+    return aligned(table, 4) && (!batch || !table_width || table);
+}
 int check_pages(int64_t pages, int64_t page_size, const int32_t *table, int64_t batch,
                 int64_t table_width, int64_t table_stride) {
-    if (pages < 0 || pages > kMaxIndex || page_size < 1 || page_size > kMaxIndex || batch < 0 ||
-        batch > kMaxIndex || table_width < 0 || table_width > kMaxIndex ||
-        !stride_ok(table_stride) || !aligned(table, 4) || (batch && table_width && !table))
-        return BMMC_ERR_INVALID_ARG;
-    return BMMC_OK;
+    return page_sizes_ok(pages, page_size, batch, table_width, table_stride) &&
+                   table_ok(table, batch, table_width)
+               ? BMMC_OK
+               : BMMC_ERR_INVALID_ARG;
 }
 
 int check_places(int64_t tokens, const int32_t *sequences, const void *positions,
@@ -100,7 +107,7 @@ bool overwrites(const void *p, const Extent &e, const Steps &steps, int element,
 
 bool dim_ok(int dim, int least) { return dim >= least && dim <= BMMC_MAX_HEAD_DIM; }
 
-// Sizes of an attention alone, without what its pointers point to.
+// Sizes of an attention alone; of its pointers only whether there are starts.
 int check_attention_sizes(const bmmc_attention &a) {
     if (a.tokens < 0 || a.tokens > kMaxIndex || a.heads < 1 || a.q_heads < 1 ||
         a.q_heads > kMaxHeads || a.heads > a.q_heads || a.q_heads % a.heads ||
@@ -109,7 +116,9 @@ int check_attention_sizes(const bmmc_attention &a) {
         !(a.scale > 0.0f) || !std::isfinite(a.scale) || (!a.starts && a.batch != a.tokens))
         return BMMC_ERR_INVALID_ARG;
     if (a.tokens > kMaxIndex / (a.q_heads / a.heads)) return BMMC_ERR_INVALID_ARG;
-    return check_pages(a.pages, a.page_size, a.table, a.batch, a.table_width, a.table_stride);
+    return page_sizes_ok(a.pages, a.page_size, a.batch, a.table_width, a.table_stride)
+               ? BMMC_OK
+               : BMMC_ERR_INVALID_ARG;
 }
 
 int32_t pitch_of(const bmmc_attention &a) { return (a.v_dim + 3) / 4 * 4; }
@@ -139,7 +148,7 @@ int bmmc_cache_attention(const bmmc_attention *a, const bmmc_scaled_cache *k_cac
     int st = check_attention_sizes(*a);
     if (st != BMMC_OK) return st;
     const int64_t need = bmmc_cache_attention_workspace(a);
-    if (!stride_ok(a->q_token) || !stride_ok(a->q_head) || !stride_ok(a->out_token) ||
+    if (!table_ok(a->table, a->batch, a->table_width) || !stride_ok(a->q_token) || !stride_ok(a->q_head) || !stride_ok(a->out_token) ||
         !stride_ok(a->out_head) || !aligned(workspace, 16) || workspace_bytes < 0)
         return BMMC_ERR_INVALID_ARG;
     if (a->tokens == 0) return BMMC_OK;

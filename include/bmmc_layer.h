@@ -81,8 +81,9 @@ typedef struct bmmc_attention {
     int clear_rest;
 } bmmc_attention;
 
-/* Bytes of device workspace that the call needs, which depend on sizes alone
- * (-1 if an argument is out of range).  It needs no initial value, nothing is
+/* Bytes of device workspace that the call needs, which depend on sizes and on
+ * whether there are starts alone: other pointers are not looked at (-1 if a size
+ * is out of range).  It needs no initial value, nothing is
  * kept in it from one call to the next, and calls that run at the same time
  * need one each. */
 int64_t bmmc_cache_attention_workspace(const bmmc_attention *a);

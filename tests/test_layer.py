@@ -220,6 +220,20 @@ def test_attention_workspace(host):
     assert host.bmmc_cache_attention_workspace(_attention(tokens=1 << 20)) == 0
 
 
+def test_workspaces_are_known_before_there_are_arrays(host):
+    """A program may ask for the workspace's size before it has any array; with and without starts."""
+    nothing = dict(q=None, out=None, table=None, lengths=None, q_token=-1, out_head=-1)
+    for starts, batch in ((0, 3), (None, 10)):
+        need = host.bmmc_cache_attention_workspace(_attention(starts=None if starts is None else C + 0x2000, batch=batch))
+        assert need > 0
+        some = None if starts is None else 4
+        assert host.bmmc_cache_attention_workspace(_attention(**nothing, starts=some, batch=batch)) == need
+    for changes in ({"table": None}, {"table": C + 2}):
+        a = _attention(**changes)
+        assert host.bmmc_cache_attention(a, _cache(D), _cache(E), 1 << 40, 1 << 30, None) == BAD
+    assert host.bmmc_cache_attention(_attention(tokens=0, table=C + 2), _cache(D), _cache(E), None, 0, None) == BAD
+
+
 def _heads(at, token=6 * 64, heads=2, dim=64, out=None, **changes):
     h = dict(heads=heads, in_batch=0, in_token=token, in_head=dim, out_batch=0, out_token=token, out_head=dim)
     h.update(changes)
