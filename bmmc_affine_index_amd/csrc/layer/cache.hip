@@ -22,7 +22,7 @@ namespace bmmc {
 
 namespace {
 
-constexpr int kPer = 8;  // elements of a row in a lane
+constexpr int kPer = 8;  // elements of a vector; to quantize, a lane has two of its row
 
 // Where a row's lanes are: `lanes` a row, a power of two, and 64 / lanes rows a wave.
 struct RowCut {

@@ -1,6 +1,6 @@
 // layer.h -- what the host side (api.cpp) and the kernels of the layer's
 // operators share: the launchers, the kernels' arguments and the plan of the
-// attention, which both sides compute with the same functions.
+// attention, which the host side makes from the sizes.
 #pragma once
 
 #include "../../../include/bmmc_layer.h"
@@ -11,16 +11,17 @@ namespace bmmc {
 // ---- attention -------------------------------------------------------------
 
 // A sequence's new tokens, times the heads that share a key head, are the rows
-// of its products: row r is token r / group, head r % group.  A tile is kRows
+// of its products: row r is token r / group, head r % group.  A tile is `rows`
 // rows over the keys that any of them sees; a unit is as many keys as a
 // workgroup takes at once.
 //
-// Few rows leave few workgroups, so the units of all tiles, one after the other,
+// Few tiles leave few workgroups; then the units of all tiles, one after the other,
 // are cut into as many equal shares as run at the same time: a workgroup takes
 // one of them, be it a part of a tile or several tiles.  Where it ends inside a
 // tile, what it has of the tile goes to the workspace, and a second launch joins
 // the parts.  The lengths are on the device, and so are the shares: a long
-// sequence among short ones is spread over many.
+// sequence among short ones is spread over many.  Without shares a tile is one
+// workgroup's, however long its sequence is.
 struct AttendPlan {
     int32_t rows, unit;   // of a tile; keys of a step
     int32_t shares;       // of a key head; 0: each tile is one workgroup's

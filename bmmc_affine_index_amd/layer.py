@@ -23,8 +23,6 @@ import ctypes
 
 from .tokens import (_calls, _constant, _need, _run, bmmc_heads, bmmc_rotation, tokens_lib)
 
-LEAST_ATTENDED = 8
-
 LAYER_EXPORTED = ("bmmc_cache_attention_workspace", "bmmc_cache_attention", "bmmc_cache_quantize",
                   "bmmc_cache_read", "bmmc_expert_balance_workspace", "bmmc_expert_balance",
                   "bmmc_expert_balance_backward")
