@@ -86,22 +86,30 @@ int check_places(int64_t tokens, const int32_t *sequences, const void *positions
 
 // Numbers that a call reads besides rows: `rows` times `bytes` bytes, `stride` bytes apart.
 struct Numbers {
-    const void *at;
-    int64_t bytes, rows, stride;
+    const void *at = nullptr;
+    int64_t bytes = 0, rows = 0, stride = 0;
+    Extent all{0, 0};
+    Numbers() {}
+    Numbers(const void *p, int64_t n, int64_t rows_, int64_t stride_)
+        : at(p), bytes(p ? n : 0), rows(rows_), stride(stride_) {
+        if (bytes > 0) all = extent(p, 1, bytes, &rows, &stride, 1);
+    }
 };
 
-Numbers flat(const void *p, int64_t bytes) { return Numbers{p, p ? bytes : 0, 1, 0}; }
+Numbers flat(const void *p, int64_t bytes) { return Numbers(p, bytes, 1, 0); }
 
 Numbers table_of(const int32_t *table, int64_t batch, int64_t width, int64_t stride) {
-    return Numbers{table, 4 * width, batch, 4 * stride};
+    return Numbers(table, 4 * width, batch, 4 * stride);
 }
 
-// Whether a written array, of extent e, has a byte of what is read.
-bool overwrites(const void *p, const Extent &e, const Steps &steps, int element, const Numbers &r) {
-    if (r.bytes <= 0 || !meet(e, extent(r.at, 1, r.bytes, &r.rows, &r.stride, 1))) return false;
-    Steps in_bytes = steps;
+// Whether a written array, of extent e, has a byte of what is read.  Its steps are
+// looked at only where the two extents meet, as they seldom do.
+template <class F>
+bool overwrites(const void *p, const Extent &e, F steps, int element, const Numbers &r) {
+    if (!meet(e, r.all)) return false;
+    Steps in_bytes = steps();
     in_bytes.inner *= element;
-    for (int i = 0; i < steps.dims; ++i) in_bytes.strides[i] *= element;
+    for (int i = 0; i < in_bytes.dims; ++i) in_bytes.strides[i] *= element;
     return share(p, in_bytes, r.at, Steps(r.bytes, &r.rows, &r.stride, 1), 1);
 }
 
@@ -173,8 +181,8 @@ int bmmc_cache_attention(const bmmc_attention *a, const bmmc_scaled_cache *k_cac
         if (meet(out, e) || meet(work, e)) return BMMC_ERR_ALIAS;
     for (const Numbers &r : {table_of(a->table, a->batch, a->table_width, a->table_stride),
                              flat(a->lengths, 4 * a->batch), flat(a->starts, 4 * (a->batch + 1))})
-        if (overwrites(a->out, out, Steps(a->v_dim, sizes, os, 2), bytes, r) ||
-            overwrites(workspace, work, Steps(need, nullptr, nullptr, 0), 1, r))
+        if (overwrites(a->out, out, [&] { return Steps(a->v_dim, sizes, os, 2); }, bytes, r) ||
+            overwrites(workspace, work, [&] { return Steps(need, nullptr, nullptr, 0); }, 1, r))
             return BMMC_ERR_ALIAS;
     AttendArgs x{};
     x.a = *a;
@@ -260,15 +268,22 @@ int bmmc_cache_quantize(const bmmc_heads *q, const bmmc_heads *k, const bmmc_hea
         numbers[3] = flat(rotation->freqs, rotation->pairs * (rotation->freqs_are_64 ? 8 : 4));
         numbers[4] = flat(rotation->axis_of_pair, rotation->pairs * 4);
         if (rotation->positions)
-            numbers[5] = Numbers{rotation->positions, turn * tokens, rotation->axes,
-                                 turn * rotation->axis_stride};
+            numbers[5] = Numbers(rotation->positions, turn * tokens, rotation->axes,
+                                 turn * rotation->axis_stride);
     }
+    const auto data = [&](const bmmc_scaled_cache &c, int dim) {
+        return [&c, dim, pages, page_size, k] { return data_steps(c, pages, page_size, k->heads, dim); };
+    };
+    const auto scale = [&](const bmmc_scaled_cache &c) {
+        return [&c, pages, page_size, k] { return scale_steps(c, pages, page_size, k->heads); };
+    };
     for (const Numbers &r : numbers)
-        if (overwrites(k_cache->data, kc.data, data_steps(*k_cache, pages, page_size, k->heads, k_dim), 1, r) ||
-            overwrites(v_cache->data, vc.data, data_steps(*v_cache, pages, page_size, k->heads, v_dim), 1, r) ||
-            overwrites(k_cache->scale, kc.scale, scale_steps(*k_cache, pages, page_size, k->heads), 4, r) ||
-            overwrites(v_cache->scale, vc.scale, scale_steps(*v_cache, pages, page_size, k->heads), 4, r) ||
-            (q && overwrites(q->out, qe.out, steps_out(*q, 1, tokens, k_dim), element_bytes(type), r)))
+        if (overwrites(k_cache->data, kc.data, data(*k_cache, k_dim), 1, r) ||
+            overwrites(v_cache->data, vc.data, data(*v_cache, v_dim), 1, r) ||
+            overwrites(k_cache->scale, kc.scale, scale(*k_cache), 4, r) ||
+            overwrites(v_cache->scale, vc.scale, scale(*v_cache), 4, r) ||
+            (q && overwrites(q->out, qe.out, [&] { return steps_out(*q, 1, tokens, k_dim); },
+                             element_bytes(type), r)))
             return BMMC_ERR_ALIAS;
     QuantizeArgs a{};
     if (q) a.q = *q;
@@ -330,8 +345,8 @@ int bmmc_cache_read(const bmmc_heads *k, const bmmc_heads *v, const bmmc_scaled_
         if (meet(c, ke.out) || meet(c, ve.out)) return BMMC_ERR_ALIAS;
     for (const Numbers &r : {table_of(table, batch, table_width, table_stride), flat(sequences, 4 * tokens),
                              flat(positions, (position_type == BMMC_I64 ? 8 : 4) * tokens)})
-        if (overwrites(k->out, ke.out, steps_out(*k, 1, tokens, k_dim), element_bytes(type), r) ||
-            overwrites(v->out, ve.out, steps_out(*v, 1, tokens, v_dim), element_bytes(type), r))
+        if (overwrites(k->out, ke.out, [&] { return steps_out(*k, 1, tokens, k_dim); }, element_bytes(type), r) ||
+            overwrites(v->out, ve.out, [&] { return steps_out(*v, 1, tokens, v_dim); }, element_bytes(type), r))
             return BMMC_ERR_ALIAS;
     ReadArgs a{};
     a.k = *k;
