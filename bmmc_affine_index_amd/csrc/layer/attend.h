@@ -451,8 +451,9 @@ __device__ __forceinline__ void wait_for(f4 &x) { asm volatile("s_nop 15" : "+v"
 // So that no bits are lost for the exponent's, the weight goes into two products, as its
 // rounding and as the rounding of what that leaves out, which is 2^-16 of it at most
 // (float16: 2^-11).  e4m3's values are all values of both types.  One product and two:
-// 4096 tokens over 4 x 2048 places, 16 over 4 heads of 128, 154 us (bfloat16) and 181;
-// one token of 128 sequences of up to 4096, 24 over 4 heads of 96, 67.0 us and 67.7.
+// 4096 tokens of 4 sequences behind up to 2048 places, 16 over 4 heads of 128, 154 us
+// (bfloat16) and 181; one token of 128 sequences of up to 4096, 24 over 4 heads of 96,
+// 67.0 us and 67.7.
 template <typename T, bool ROWS> struct Weighed {
     typedef T type;
     static constexpr bool kTwo = false;
