@@ -156,8 +156,9 @@ int bmmc_cache_attention(const bmmc_attention *a, const bmmc_scaled_cache *k_cac
     int st = check_attention_sizes(*a);
     if (st != BMMC_OK) return st;
     const int64_t need = bmmc_cache_attention_workspace(a);
-    if (!table_ok(a->table, a->batch, a->table_width) || !stride_ok(a->q_token) || !stride_ok(a->q_head) || !stride_ok(a->out_token) ||
-        !stride_ok(a->out_head) || !aligned(workspace, 16) || workspace_bytes < 0)
+    if (!table_ok(a->table, a->batch, a->table_width) || !stride_ok(a->q_token) ||
+        !stride_ok(a->q_head) || !stride_ok(a->out_token) || !stride_ok(a->out_head) ||
+        !aligned(workspace, 16) || workspace_bytes < 0)
         return BMMC_ERR_INVALID_ARG;
     if (a->tokens == 0) return BMMC_OK;
     const int bytes = element_bytes(a->type);
@@ -261,8 +262,8 @@ int bmmc_cache_quantize(const bmmc_heads *q, const bmmc_heads *k, const bmmc_hea
             return BMMC_ERR_ALIAS;
     }
     const int64_t each = position_type == BMMC_I64 ? 8 : 4;
-    Numbers numbers[6] = {table_of(table, batch, table_width, table_stride), flat(sequences, 4 * tokens),
-                          flat(positions, each * tokens)};
+    Numbers numbers[6] = {table_of(table, batch, table_width, table_stride),
+                          flat(sequences, 4 * tokens), flat(positions, each * tokens)};
     if (rotation) {
         const int64_t turn = rotation->position_type == BMMC_I64 ? 8 : 4;
         numbers[3] = flat(rotation->freqs, rotation->pairs * (rotation->freqs_are_64 ? 8 : 4));
@@ -343,10 +344,12 @@ int bmmc_cache_read(const bmmc_heads *k, const bmmc_heads *v, const bmmc_scaled_
         return BMMC_ERR_ALIAS;
     for (const Extent &c : {kc.data, kc.scale, vc.data, vc.scale})
         if (meet(c, ke.out) || meet(c, ve.out)) return BMMC_ERR_ALIAS;
-    for (const Numbers &r : {table_of(table, batch, table_width, table_stride), flat(sequences, 4 * tokens),
-                             flat(positions, (position_type == BMMC_I64 ? 8 : 4) * tokens)})
-        if (overwrites(k->out, ke.out, [&] { return steps_out(*k, 1, tokens, k_dim); }, element_bytes(type), r) ||
-            overwrites(v->out, ve.out, [&] { return steps_out(*v, 1, tokens, v_dim); }, element_bytes(type), r))
+    const int bytes = element_bytes(type);
+    const int64_t each = position_type == BMMC_I64 ? 8 : 4;
+    for (const Numbers &r : {table_of(table, batch, table_width, table_stride),
+                             flat(sequences, 4 * tokens), flat(positions, each * tokens)})
+        if (overwrites(k->out, ke.out, [&] { return steps_out(*k, 1, tokens, k_dim); }, bytes, r) ||
+            overwrites(v->out, ve.out, [&] { return steps_out(*v, 1, tokens, v_dim); }, bytes, r))
             return BMMC_ERR_ALIAS;
     ReadArgs a{};
     a.k = *k;

@@ -103,7 +103,8 @@ def cache_attention(q, k_cache, v_cache, page_table, lengths, starts=None, k_sca
     `out` as it is.  Scores and sums are in 32 bits; weights, times v_scale
     where that is one for each row, are rounded to q's type before they meet the
     values, and so that 2^-16 of one is left out at most where q is float16 and
-    v_scale is one for each row.  There is no gradient."""
+    v_scale is one for each row.  Otherwise float16 loses bits of weights below
+    2^-21 of a row's largest, and those below 2^-32.  There is no gradient."""
     return _run(_calls().attention, (q, k_cache, v_cache, page_table, lengths, starts, k_scale,
                                      v_scale, scale, window, out), stream)[0]
 
